@@ -1,9 +1,10 @@
 """Build libfa_gb300.so in-tree with nvcc (sm_103a only).
 
-Three translation units: fa_api.cu (the C-ABI front end with every forward,
-split-KV merge and backward kernel instantiation), fa_probe.cu (the
-exp2-throughput probe) and fa_selftest.cu (the bounded-wait self-test),
-compiled in one nvcc call.
+Five translation units: fa_api.cu (the C-ABI front end with every dense
+forward, split-KV merge and backward kernel instantiation), fa_rope.cu (rotary
+positions and the paged cache's append), fa_paged.cu (attention over the paged
+cache), fa_probe.cu (the exp2-throughput probe) and fa_selftest.cu (the
+bounded-wait self-test), compiled in parallel by one nvcc call.
 """
 from __future__ import annotations
 
@@ -18,8 +19,10 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa_gb300.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_probe.cu", "fa_selftest.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_ptx.cuh", "fa_fwd_kernel.cuh", "fa_fwd_persist.cuh", "fa_bwd_kernel.cuh")] + [
+SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_rope.cu", "fa_paged.cu", "fa_probe.cu", "fa_selftest.cu")]
+DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_ptx.cuh", "fa_host.h", "fa_fwd_kernel.cuh", "fa_fwd_persist.cuh",
+                                                       "fa_bwd_kernel.cuh", "fa_rope_kernel.cuh",
+                                                       "fa_paged_kernel.cuh")] + [
     os.path.join(INCLUDE, "fa.h")]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -33,7 +36,7 @@ def nvcc() -> str:
 
 
 def command(out: str = LIB_PATH, verbose_ptxas: bool = False) -> list[str]:
-    cmd = [nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17", "--threads=0", "-shared", "-Xcompiler", "-fPIC",
            "-I", INCLUDE, "-I", CSRC, "-o", out, *SOURCES, "-lcudart"]
     if verbose_ptxas:
         cmd.insert(1, "-Xptxas=-v")

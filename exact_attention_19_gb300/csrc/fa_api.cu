@@ -13,17 +13,9 @@
 #include "fa_fwd_kernel.cuh"
 #include "fa_fwd_persist.cuh"
 #include "fa_bwd_kernel.cuh"
+#include "fa_host.h"
 
-namespace {
-
-constexpr int kVersion = 100;  // 0.1.0
-constexpr int kMaxDevices = 64;
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                                   CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                                   CUtensorMapFloatOOBfill);
-
+namespace fa_host {
 EncodeTiledFn encode_fn() {
   static std::once_flag once;
   static EncodeTiledFn fn = nullptr;
@@ -37,6 +29,26 @@ EncodeTiledFn encode_fn() {
   });
   return fn;
 }
+
+bool is_device_pointer(const void* p, int dev) {
+  cudaPointerAttributes a;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    cudaGetLastError();  // clear the sticky-free error state of this query
+    return false;
+  }
+  if (a.type == cudaMemoryTypeManaged) return true;
+  return a.type == cudaMemoryTypeDevice && a.device == dev;
+}
+}  // namespace fa_host
+
+namespace {
+
+using fa_host::EncodeTiledFn;
+using fa_host::encode_fn;
+using fa_host::is_device_pointer;
+using fa_host::kMaxDevices;
+
+constexpr int kVersion = 100;  // 0.1.0
 
 // Per-device one-time state: compute capability check and the kernels'
 // shared-memory opt-in.  0 = not yet, 1 = ready, -1 = unsupported device.
@@ -131,16 +143,6 @@ int prepare_device(int dev) {
     return FA_ERR_LAUNCH;
   g_dev_state[dev].store(1, std::memory_order_release);
   return FA_OK;
-}
-
-bool is_device_pointer(const void* p, int dev) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();  // clear the sticky-free error state of this query
-    return false;
-  }
-  if (a.type == cudaMemoryTypeManaged) return true;
-  return a.type == cudaMemoryTypeDevice && a.device == dev;
 }
 
 // 3-D tensor map over a [BH, N, D] bf16 tensor: dims (D, N, BH), box
@@ -358,6 +360,33 @@ int launch_single_pass(int B, int H, int Nq, int Nk, int d, int causal, const CU
 
 }  // namespace
 
+namespace fa_host {
+
+int current_device(int* dev, int* sms) {
+  if (cudaGetDevice(dev) != cudaSuccess) return FA_ERR_LAUNCH;
+  const int st = prepare_device(*dev);
+  if (st == FA_OK) *sms = g_dev_sms_or(*dev, 148);
+  return st;
+}
+
+unsigned int* status_word(int dev) {
+  static std::atomic<unsigned int*> ptrs[kMaxDevices];
+  if (dev < 0 || dev >= kMaxDevices) return nullptr;
+  unsigned int* ptr = ptrs[dev].load(std::memory_order_acquire);
+  if (!ptr) {  // threads that race here store the same address
+    void* v = nullptr;
+    if (cudaGetSymbolAddress(&v, fa::g_fa_status) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    ptr = static_cast<unsigned int*>(v);
+    ptrs[dev].store(ptr, std::memory_order_release);
+  }
+  return ptr;
+}
+
+}  // namespace fa_host
+
 extern "C" {
 
 int fa_version(void) { return kVersion; }
@@ -375,7 +404,9 @@ const char* fa_strerror(int status) {
     case FA_ERR_TIMEOUT: return "a kernel wait timed out";
     case FA_ERR_SCALE: return "scale must be finite and > 0";
     case FA_ERR_POINTER: return "a tensor pointer is not device memory of the current device";
-    case FA_ERR_WORKSPACE: return "split-KV workspace is missing or smaller than fa_splitkv_workspace_bytes()";
+    case FA_ERR_WORKSPACE: return "workspace is missing or smaller than its fa_*_workspace_bytes()";
+    case FA_ERR_PAGE: return "a page index or a sequence length lies outside the cache or its block table";
+    case FA_ERR_STRIDE: return "a stride is not a positive multiple of 8 elements, or too large";
     default: return "unknown status";
   }
 }
@@ -677,7 +708,8 @@ int fa_fwd_status(cudaStream_t stream, unsigned int* detail, int clear) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(fa::g_fa_status, &zero, sizeof(zero)) != cudaSuccess) return FA_ERR_LAUNCH;
   }
-  return word ? FA_ERR_TIMEOUT : FA_OK;
+  if (word & FA_STATUS_TIMEOUT) return FA_ERR_TIMEOUT;
+  return (word & FA_STATUS_PAGE) ? FA_ERR_PAGE : FA_OK;
 }
 
 }  // extern "C"

@@ -1,0 +1,734 @@
+// fa_paged_kernel.cuh -- attention of a few new tokens per sequence over a
+// paged K/V cache, with an optional prefix that every sequence shares.
+//
+// Rows.  Query head h = hk * G + g reads K/V head hk (G = H / Hk); the G * T
+// query rows of one (sequence, K/V head) are contiguous in [B, H, T, d] and
+// share every K/V byte.  Row r of them is token t = r % T.  With len the
+// sequence's own cached tokens and fresh its new ones, token t sits at own
+// position len - fresh + t and sees the own keys its window reaches, and every
+// prefix key at or before it.
+//
+// Schedule.  A work unit is one block of rows against one tile of keys.  All
+// units of a call form one line: first the prefix (its row blocks run over the
+// batch's rows of a K/V head, so its K/V is read once for the batch and not
+// once per sequence), then the sequences' own keys.  CTA c takes units
+// [c W / P, (c + 1) W / P): equal shares whatever the lengths, computed on the
+// device from the lengths there, so the host needs none of them and a captured
+// launch stays right as the sequences grow.  A CTA that holds all units of a
+// row block writes its output; else it writes its part (O normalised by its
+// own sum, and L, the base-2 log of that sum) and fa_paged_merge_kernel joins
+// the parts:  L = log2 sum 2^L_i,  O = sum 2^(L_i - L) O_i.
+#pragma once
+
+#include <cstdint>
+#include <type_traits>
+
+#include <cuda.h>
+
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+// status word bits of the paged kernels (fa.h)
+constexpr unsigned kPagedTimeout = 1u, kPagedPage = 2u;
+
+struct PagedParams {
+  const uint16_t* q;        // [B, H, T, D]
+  uint16_t* out;            // [B, H, T, D]
+  float* lse;               // [B, H, T]
+  const int* table;         // [B, max_pages]
+  const int* lens;          // [B]
+  const int* new_lens;      // [B] or nullptr
+  const int* prefix_pages;  // [ceil(prefix_len / page)]
+  int B, Hk, T, rows;       // rows = G * T of one (sequence, K/V head)
+  int n_pages, max_pages, page_shift;
+  int capacity;             // tokens a row of the table can hold (clipped to an int)
+  int prefix_len;           // 0: no prefix
+  int left, right;          // own window, -1 = open
+  float scale_log2;         // scale * log2(e)
+  long long* plan;          // [0] units, [1] CTAs with work, [2 + b] first own unit of sequence b, [2 + B] units
+  float* piece_o;           // [2 * grid, row block, D] parts of the row blocks a CTA shares with others
+  float* piece_l;           // [2 * grid, row block]
+  float* whole_o;           // [2, B * H * T, D] with a prefix: row blocks one CTA finished (0 prefix, 1 own)
+  float* whole_l;           // [2, B * H * T]
+  unsigned int* status;
+};
+
+// The own keys [lo, hi) of a sequence that any of its new tokens sees.
+struct SeqKeys {
+  int len, fresh, lo, hi;
+};
+__device__ __forceinline__ SeqKeys seq_keys(const PagedParams& p, int b) {
+  SeqKeys s;
+  s.len = max(0, min(__ldg(p.lens + b), p.capacity));
+  s.fresh = p.new_lens ? max(0, min(__ldg(p.new_lens + b), p.T)) : p.T;
+  s.hi = s.fresh > 0 ? s.len : 0;
+  s.lo = p.left < 0 ? 0 : static_cast<int>(max(0ll, static_cast<long long>(s.len) - s.fresh - p.left));
+  s.lo = min(s.lo, s.hi);
+  return s;
+}
+__device__ __forceinline__ int tiles_of(int lo, int hi, int tile) { return hi > lo ? (hi + tile - 1) / tile - lo / tile : 0; }
+
+// Own keys [lo, hi) that one row (token t of a sequence) sees.
+__device__ __forceinline__ void row_own_keys(const PagedParams& p, const SeqKeys& s, int t, int& lo, int& hi) {
+  const long long pos = static_cast<long long>(s.len) - s.fresh + t;
+  lo = p.left < 0 ? 0 : static_cast<int>(max(0ll, pos - p.left));
+  hi = p.right < 0 ? s.len : static_cast<int>(max(0ll, min(static_cast<long long>(s.len), pos + p.right + 1)));
+  if (t >= s.fresh || (p.prefix_len > 0 && pos < 0)) hi = 0;
+}
+// Prefix keys [0, hi) that one row sees: all of them, unless it holds no token.
+__device__ __forceinline__ int row_prefix_keys(const PagedParams& p, const SeqKeys& s, int t) {
+  return (t < s.fresh && s.len - s.fresh + t >= 0) ? p.prefix_len : 0;
+}
+
+// A row block against the tiles of its keys that this CTA holds.
+struct PagedWalk {
+  long long g, gend;  // first unit of the current segment part, end of the CTA's units
+  bool own;           // prefix or own keys
+  int b, hk, rb;      // sequence (own), K/V head, row block
+  int tile0, n;       // first key tile of the row block and their number
+  int j, jend;        // the part of them this CTA holds
+  int lo, hi;         // keys that any row of the segment may see
+};
+
+template <int RB, int TILE>
+struct PagedSchedule {
+  static __device__ __forceinline__ int own_blocks(const PagedParams& p) { return (p.rows + RB - 1) / RB; }
+  static __device__ __forceinline__ int prefix_blocks(const PagedParams& p) {
+    return static_cast<int>((static_cast<long long>(p.B) * p.rows + RB - 1) / RB);
+  }
+  static __device__ __forceinline__ int prefix_tiles(const PagedParams& p) { return (p.prefix_len + TILE - 1) / TILE; }
+  static __device__ __forceinline__ long long prefix_units(const PagedParams& p) {
+    return p.prefix_len > 0 ? static_cast<long long>(p.Hk) * prefix_blocks(p) * prefix_tiles(p) : 0ll;
+  }
+  static __device__ __forceinline__ long long cta_start(long long units, long long ctas, long long c) {
+    return c * units / ctas;
+  }
+  static __device__ __forceinline__ long long cta_of(long long units, long long ctas, long long x) {
+    return ((x + 1) * ctas - 1) / units;
+  }
+
+  static __device__ __forceinline__ void enter_seq(const PagedParams& p, PagedWalk& w) {
+    for (;; ++w.b) {  // w.g < w.gend, so a sequence with units follows
+      const SeqKeys s = seq_keys(p, w.b);
+      w.lo = s.lo;
+      w.hi = s.hi;
+      w.tile0 = s.lo / TILE;
+      w.n = tiles_of(s.lo, s.hi, TILE);
+      if (w.n > 0 || w.b + 1 >= p.B) return;
+    }
+  }
+  static __device__ __forceinline__ void part(PagedWalk& w) {
+    w.jend = static_cast<int>(min(static_cast<long long>(w.n), w.j + (w.gend - w.g)));
+  }
+  // first segment of the units [g, gend), g < gend; b, b_unit: the sequence that holds g and its first
+  // unit (own units only)
+  static __device__ __forceinline__ void begin(const PagedParams& p, PagedWalk& w, long long g, long long gend, int b,
+                                               long long b_unit) {
+    w.g = g;
+    w.gend = gend;
+    const long long pu = prefix_units(p);
+    w.own = g >= pu;
+    if (!w.own) {
+      w.n = prefix_tiles(p);
+      w.tile0 = 0;
+      w.lo = 0;
+      w.hi = p.prefix_len;
+      const long long i = g / w.n;
+      w.j = static_cast<int>(g - i * w.n);
+      w.hk = static_cast<int>(i / prefix_blocks(p));
+      w.rb = static_cast<int>(i % prefix_blocks(p));
+      w.b = 0;
+    } else {
+      w.b = b;
+      enter_seq(p, w);
+      const long long i = (g - b_unit) / w.n;
+      w.j = static_cast<int>((g - b_unit) - i * w.n);
+      w.hk = static_cast<int>(i / own_blocks(p));
+      w.rb = static_cast<int>(i % own_blocks(p));
+    }
+    part(w);
+  }
+  // j0: the part's first tile as begin or next left it
+  static __device__ __forceinline__ bool next(const PagedParams& p, PagedWalk& w, int j0) {
+    w.g += w.jend - j0;
+    if (w.g >= w.gend) return false;
+    w.j = 0;
+    const int blocks = w.own ? own_blocks(p) : prefix_blocks(p);
+    if (++w.rb == blocks) {
+      w.rb = 0;
+      if (++w.hk == p.Hk) {
+        w.hk = 0;
+        if (w.own) ++w.b;
+        w.own = true;
+        enter_seq(p, w);
+      }
+    }
+    part(w);
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// Row blocks of 16: warp-level MMAs.
+// ---------------------------------------------------------------------------
+// Decoding is bound by reading K and V once: 2 D multiply-adds per row and
+// 2-byte element leave a block of 16 rows far below the tensor rate, so the
+// warp-level m16n8k16 MMA (fed from registers) carries it, and each warp runs
+// alone: it streams its own 16 keys of every 64-key tile through its own ring
+// of TMA boxes (4 KB each at D = 128), holds its own running maximum, sum and O
+// accumulator, and meets the other warps only at the end of a row block.  No
+// barrier between warps stands in the loop, so their waits overlap.
+template <int D>
+struct PagedCfg {
+  static constexpr int kWarps = 4, kThreads = 128;
+  static constexpr int kRows = 16, kKeys = 16, kTile = kWarps * kKeys;
+  static constexpr int kBoxes = D / 64;
+  static constexpr uint32_t kBoxBytes = kKeys * 128u;
+  static constexpr uint32_t kItemBytes = kBoxes * kBoxBytes;  // 16 keys of K or of V
+  static constexpr int kRing = D == 128 ? 5 : 10;             // items per warp: 20 KB in flight
+  static constexpr uint32_t kRingBytes = kWarps * kRing * kItemBytes;
+  static constexpr int kMergeStride = D / 2 + 8;  // floats; + 8 spreads the rows over the banks
+  static constexpr uint32_t kMergeOff = kRingBytes;
+  static constexpr uint32_t kStatOff = kMergeOff + kWarps * 16 * kMergeStride * 4;
+  static constexpr uint32_t kBarOff = kStatOff + kWarps * 16 * 8;
+  static constexpr uint32_t kSmemBytes = kBarOff + kWarps * kRing * 8 + 128 + 1024;  // + alignment slack
+  static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
+};
+
+// TMA tile load from a 4-D map (d, token of the page, K/V head, page).  A page
+// index outside the map loads zeros.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
+// c[16 x 8] += a[16 x 16] b[16 x 8], bf16 in, fp32 accumulators
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Block-wide: units of the call, the CTA's share of them and the sequence its
+// first own unit lies in.  CTA 0 leaves the plan for the merge kernel.
+template <int RB, int TILE, int THREADS>
+__device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scratch /* shared, THREADS / 32 + 4 */,
+                                            long long min_units, PagedWalk& w) {
+  using S = PagedSchedule<RB, TILE>;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kWarps = THREADS / 32;
+  const long long per = static_cast<long long>(p.Hk) * S::own_blocks(p);
+  const long long pu = S::prefix_units(p);
+  long long total = pu, ctas = 1, g = 0, gend = 0;
+  // pass 0 sums, pass 1 finds the sequence that holds unit g
+  for (int pass = 0; pass < 2; ++pass) {
+    long long run = pu;
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+      const int b = b0 + static_cast<int>(threadIdx.x);
+      long long mine = 0;
+      if (b < p.B) {
+        const SeqKeys s = seq_keys(p, b);
+        mine = per * tiles_of(s.lo, s.hi, TILE);
+        if (pass == 0 && blockIdx.x == 0 && __ldg(p.lens + b) > p.capacity) atomicOr(p.status, kPagedPage);
+      }
+      long long incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      if (lane == 31) scratch[warp] = incl;
+      __syncthreads();
+      long long before = run, all = 0;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        if (i < warp) before += scratch[i];
+        all += scratch[i];
+      }
+      const long long first = before + incl - mine;
+      if (pass == 0 && blockIdx.x == 0 && b < p.B) p.plan[2 + b] = first;
+      if (pass == 1 && mine > 0 && first <= g && g < first + mine) {
+        scratch[kWarps] = b;
+        scratch[kWarps + 1] = first;
+      }
+      run += all;
+      __syncthreads();
+    }
+    if (pass == 0) {
+      total = run;
+      ctas = min(static_cast<long long>(gridDim.x), max(1ll, total / min_units));
+      if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.plan[0] = total;
+        p.plan[1] = ctas;
+        p.plan[2 + p.B] = total;
+      }
+      if (static_cast<long long>(blockIdx.x) >= ctas) return false;
+      g = S::cta_start(total, ctas, blockIdx.x);
+      gend = S::cta_start(total, ctas, blockIdx.x + 1);
+      if (g >= gend) return false;
+      if (g < pu) break;
+    }
+  }
+  S::begin(p, w, g, gend, g < pu ? 0 : static_cast<int>(scratch[kWarps]), g < pu ? 0 : scratch[kWarps + 1]);
+  return true;
+}
+
+constexpr long long kPagedMinUnits = 2;  // units a CTA takes at least
+
+template <int D>
+__global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
+    fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const PagedParams p) {
+  using C = PagedCfg<D>;
+  using S = PagedSchedule<C::kRows, C::kTile>;
+  constexpr int kNT = D / 8;   // 8-column tiles of O
+  constexpr int kKT = D / 16;  // 16-deep steps of Q K^T
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long scratch[C::kWarps + 4];
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  const uint32_t base = (raw_addr + 1023u) & ~1023u;
+  uint8_t* const sbase = smem_raw + (base - raw_addr);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(sbase + C::kBarOff + C::kWarps * C::kRing * 8);
+  const uint32_t bars = base + C::kBarOff + warp * C::kRing * 8;  // this warp's ring
+  const uint32_t ring = base + warp * C::kRing * C::kItemBytes;
+  float* const merge = reinterpret_cast<float*>(sbase + C::kMergeOff);
+  float* const stat = reinterpret_cast<float*>(sbase + C::kStatOff);  // [warp][16 rows][m, l]
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lane == 0) {
+    for (int i = 0; i < C::kRing; ++i) mbar_init(bars + 8 * i, 1);
+    if (warp == 0) *abort_flag = 0;
+    mbar_init_fence();
+  }
+  PagedWalk w;
+  if (!paged_share<C::kRows, C::kTile, C::kThreads>(p, scratch, kPagedMinUnits, w)) return;
+  const PagedWalk first = w;
+  __syncthreads();
+
+  // ---- this warp's stream of TMA items -----------------------------------
+  // The fetch side walks the same segments ahead of the products: K then V of
+  // every 16-key piece in range, one page index read ahead.
+  PagedWalk f = w;
+  int f_j0 = w.j;
+  int f_k0 = 0, f_hk = 0, f_page = 0, n_k0 = 0, n_hk = 0, n_page = 0;
+  bool f_more = true, n_more = true, f_is_v = false;
+  int f_slot = 0;  // ring slot of the next item
+  auto seek = [&]() {  // n_*: the next 16-key piece of this warp, n_more false when none is left
+    for (;;) {
+      while (f.j < f.jend) {
+        const int k0 = (f.tile0 + f.j) * C::kTile + warp * C::kKeys;
+        if (k0 < f.hi && k0 + C::kKeys > f.lo) {
+          const int pi = k0 >> p.page_shift;
+          const int* src = f.own ? p.table + static_cast<long long>(f.b) * p.max_pages + pi : p.prefix_pages + pi;
+          n_page = __ldg(src);
+          n_k0 = k0;
+          n_hk = f.hk;
+          ++f.j;
+          return;
+        }
+        ++f.j;
+      }
+      if (!S::next(p, f, f_j0)) {
+        n_more = false;
+        return;
+      }
+      f_j0 = 0;
+    }
+  };
+  auto take = [&]() {  // the piece sought becomes the one being fetched; seek the one after it
+    f_more = n_more;
+    f_k0 = n_k0;
+    f_hk = n_hk;
+    f_page = n_page;
+    if (n_more) seek();
+  };
+  int issued = 0, consumed = 0;
+  auto issue = [&]() {  // one item into f_slot, which is free
+    if (!f_more) return;
+    if (lane == 0) {
+      const uint32_t bar = bars + 8 * f_slot, dst = ring + f_slot * C::kItemBytes;
+      if (!f_is_v && static_cast<unsigned>(f_page) >= static_cast<unsigned>(p.n_pages)) atomicOr(p.status, kPagedPage);
+      mbar_arrive_expect_tx(bar, C::kItemBytes);
+      const int slot = f_k0 & ((1 << p.page_shift) - 1);
+#pragma unroll
+      for (int x = 0; x < C::kBoxes; ++x)
+        tma_load_4d(dst + x * C::kBoxBytes, f_is_v ? &tmV : &tmK, bar, x * 64, slot, f_hk, f_page);
+    }
+    ++issued;
+    f_slot = f_slot + 1 == C::kRing ? 0 : f_slot + 1;
+    if (f_is_v) take();
+    f_is_v = !f_is_v;
+  };
+  seek();
+  take();
+  for (int i = 0; i < C::kRing; ++i) issue();
+
+  int c_slot = 0;
+  uint32_t c_phase = 0;
+  bool ok = true;
+  auto wait_item = [&]() -> uint32_t {  // address of the next item once it has landed
+    if (ok) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bars + 8 * c_slot, c_phase, abort_flag));
+      if (!ok) {
+        *abort_flag = 1;
+        if (lane == 0) atomicOr(p.status, kPagedTimeout | (1u << 8));
+      }
+    }
+    return ring + c_slot * C::kItemBytes;
+  };
+  auto free_item = [&]() {
+    if (ok) {
+      ++consumed;
+      __syncwarp();
+      issue();
+    }
+    if (++c_slot == C::kRing) {
+      c_slot = 0;
+      c_phase ^= 1u;
+    }
+  };
+
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  const int g8 = lane >> 2, q4 = lane & 3;  // this thread's rows g8, g8 + 8 and columns 2 q4, 2 q4 + 1
+  bool more = true;
+  int j0 = w.j;
+  while (more) {
+    // ---- the segment's rows ------------------------------------------------
+    const bool own = w.own;
+    int lo[2], hi[2];
+    uint32_t qf[kKT][4];
+    long long out_row[2];  // row in [B * H * T], -1: none
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = w.rb * C::kRows + g8 + 8 * i;
+      int b = w.b, rr = r;
+      bool there = r < p.rows;
+      if (!own) {
+        b = r / p.rows;
+        rr = r - b * p.rows;
+        there = b < p.B;
+      }
+      lo[i] = 0;
+      hi[i] = 0x7fffffff;  // a row of the block that does not exist needs no mask: nothing of it is stored
+      out_row[i] = -1;
+      const uint32_t* src = nullptr;
+      if (there) {
+        const SeqKeys s = seq_keys(p, b);
+        if (own) row_own_keys(p, s, rr % p.T, lo[i], hi[i]);
+        else hi[i] = row_prefix_keys(p, s, rr % p.T);
+        out_row[i] = (static_cast<long long>(b) * p.Hk + w.hk) * p.rows + rr;
+        src = reinterpret_cast<const uint32_t*>(p.q + out_row[i] * D);
+      }
+#pragma unroll
+      for (int kk = 0; kk < kKT; ++kk) {
+        qf[kk][i] = there ? __ldg(src + kk * 8 + q4) : 0u;
+        qf[kk][2 + i] = there ? __ldg(src + kk * 8 + 4 + q4) : 0u;
+      }
+    }
+    float o[kNT][4];
+#pragma unroll
+    for (int i = 0; i < kNT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float m[2] = {NEG_INF, NEG_INF}, l[2] = {0.f, 0.f};  // base-2 scaled units; l: this thread's share
+
+    for (int j = w.j; j < w.jend; ++j) {
+      const int k0 = (w.tile0 + j) * C::kTile + warp * C::kKeys;
+      if (!(k0 < w.hi && k0 + C::kKeys > w.lo)) continue;
+      // S = Q K^T over 16 keys
+      const uint32_t kt = wait_item();
+      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      const int mi = lane >> 3, r8 = lane & 7;
+      if (ok) {
+        const int row = (mi >> 1) * 8 + r8;  // key
+#pragma unroll
+        for (int kk = 0; kk < kKT; ++kk) {
+          uint32_t b0, b1, b2, b3;
+          const uint32_t chunk = static_cast<uint32_t>((kk & 3) * 2 + (mi & 1));
+          ldmatrix4(kt + (kk >> 2) * C::kBoxBytes + row * 128 + ((chunk ^ static_cast<uint32_t>(row & 7)) << 4), b0, b1,
+                    b2, b3);
+          mma16816(s[0], qf[kk], b0, b1);
+          mma16816(s[1], qf[kk], b2, b3);
+        }
+      }
+      free_item();
+      // masks: rows' own bounds
+      const bool cut = k0 < max(lo[0], lo[1]) || k0 + C::kKeys > min(hi[0], hi[1]);
+      if (__any_sync(0xffffffffu, cut)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = k0 + i * 8 + q4 * 2 + (e & 1);
+            if (key < lo[e >> 1] || key >= hi[e >> 1]) s[i][e] = NEG_INF;
+          }
+      }
+      uint32_t pf[4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float m_new = fmaxf(m[i], mx * p.scale_log2);
+        // the running maximum is exact here (no threshold), so the largest
+        // probability of a row is 1 and its bf16 rounding is exact
+        if (__any_sync(0xffffffffu, m_new > m[i])) {
+          const float alpha = m[i] == NEG_INF ? 0.f : ex2(m[i] - m_new);
+          m[i] = m_new;
+          l[i] *= alpha;
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) {
+            o[n][2 * i] *= alpha;
+            o[n][2 * i + 1] *= alpha;
+          }
+        }
+        const float ref = m[i] == NEG_INF ? 0.f : -m[i];
+        const float e0 = ex2(fmaf(s[0][2 * i], p.scale_log2, ref)), e1 = ex2(fmaf(s[0][2 * i + 1], p.scale_log2, ref));
+        const float e2 = ex2(fmaf(s[1][2 * i], p.scale_log2, ref)), e3 = ex2(fmaf(s[1][2 * i + 1], p.scale_log2, ref));
+        l[i] += (e0 + e1) + (e2 + e3);
+        pf[i] = pack_bf16(e0, e1);  // P in bf16 for the product, as in fa_fwd
+        pf[2 + i] = pack_bf16(e2, e3);
+      }
+      // O += P V; keys outside the segment's range may hold anything (the end
+      // of a page, a page given back): their V counts as zero, as 0 * NaN would not
+      const uint32_t vt = wait_item();
+      if (ok) {
+        const int row = (mi & 1) * 8 + r8;  // key
+        const bool edge = k0 < w.lo || k0 + C::kKeys > w.hi;
+        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int key = k0 + i * 8 + q4 * 2;
+            keep[i] = ((key >= w.lo && key < w.hi) ? 0xffffu : 0u) |
+                      ((key + 1 >= w.lo && key + 1 < w.hi) ? 0xffff0000u : 0u);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kNT; n += 2) {
+          uint32_t b0, b1, b2, b3;
+          const uint32_t chunk = static_cast<uint32_t>((n & 7) + (mi >> 1));
+          ldmatrix4_t(vt + (n >> 3) * C::kBoxBytes + row * 128 + ((chunk ^ static_cast<uint32_t>(row & 7)) << 4), b0,
+                      b1, b2, b3);
+          mma16816(o[n], pf, b0 & keep[0], b1 & keep[1]);
+          mma16816(o[n + 1], pf, b2 & keep[0], b3 & keep[1]);
+        }
+      }
+      free_item();
+    }
+
+    // ---- join the four warps: each ends with D / 4 columns of all rows ----
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+    }
+    float acc[kNT / 2][4];
+    auto exchange = [&](const int other, const bool upper, auto& from, auto& to, auto half) {
+      // this warp keeps the upper (or lower) half of its columns and gets the
+      // other warp's values of the same columns
+      constexpr int kHalf = decltype(half)::value;
+      float* const mine = merge + warp * 16 * C::kMergeStride;
+      __syncthreads();  // the buffer is free
+#pragma unroll
+      for (int n = 0; n < kHalf; ++n) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float x = upper ? from[n][2 * i] : from[kHalf + n][2 * i];
+          const float y = upper ? from[n][2 * i + 1] : from[kHalf + n][2 * i + 1];
+          *reinterpret_cast<float2*>(mine + (g8 + 8 * i) * C::kMergeStride + n * 8 + 2 * q4) = make_float2(x, y);
+        }
+      }
+      if (q4 == 0) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<float2*>(stat + (warp * 16 + g8 + 8 * i) * 2) = make_float2(m[i], l[i]);
+      }
+      __syncthreads();
+      const float* const theirs = merge + other * 16 * C::kMergeStride;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float2 ml = *reinterpret_cast<const float2*>(stat + (other * 16 + g8 + 8 * i) * 2);
+        const float m_new = fmaxf(m[i], ml.x);
+        const float a = m[i] == NEG_INF ? 0.f : ex2(m[i] - m_new);
+        const float c = ml.x == NEG_INF ? 0.f : ex2(ml.x - m_new);
+        m[i] = m_new;
+        l[i] = a * l[i] + c * ml.y;
+#pragma unroll
+        for (int n = 0; n < kHalf; ++n) {
+          const float2 t =
+              *reinterpret_cast<const float2*>(theirs + (g8 + 8 * i) * C::kMergeStride + n * 8 + 2 * q4);
+          const float x = upper ? from[kHalf + n][2 * i] : from[n][2 * i];
+          const float y = upper ? from[kHalf + n][2 * i + 1] : from[n][2 * i + 1];
+          to[n][2 * i] = a * x + c * t.x;
+          to[n][2 * i + 1] = a * y + c * t.y;
+        }
+      }
+    };
+    exchange(warp ^ 1, (warp & 1) != 0, o, acc, std::integral_constant<int, kNT / 2>{});
+    float fin[kNT / 4][4];
+    exchange(warp ^ 2, (warp & 2) != 0, acc, fin, std::integral_constant<int, kNT / 4>{});
+    const int col = (warp & 1) * (D / 2) + (warp >> 1) * (D / 4) + 2 * q4;
+
+    // ---- write the row block, or this CTA's part of it ---------------------
+    const bool whole = w.jend - w.j == w.n;
+    const long long slot = w.g == first.g ? 2ll * blockIdx.x : 2ll * blockIdx.x + 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (out_row[i] < 0) continue;
+      const float inv = l[i] > 0.f ? 1.0f / l[i] : 0.f;
+      const float lb = l[i] > 0.f ? m[i] + __log2f(l[i]) : NEG_INF;
+      if (whole && p.prefix_len == 0) {
+        uint16_t* const dst = p.out + out_row[i] * D + col;
+#pragma unroll
+        for (int n = 0; n < kNT / 4; ++n)
+          *reinterpret_cast<uint32_t*>(dst + n * 8) = pack_bf16(fin[n][2 * i] * inv, fin[n][2 * i + 1] * inv);
+        if (col == 0) p.lse[out_row[i]] = lb * 0.69314718055994530942f;
+      } else {
+        const long long prow = whole ? (own ? static_cast<long long>(p.B) * p.Hk * p.rows : 0ll) + out_row[i]
+                                     : slot * C::kRows + g8 + 8 * i;
+        float* const dst = (whole ? p.whole_o : p.piece_o) + prow * D + col;
+#pragma unroll
+        for (int n = 0; n < kNT / 4; ++n)
+          *reinterpret_cast<float2*>(dst + n * 8) = make_float2(fin[n][2 * i] * inv, fin[n][2 * i + 1] * inv);
+        if (col == 0) (whole ? p.whole_l : p.piece_l)[prow] = lb;
+      }
+    }
+    more = S::next(p, w, j0);
+    j0 = 0;
+  }
+  if (!ok) {  // let every copy in flight land before the CTA's shared memory goes
+    for (int i = consumed; i < issued; ++i)
+      mbar_wait(bars + 8 * (i % C::kRing), static_cast<uint32_t>(i / C::kRing) & 1u, nullptr);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Joins the parts of every row that more than one CTA (or the prefix and the
+// own keys) contributed to, and writes the rows that saw no key.  One CTA of
+// four warps per row: the warps take the parts in turn, each lane D / 32
+// columns, and meet in shared memory.
+// ---------------------------------------------------------------------------
+template <int D, int RB, int TILE>
+__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p) {
+  using S = PagedSchedule<RB, TILE>;
+  constexpr int kPer = D / 32;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long row = blockIdx.x;
+  const long long bh = row / p.rows;
+  const int rr = static_cast<int>(row - bh * p.rows), hk = static_cast<int>(bh % p.Hk), b = static_cast<int>(bh / p.Hk);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  const long long units = p.plan[0], ctas = p.plan[1];
+  const long long all_rows = static_cast<long long>(p.B) * p.Hk * p.rows;
+
+  // CTAs [c0, c1] that hold the row's own keys, [d0, d1] its prefix keys (empty: c0 > c1)
+  const long long u0 = p.plan[2 + b];
+  const int blocks = S::own_blocks(p);
+  const long long n = (p.plan[3 + b] - u0) / (static_cast<long long>(p.Hk) * blocks);
+  const long long x0 = u0 + (static_cast<long long>(hk) * blocks + rr / RB) * n;
+  long long c0 = 1, c1 = 0, d0 = 1, d1 = 0, y0 = 0;
+  if (n > 0) {
+    c0 = S::cta_of(units, ctas, x0);
+    c1 = S::cta_of(units, ctas, x0 + n - 1);
+  }
+  const long long pr = static_cast<long long>(b) * p.rows + rr;  // row among the K/V head's prefix rows
+  if (p.prefix_len > 0) {
+    const int nt = S::prefix_tiles(p);
+    y0 = (static_cast<long long>(hk) * S::prefix_blocks(p) + pr / RB) * nt;
+    d0 = S::cta_of(units, ctas, y0);
+    d1 = S::cta_of(units, ctas, y0 + nt - 1);
+  } else if (n > 0 && c0 == c1) {
+    return;  // written by the one CTA that held it
+  }
+  const int n_own = static_cast<int>(c1 - c0 + 1), n_all = n_own + static_cast<int>(d1 - d0 + 1);
+  // part i of the row: O and L
+  auto part = [&](int i, const float*& po, const float*& pl) {
+    const bool own = i < n_own;
+    const long long a = own ? c0 : d0, z = own ? c1 : d1, start = own ? x0 : y0;
+    if (a == z) {
+      const long long at = (own ? all_rows : 0ll) + row;
+      po = p.whole_o + at * D;
+      pl = p.whole_l + at;
+      return;
+    }
+    const long long c = a + (own ? i : i - n_own);
+    // a CTA's first segment is its part 0; the row block is that one unless it starts inside the CTA
+    const long long slot = 2 * c + (S::cta_start(units, ctas, c) >= start ? 0 : 1);
+    const long long at = slot * RB + (own ? rr % RB : static_cast<int>(pr % RB));
+    po = p.piece_o + at * D;
+    pl = p.piece_l + at;
+  };
+  float mx = NEG_INF, sum = 0.f, acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  for (int i = warp; i < n_all; i += 4) {
+    const float *po, *pl;
+    part(i, po, pl);
+    const float L = *pl;
+    float v[kPer];
+    if constexpr (kPer == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(po + lane * 4);
+      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+    } else {
+      const float2 t = *reinterpret_cast<const float2*>(po + lane * 2);
+      v[0] = t.x; v[1] = t.y;
+    }
+    if (L == NEG_INF) continue;
+    const float m_new = fmaxf(mx, L);
+    const float a = mx == NEG_INF ? 0.f : ex2(mx - m_new), c = ex2(L - m_new);
+    mx = m_new;
+    sum = a * sum + c;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = a * acc[e] + c * v[e];
+  }
+  __shared__ float sh[4][D + 2];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) sh[warp][lane * kPer + e] = acc[e];
+  if (lane == 0) {
+    sh[warp][D] = mx;
+    sh[warp][D + 1] = sum;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  float top = NEG_INF, tot = 0.f, fin[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) fin[e] = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = fmaxf(top, sh[i][D]);
+  if (top != NEG_INF) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float c = sh[i][D] == NEG_INF ? 0.f : ex2(sh[i][D] - top);
+      tot += c * sh[i][D + 1];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) fin[e] += c * sh[i][lane * kPer + e];
+    }
+  }
+  const float inv = tot > 0.f ? 1.0f / tot : 0.f;
+  uint16_t* const dst = p.out + row * D + lane * kPer;
+  if constexpr (kPer == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(fin[0] * inv, fin[1] * inv), pack_bf16(fin[2] * inv, fin[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(fin[0] * inv, fin[1] * inv);
+  if (lane == 0) p.lse[row] = tot > 0.f ? (top + __log2f(tot)) * 0.69314718055994530942f : NEG_INF;
+}
+
+}  // namespace fa

@@ -1,0 +1,203 @@
+// fa_rope_kernel.cuh -- rotary positions over [B, H, N, d] tensors, and the
+// same rotation on the way into a paged K/V cache.
+//
+// Pair i of a head's rotated part at position p turns by the angle p * w_i:
+//   y0 = mag (x0 cos - x1 sin),  y1 = mag (x1 cos + x0 sin)
+// with (x0, x1) = (x[i], x[i + rot/2]) (half layout) or (x[2i], x[2i + 1])
+// (interleaved).  The backward is the transpose: sin negated, same mag.
+//
+// The angle: w_i comes in 64 bits.  Each thread turns it once into a fixed-
+// point number of turns per position modulo 1 (64 fraction bits: the double's
+// 53-bit significand times 2^66 / 2 pi, shifted by its exponent), so that
+// p * w_i modulo one turn is ONE wrapping 64-bit integer multiplication, exact
+// for every position: an fp32 product loses the angle from about p = 10^5 on,
+// and fp64 arithmetic runs at a small fraction of the fp32 rate here.
+//
+// Bound: memory, 4 bytes per element (bf16 read + write).  One thread owns 16
+// elements (two 16-byte chunks, 8 pairs) of one token and walks over heads with
+// its 8 cosines and sines in registers, so the angles are computed once per
+// token and chunk, not per head.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+namespace fa {
+
+constexpr unsigned kStatusPage = 2u;  // FA_STATUS_PAGE
+
+// Strides in elements of a [B, heads, N, d] view whose d is contiguous.
+struct RopeView {
+  long long b, h, n;
+};
+
+struct RopeParams {
+  const uint16_t* src[3];  // q, k, v (v: append only, copied)
+  uint16_t* dst[3];        // q, k outputs; append: q output, K cache, V cache
+  RopeView src_s[3];
+  RopeView dst_s[3];       // append: the caches' page, head and token strides
+  int heads[3];            // heads of each tensor (0: absent)
+  const double* inv_freq;  // [rot / 2], radians per position
+  const int* positions;    // [B or 1, N] or nullptr (position = offset + token)
+  long long pos_stride;    // N, or 0 for one row shared by the batch
+  long long offset;
+  long long tokens;        // B * N
+  int N;
+  int rot;
+  int heads_per_cta;       // heads (counted over all tensors) one CTA walks over
+  float mag, sin_sign;
+  // append only
+  const int* block_table;  // [B, max_pages]
+  const int* seq_lens;     // [B], with the new tokens
+  const int* new_lens;     // [B] or nullptr (N each)
+  int n_pages, max_pages, page_shift;
+  unsigned int* status;
+};
+
+// radians per position -> turns per position modulo 1, 64 fraction bits
+__device__ __forceinline__ unsigned long long turns_per_position(double w) {
+  constexpr unsigned long long kInv2Pi66 = 0xA2F9836E4E44152Aull;  // 2^66 / (2 pi)
+  const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(w));
+  const int expo = static_cast<int>((bits >> 52) & 0x7ffu);
+  const unsigned long long frac = bits & 0xfffffffffffffull;
+  if (expo == 0 || expo == 0x7ff) return 0ull;  // zero, subnormal (below 2^-64 turns) or not finite
+  const unsigned long long m = frac | (1ull << 52);
+  // |w| = m 2^(expo - 1075); turns 2^64 = (m * kInv2Pi66) >> (1077 - expo)
+  const unsigned long long lo = m * kInv2Pi66, hi = __umul64hi(m, kInv2Pi66);
+  const int s = 1077 - expo;
+  unsigned long long f;
+  if (s >= 128) f = 0ull;
+  else if (s >= 64) f = hi >> (s - 64);
+  else if (s > 0) f = (hi << (64 - s)) | (lo >> s);
+  else f = s > -64 ? lo << (-s) : 0ull;
+  return (bits >> 63) ? 0ull - f : f;
+}
+
+// 16-byte load, streamed: every element is read once
+__device__ __forceinline__ uint4 ld_stream16(const uint16_t* p) {
+  return __ldcs(reinterpret_cast<const uint4*>(p));
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+// round to nearest even; `lo` in bits 0-15
+__device__ __forceinline__ uint32_t rope_pack(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// The 16 elements (a: first chunk, b: second) of one head, rotated.
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotate16(uint4& a, uint4& b, const float (&c)[8], const float (&s)[8]) {
+  uint32_t* const pa = &a.x;
+  uint32_t* const pb = &b.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (INTERLEAVED) {
+      const float a0 = bf16_lo(pa[i]), a1 = bf16_hi(pa[i]), b0 = bf16_lo(pb[i]), b1 = bf16_hi(pb[i]);
+      pa[i] = rope_pack(fmaf(a0, c[i], -(a1 * s[i])), fmaf(a1, c[i], a0 * s[i]));
+      pb[i] = rope_pack(fmaf(b0, c[4 + i], -(b1 * s[4 + i])), fmaf(b1, c[4 + i], b0 * s[4 + i]));
+    } else {
+      const float x0 = bf16_lo(pa[i]), x1 = bf16_hi(pa[i]), y0 = bf16_lo(pb[i]), y1 = bf16_hi(pb[i]);
+      pa[i] = rope_pack(fmaf(x0, c[2 * i], -(y0 * s[2 * i])), fmaf(x1, c[2 * i + 1], -(y1 * s[2 * i + 1])));
+      pb[i] = rope_pack(fmaf(y0, c[2 * i], x0 * s[2 * i]), fmaf(y1, c[2 * i + 1], x1 * s[2 * i + 1]));
+    }
+  }
+}
+
+constexpr int kRopeThreads = 256;
+
+// grid: x = tiles of kRopeThreads / (D / 16) tokens, y = groups of heads.
+// PAGED: k and v go to the cache slots of their sequence's pages, q to dst[0];
+// a token past its sequence's new tokens, or whose slot lies outside the
+// cache, is not written.
+template <int D, bool INTERLEAVED, bool PAGED>
+__global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
+  constexpr int kUnits = D / 16;  // threads per token
+  const long long tok = static_cast<long long>(blockIdx.x) * (kRopeThreads / kUnits) + threadIdx.x / kUnits;
+  const int u = threadIdx.x % kUnits;
+  if (tok >= p.tokens) return;
+  const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok - static_cast<long long>(b) * p.N);
+
+  // head range of this CTA over q, then k, then v
+  const int h_lo = blockIdx.y * p.heads_per_cta, h_hi = h_lo + p.heads_per_cta;
+
+  long long pos;
+  long long page = 0, slot = 0;
+  bool cached = true;  // the token has a slot in the cache
+  if constexpr (PAGED) {
+    const int fresh = p.new_lens ? min(p.new_lens[b], p.N) : p.N;
+    if (n >= fresh) return;
+    const long long own = static_cast<long long>(p.seq_lens[b]) - fresh + n;
+    if (own < 0) return;  // no token: a padded entry of the batch
+    pos = p.offset + own;
+    if (h_hi > p.heads[0]) {
+      const long long pi = own >> p.page_shift;
+      cached = pi < p.max_pages;
+      if (cached) {
+        page = p.block_table[static_cast<long long>(b) * p.max_pages + pi];
+        cached = page >= 0 && page < p.n_pages;
+      }
+      if (!cached && u == 0) atomicOr(p.status, kStatusPage);
+      slot = own & ((1ll << p.page_shift) - 1);
+    }
+  } else {
+    pos = p.offset + (p.positions ? p.positions[b * p.pos_stride + n] : n);
+  }
+
+  // chunks of this thread: 8 rotation pairs, or 16 elements that pass through
+  const bool turns = u < p.rot / 16;
+  const int c0 = (turns && !INTERLEAVED) ? 8 * u : 16 * u;
+  const int c1 = (turns && !INTERLEAVED) ? p.rot / 2 + 8 * u : 16 * u + 8;
+  float c[8], s[8];
+  if (turns && h_lo < p.heads[0] + p.heads[1]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const unsigned long long phase =
+          static_cast<unsigned long long>(pos) * turns_per_position(__ldg(p.inv_freq + 8 * u + i));
+      // the upper 32 bits as a signed fraction of a turn, in [-1/2, 1/2); angle / pi = 2 turns
+      const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f;
+      float sn, cs;
+      sincospif(half_turns, &sn, &cs);
+      c[i] = cs * p.mag;
+      s[i] = sn * (p.mag * p.sin_sign);
+    }
+  }
+
+  int first = 0;  // heads before this tensor
+#pragma unroll
+  for (int t = 0; t < (PAGED ? 3 : 2); ++t) {
+    const int lo = max(h_lo - first, 0), hi = min(h_hi - first, p.heads[t]);
+    first += p.heads[t];
+    if (lo >= hi) continue;
+    const uint16_t* src = p.src[t] + b * p.src_s[t].b + n * p.src_s[t].n;
+    uint16_t* dst;
+    if (PAGED && t > 0) {
+      if (!cached) continue;
+      dst = p.dst[t] + page * p.dst_s[t].b + slot * p.dst_s[t].n;
+    } else {
+      dst = p.dst[t] + b * p.dst_s[t].b + n * p.dst_s[t].n;
+    }
+    constexpr int kU = 4;  // heads in flight: 8 loads of 16 bytes per thread
+    for (int h = lo; h < hi; h += kU) {
+      uint4 a[kU], e[kU];
+#pragma unroll
+      for (int i = 0; i < kU; ++i)
+        if (h + i < hi) {
+          a[i] = ld_stream16(src + (h + i) * p.src_s[t].h + c0);
+          e[i] = ld_stream16(src + (h + i) * p.src_s[t].h + c1);
+        }
+#pragma unroll
+      for (int i = 0; i < kU; ++i)
+        if (h + i < hi) {
+          if (t < 2 && turns) rotate16<INTERLEAVED>(a[i], e[i], c, s);
+          *reinterpret_cast<uint4*>(dst + (h + i) * p.dst_s[t].h + c0) = a[i];
+          *reinterpret_cast<uint4*>(dst + (h + i) * p.dst_s[t].h + c1) = e[i];
+        }
+    }
+  }
+}
+
+}  // namespace fa

@@ -47,7 +47,10 @@ typedef enum {
   FA_ERR_TIMEOUT = 8,       /* a kernel wait gave up (reported by fa_fwd_status)           */
   FA_ERR_SCALE = 9,         /* scale is not a finite positive number                       */
   FA_ERR_POINTER = 10,      /* a tensor pointer is not device memory of the current device */
-  FA_ERR_WORKSPACE = 11     /* split-KV workspace missing or smaller than required         */
+  FA_ERR_WORKSPACE = 11,    /* split-KV workspace missing or smaller than required         */
+  FA_ERR_PAGE = 12,         /* a page index or sequence length outside the cache (reported by
+                               fa_fwd_status: the values are known on the device alone)    */
+  FA_ERR_STRIDE = 13        /* a stride is not a positive multiple of 8 elements           */
 } fa_status;
 
 /*
@@ -185,6 +188,136 @@ int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, co
 /* Workspace bytes fa_bwd and fa_bwd_window need (0 for invalid sizes). */
 size_t fa_bwd_workspace_bytes(int B, int H, int Nq);
 
+/*
+ * fa_rope -- rotary positions of queries and keys, and their backward.
+ *
+ * The pair (x0, x1) number i of a head's first `rot` elements, at position p,
+ * becomes
+ *     mag * (x0 cos a - x1 sin a,  x1 cos a + x0 sin a),   a = p * inv_freq[i],
+ * with x0 = x[i], x1 = x[i + rot / 2] (interleaved = 0) or x0 = x[2i],
+ * x1 = x[2i + 1] (interleaved = 1); elements from rot on are copied unscaled.
+ * backward = 1 applies the transpose (the gradient of the above: sin negated,
+ * the same mag).
+ *
+ * q, q_out    bf16 [B, H, N, d];  k, k_out bf16 [B, Hk, N, d], Hk = 0: no k.
+ *             An output may be its own input (same pointer, same strides);
+ *             otherwise it must not overlap an input.
+ * inv_freq    fp64 [rot / 2], radians per position (any scaling of long
+ *             contexts is in these values and in mag).  The angle is exact for
+ *             every position: positions multiply a 64-bit fraction of a turn.
+ * positions   int32 [B, N] (position_stride, >= N, int32s from one sequence to the
+ *             next) or one row for all (position_stride 0); NULL: position
+ *             = offset + row.  offset is added in both cases.
+ * strides     host array of 12: batch, head and row strides, in elements, of q, k,
+ *             q_out and k_out (d is contiguous); multiples of 8, outputs' > 0 (a
+ *             dimension of size 1 may name any valid stride).  NULL: all
+ *             contiguous.  Read during the call only.
+ * d           64 or 128;  rot a multiple of 16, 16..d;  mag finite.
+ * Products and sums in fp32, one rounding to bf16 (nearest even).
+ * Asynchronous on `stream`; N == 0 is a successful no-op.  Errors as fa_fwd, plus
+ * FA_ERR_STRIDE.
+ */
+int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq, const int* positions,
+            long long position_stride, long long offset, const long long* strides, int B, int H, int Hk, int N, int d,
+            int rot, float mag, int interleaved, int backward, cudaStream_t stream);
+
+/*
+ * The paged K/V cache of fa_kv_append, fa_fwd_paged and fa_fwd_prefix.
+ *
+ * k_cache, v_cache  bf16 [n_pages, Hk, page_size, d] views with free page, head
+ *                   and token strides (elements, multiples of 8, > 0; d contiguous),
+ *                   so token-major pages [n_pages, page_size, Hk, d] are the same
+ *                   cache with other strides.  page_size 16, 32, 64, 128 or 256.
+ * block_table       int32 [B, max_pages]: entry i of a sequence names the page of
+ *                   its tokens [i * page_size, (i + 1) * page_size).  Entries
+ *                   past the sequence's length, or wholly below its window, are
+ *                   not read.
+ * seq_lens          int32 [B]: tokens of each sequence in the cache, the new ones
+ *                   of this step INCLUDED (the same values serve the append and
+ *                   the attention of a step).  <= 0: an empty entry.
+ * new_lens          int32 [B]: how many of the T new rows each sequence has
+ *                   (clamped to 0..T), or NULL: T each.  Row t < new_lens[b] is
+ *                   the token at own position seq_lens[b] - new_lens[b] + t;
+ *                   rows past it are padding, and so are rows whose position
+ *                   would be negative.
+ * A page index that is needed and lies outside [0, n_pages), or a length past
+ * max_pages * page_size, raises bit 1 of the status word (fa_fwd_status:
+ * FA_ERR_PAGE): the append skips the token, the attention reads zeros for the
+ * page or stops at the table's end; memory outside the cache is never touched.
+ */
+
+/*
+ * fa_kv_append -- put the new tokens' keys (rotated as by fa_rope) and values
+ * into their cache slots, and rotate their queries, in one kernel.
+ *
+ * q, q_out  bf16 [B, H, T, d] (H = 0: keys and values only);  k, v bf16
+ *           [B, Hk, T, d].  Padding rows are neither read nor written.
+ * strides   host array of 18: batch, head and row strides of q, k and v, the same
+ *           of q_out, then page, head and token strides of k_cache and v_cache.
+ * rot       0 (nothing turns; inv_freq may be NULL) or as in fa_rope; position =
+ *           offset + own position (a shared prefix's length goes in offset).
+ * Two tokens of one call must not share a slot.  Cache slots of other tokens
+ * stay as they are.  Errors as fa_rope; T == 0 is a successful no-op.
+ * The first call on a device looks up the status word's address there: make
+ * that first call before any stream capture.
+ */
+int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
+                 const double* inv_freq, const int* block_table, const int* seq_lens, const int* new_lens,
+                 const long long* strides, int B, int H, int Hk, int T, int d, int rot, int n_pages, int page_size,
+                 int max_pages, long long offset, float mag, int interleaved, cudaStream_t stream);
+
+/*
+ * fa_fwd_paged -- O and LSE (as fa_fwd) of the new tokens' queries over their
+ * sequences' cached keys, grouped heads included: query head h reads K/V head
+ * h / (H / Hk).
+ *
+ * q, o  bf16 [B, H, T, d] contiguous;  lse fp32 [B, H, T].
+ * The token at own position pos sees own keys j with
+ *     pos - window_left <= j <= pos + window_right,   0 <= j < seq_lens[b],
+ * -1 leaving a side open: (-1, 0) is causal, (-1, -1) every cached key (an
+ * encoder's states of a length per sequence).  Padding rows and rows that see
+ * no key get O = 0, LSE = -inf.  Slots outside every row's window or past the
+ * length may hold anything, NaN included; a key that some rows of a sequence
+ * see and others do not must be finite.
+ * strides    host array of 6: page, head and token strides of k_cache, v_cache.
+ * workspace  fa_paged_workspace_bytes(B, H, Hk, T, d, 0) bytes, 16-byte
+ *            aligned, not read before it is written, used by nothing else until
+ *            the call's kernels have finished (two calls that may overlap, or two
+ *            captured graphs that may, need one each).
+ * Lengths are read on the device, so a captured call may be replayed as they
+ * grow (within max_pages).  No atomics order the sums: results repeat bit
+ * for bit on one GPU.  Errors as fa_fwd, plus FA_ERR_STRIDE and FA_ERR_WORKSPACE;
+ * T == 0 is a successful no-op.  First call before any stream capture, as
+ * fa_kv_append.
+ */
+int fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, const int* block_table,
+                 const int* seq_lens, const int* new_lens, const long long* strides, int B, int H, int Hk, int T, int d,
+                 int n_pages, int page_size, int max_pages, float scale, int window_left, int window_right,
+                 void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fa_fwd_prefix -- fa_fwd_paged (causal) for a batch whose sequences all begin
+ * with the same prefix_len tokens: the prefix's K and V are read once for the
+ * batch, its part and each sequence's own are joined as in fa_fwd_splitkv.
+ *
+ * prefix_pages  int32 [ceil(prefix_len / page_size)]: the prefix's pages.
+ * prefix_len    > 0, known to the host.
+ * block_table and seq_lens describe the sequences' OWN tokens, after the prefix;
+ * every row that holds a token sees the whole prefix and its own keys up to
+ * itself.  seq_lens[b] <= 0: an empty entry (O = 0, LSE = -inf).
+ * workspace     fa_paged_workspace_bytes(B, H, Hk, T, d, prefix_len) bytes.
+ * Otherwise as fa_fwd_paged.
+ */
+int fa_fwd_prefix(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                  const int* prefix_pages, int prefix_len, const int* block_table, const int* seq_lens,
+                  const int* new_lens, const long long* strides, int B, int H, int Hk, int T, int d, int n_pages,
+                  int page_size, int max_pages, float scale, void* workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+
+/* Workspace bytes of fa_fwd_paged (prefix_len 0) and fa_fwd_prefix on the
+ * current device (0 for invalid sizes); it does not depend on the lengths. */
+size_t fa_paged_workspace_bytes(int B, int H, int Hk, int T, int d, int prefix_len);
+
 /* Size of the fixed device array fa_fwd_splitkv_noalloc works in. */
 #define FA_NOALLOC_SCRATCH_BYTES (16u << 20)
 
@@ -213,6 +346,10 @@ size_t fa_bwd_workspace_bytes(int B, int H, int Nq);
 int fa_fwd_splitkv_noalloc(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,
                            int Nq, int Nk, int d, float scale, int causal, int n_splits, cudaStream_t stream);
 
+/* Bits of the device status word. */
+#define FA_STATUS_TIMEOUT 1u /* a bounded wait gave up; bits 8.. name the role   */
+#define FA_STATUS_PAGE 2u    /* a page index or length outside the cache or table */
+
 /* Human-readable text for a status code (static storage, never NULL). */
 const char* fa_strerror(int status);
 
@@ -227,8 +364,10 @@ int fa_version(void);
  * device status word (bit 0, and bits 8.. = 1 softmax/compute, 2 producer,
  * 4 MMA issuer, 8 epilogue), the CTA drains its in-flight copies and MMAs,
  * frees its tensor memory and exits.  *detail (optional) receives the raw
- * status word.  clear != 0 resets the word.  Returns FA_OK, FA_ERR_TIMEOUT, or
- * FA_ERR_LAUNCH if synchronisation failed.
+ * status word.  clear != 0 resets the word.  Returns FA_OK, FA_ERR_TIMEOUT,
+ * FA_ERR_PAGE (bit 1 alone: a page index or sequence length that the paged
+ * calls met lies outside the cache or its table), or FA_ERR_LAUNCH if
+ * synchronisation failed.
  */
 int fa_fwd_status(cudaStream_t stream, unsigned int* detail, int clear);
 

@@ -1,0 +1,515 @@
+"""Rotary positions, the paged cache's append, attention over the paged cache and
+shared-prefix attention, against plain 64-bit implementations (serving_ref).
+
+Caches start as NaN everywhere, so a slot that a row must not see shows up in its
+output, and a slot that the append must not touch keeps its NaN's bits.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import serving_ref as ref
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import exact_attention_19_gb300 as mod
+    from exact_attention_19_gb300 import build
+
+    build.build()
+    mod.load()
+    return mod
+
+
+@pytest.fixture(autouse=True)
+def _status(fa):
+    fa.fa_fwd_status(None, clear=True)
+    yield
+    torch.cuda.synchronize()
+    st, word = fa.fa_fwd_status(None, clear=True)
+    assert st == 0, f"status word {word:#x}"
+
+
+def rand(seed, *shape):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=g).to(torch.bfloat16).cuda()
+
+
+def f64(t):
+    return t.detach().to(torch.float64).cpu().numpy()
+
+
+# ---------------------------------------------------------------------------
+# rope
+# ---------------------------------------------------------------------------
+def packed(seed, B, N, H, Hk, d):
+    """Views [B, heads, N, d] of a packed token-major projection."""
+    x = rand(seed, B, N, (H + 2 * Hk) * d)
+    cut = [x[..., a * d:b * d].unflatten(-1, (b - a, d)).transpose(1, 2)
+           for a, b in ((0, H), (H, H + Hk), (H + Hk, H + 2 * Hk))]
+    return x, cut
+
+
+def check_rope(got, x, positions, w, mag, interleaved, sign=1.0, what=""):
+    x, got, w = f64(x), f64(got), f64(w)
+    for b in range(x.shape[0]):
+        p = positions[b] if positions.ndim == 2 else positions
+        y, size = ref.rotate(x[b], p, w, mag, interleaved, sign)
+        err = np.abs(got[b] - y)
+        assert np.all(err <= ref.rope_tol(y, size)), f"{what}: sequence {b} off by {err.max():.3e}"
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("B,H,Hk,N,d,rot", [
+    (1, 1, 1, 1, 64, 64), (2, 3, 1, 33, 64, 16), (1, 4, 4, 65, 64, 48), (3, 12, 12, 7, 64, 64),
+    (1, 8, 2, 31, 128, 128), (2, 5, 5, 129, 128, 64), (1, 2, 1, 300, 128, 112), (2, 32, 8, 40, 128, 32),
+])
+@pytest.mark.parametrize("strided", [False, True])
+def test_rope(fa, B, H, Hk, N, d, rot, interleaved, strided):
+    if strided:
+        _, (q, k, _) = packed(N, B, N, H, Hk, d)
+    else:
+        q, k = rand(N, B, H, N, d), rand(N + 1, B, Hk, N, d)
+    w, mag = fa.rope_freqs(rot)
+    assert mag == 1.0
+    yq, yk = fa.rope(q, k, w, interleaved=interleaved)
+    assert yq.is_contiguous() and yk.is_contiguous()
+    for y, x in ((yq, q), (yk, k)):
+        check_rope(y, x, np.arange(N), w, 1.0, interleaved)
+        assert torch.equal(y[..., rot:], x[..., rot:])
+
+
+@pytest.mark.parametrize("scaling,factor", [("linear", 4.0), ("base", 8.0), ("by_parts", 32.0)])
+def test_rope_far_positions(fa, scaling, factor):
+    """Any 32-bit position, negative ones too, and a large offset: the angle stays exact."""
+    N, d = 9, 128
+    q = rand(3, 2, 2, N, d)
+    w, mag = fa.rope_freqs(d, base=500000.0, scaling=scaling, factor=factor)
+    p = np.array([[0, 1, 65535, 100000, 999999, 2 ** 24 + 1, 2 ** 31 - 1, -1, -2 ** 31],
+                  [5, 4, 3, 2, 1, 0, 7, 7, 123456789]], dtype=np.int32)
+    y, none = fa.rope(q, None, w, positions=torch.from_numpy(p).cuda(), mag=mag)
+    assert none is None
+    check_rope(y, q, p, w, mag, False)
+    y, _ = fa.rope(q, None, w, positions=torch.from_numpy(p[0]).cuda(), offset=10 ** 12, interleaved=True)
+    check_rope(y, q, p[0].astype(np.int64) + 10 ** 12, w, 1.0, True)
+
+
+def test_rope_frequency_forms(fa):
+    """Zero, negative, tiny and above-one-turn frequencies."""
+    w = torch.tensor([0.0, -0.25, 1e-300, 2.0 ** -70, 7.0, 1e6, 3.5e9, 1.0], dtype=torch.float64).cuda()
+    q = rand(8, 1, 1, 5, 64)
+    y, _ = fa.rope(q, None, w, offset=3)
+    check_rope(y, q, np.arange(5) + 3, w, 1.0, False)
+
+
+def test_rope_in_place_and_strided_outputs(fa):
+    B, N, H, Hk, d = 2, 37, 4, 2, 64
+    w, _ = fa.rope_freqs(32)
+    x, (q, k, v) = packed(5, B, N, H, Hk, d)
+    q0, k0, v0 = q.clone(), k.clone(), v.clone()
+    oq, ok = fa.rope(q, k, w, q_out=q, k_out=k)
+    assert oq is q and ok is k
+    check_rope(q, q0, np.arange(N), w, 1.0, False)
+    check_rope(k, k0, np.arange(N), w, 1.0, False)
+    assert torch.equal(v, v0)  # the packed neighbour is untouched
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot", [(64, 64), (128, 48)])
+def test_rope_backward(fa, d, rot, interleaved):
+    """The formula's transpose, and differences: for the linear map R the derivative of <g, R x> along e is
+    (<g, R e> - <g, R(-e)>) / 2."""
+    B, H, Hk, N, mag = 2, 3, 1, 21, 1.25
+    w, _ = fa.rope_freqs(rot)
+    gq, gk = rand(1, B, H, N, d), rand(2, B, Hk, N, d)
+    dx = torch.zeros(B, N, (H + Hk) * d, device="cuda", dtype=torch.bfloat16)
+    oq = dx[..., :H * d].unflatten(-1, (H, d)).transpose(1, 2)
+    ok = dx[..., H * d:].unflatten(-1, (Hk, d)).transpose(1, 2)
+    dq, dk = fa.rope_bwd(gq, gk, w, offset=50, interleaved=interleaved, mag=mag, q_out=oq, k_out=ok)
+    for got, g in ((dq, gq), (dk, gk)):
+        check_rope(got, g, np.arange(N) + 50, w, mag, interleaved, -1.0)
+    for e in (0, 1, rot // 2, rot - 1, d - 1):
+        x = torch.zeros_like(gq)
+        x[..., e] = 1.0
+        up, _ = fa.rope(x, None, w, offset=50, interleaved=interleaved, mag=mag)
+        down, _ = fa.rope(-x, None, w, offset=50, interleaved=interleaved, mag=mag)
+        terms = f64(gq) * (f64(up) - f64(down)) / 2
+        diff = terms.sum(-1)
+        # each of the two terms of R e is rounded to bf16 once, the gradient once
+        tol = ref.U * (np.abs(terms).sum(-1) + np.abs(diff)) + 2.0 ** -18 * mag * np.abs(f64(gq)).max()
+        assert np.all(np.abs(f64(dq)[..., e] - diff) <= tol)
+
+
+# ---------------------------------------------------------------------------
+# the paged cache
+# ---------------------------------------------------------------------------
+class Cache:
+    """A cache whose pages lie in random order; unused slots hold NaN."""
+
+    def __init__(self, seed, B, Hk, d, page, max_len, token_major=False, prefix_len=0):
+        self.page, self.d, self.Hk = page, d, Hk
+        rng = np.random.default_rng(seed)
+        self.max_pages = max(1, -(-max_len // page))
+        n_prefix = -(-prefix_len // page)
+        n_pages = B * self.max_pages + n_prefix + 2
+        order = rng.permutation(n_pages).astype(np.int32)
+        self.table = order[:B * self.max_pages].reshape(B, self.max_pages).copy()
+        self.prefix_pages = order[B * self.max_pages:B * self.max_pages + n_prefix].copy()
+        shape = (n_pages, page, Hk, d) if token_major else (n_pages, Hk, page, d)
+        self.k = torch.full(shape, math.nan, dtype=torch.bfloat16, device="cuda")
+        self.v = torch.full(shape, math.nan, dtype=torch.bfloat16, device="cuda")
+        if token_major:
+            self.k, self.v = self.k.transpose(1, 2), self.v.transpose(1, 2)
+        self.seed = seed
+
+    def fill(self, pages, n, seed):
+        """Random K and V for tokens 0..n-1 of a page list."""
+        if n <= 0:
+            return
+        g = torch.Generator().manual_seed(seed)
+        for c in (self.k, self.v):
+            x = torch.randn(n, self.Hk, self.d, generator=g).to(torch.bfloat16).cuda()
+            j = torch.arange(n, device="cuda")
+            at = torch.from_numpy(np.asarray(pages)).cuda().long()[j // self.page]
+            c[at, :, j % self.page] = x
+
+    def device_table(self):
+        return torch.from_numpy(self.table).cuda()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("B,H,Hk,T,d,page,rot,lens,new,token_major,interleaved", [
+    (1, 1, 1, 1, 64, 16, 64, [1], None, False, False),
+    (3, 4, 2, 1, 128, 16, 128, [1, 17, 40], None, False, True),
+    (3, 4, 4, 5, 64, 32, 32, [5, 33, 64], None, True, False),
+    (4, 8, 1, 7, 128, 64, 64, [7, 3, 0, 70], [7, 2, 0, 1], False, False),
+    (2, 2, 2, 100, 64, 128, 64, [100, 130], [100, 63], True, True),
+    (2, 6, 3, 300, 128, 256, 0, [300, 512], [300, 299], False, False),
+    (2, 0, 2, 4, 64, 16, 16, [4, 9], None, False, False),
+    (3, 2, 1, 6, 64, 16, 64, [3, -4, 20], [6, 6, 9], False, False),  # lengths below the new rows, new past T
+])
+def test_append(fa, B, H, Hk, T, d, page, rot, lens, new, token_major, interleaved):
+    c = Cache(B * T, B, Hk, d, page, max(max(lens), 1) + page, token_major)
+    _, (q, k, v) = packed(T, B, T, H, Hk, d)
+    k0, v0 = c.k.clone(), c.v.clone()
+    w, mag = (fa.rope_freqs(rot, scaling="by_parts", factor=4.0) if rot else (None, 1.0))
+    q_out = torch.full((B, H, T, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = fa.kv_append(q if H else None, k, v, c.k, c.v, c.device_table(), i32(lens), w, offset=1000,
+                       new_lens=None if new is None else i32(new), interleaved=interleaved, mag=mag,
+                       q_out=q_out if H else None)
+    assert out is (q_out if H else None)
+    written = torch.zeros(k0.shape[0], page, dtype=torch.bool)
+    for b in range(B):
+        m = min(T, new[b]) if new is not None else T
+        for t in range(T):
+            own = lens[b] - m + t
+            if t >= m or own < 0:
+                if H:
+                    assert torch.all(q_out[b, :, t] == 7.0)
+                continue
+            at, slot = int(c.table[b, own // page]), own % page
+            written[at, slot] = True
+            assert torch.equal(c.v[at, :, slot], v[b, :, t])
+            pairs = [(c.k[at, :, slot], k[b, :, t])] + ([(q_out[b, :, t], q[b, :, t])] if H else [])
+            for got, x in pairs:
+                if not rot:
+                    assert torch.equal(got, x)
+                    continue
+                y, size = ref.rotate(f64(x)[:, None], [own + 1000], f64(w), mag, interleaved)
+                assert np.all(np.abs(f64(got)[:, None] - y) <= ref.rope_tol(y, size))
+    keep = ~written[:, None, :, None].expand(k0.shape).cuda()
+    for now, before in ((c.k, k0), (c.v, v0)):
+        assert torch.equal(now.contiguous().view(torch.int16)[keep], before.contiguous().view(torch.int16)[keep])
+
+
+def run_paged(fa, c, q, lens, new, window=(-1, 0), prefix_len=0, **kw):
+    args = dict(new_lens=None if new is None else i32(new), **kw)
+    if prefix_len:
+        return fa.fwd_prefix(q, c.k, c.v, torch.from_numpy(c.prefix_pages).cuda(), prefix_len, c.device_table(),
+                             i32(lens), **args)
+    return fa.fwd_paged(q, c.k, c.v, c.device_table(), i32(lens), window=window, **args)
+
+
+def paged_case(fa, seed, B, H, Hk, T, d, page, lens, new=None, window=(-1, 0), token_major=False, prefix_len=0,
+               scale=None, q_scale=1.0):
+    c = Cache(seed, B, Hk, d, page, max(max(lens), 1), token_major, prefix_len)
+    for b in range(B):
+        c.fill(c.table[b], lens[b], seed + b)
+    c.fill(c.prefix_pages, prefix_len, seed + 99)
+    q = (rand(seed + 7, B, H, T, d).float() * q_scale).to(torch.bfloat16)
+    # slots wholly below every row's window may hold anything too
+    if window[0] >= 0:
+        for b in range(B):
+            m = T if new is None else min(new[b], T)
+            low = max(0, lens[b] - m - window[0])
+            for j in range(min(low, lens[b])):
+                c.k[int(c.table[b, j // page]), :, j % page] = math.nan
+                c.v[int(c.table[b, j // page]), :, j % page] = math.inf
+            c.table[b, :low // page] = -1  # their pages may have been given back
+    used = np.array([-(-max(0, n) // page) for n in lens])
+    c.table[np.arange(c.max_pages)[None, :] >= used[:, None]] = -5
+    o, lse = run_paged(fa, c, q, lens, new, window, prefix_len, scale=scale)
+    torch.cuda.synchronize()
+    table = np.maximum(c.table, 0)
+    want = ref.paged(f64(q), f64(c.k), f64(c.v), table, lens, [T] * B if new is None else new, window[0], window[1],
+                     1 / math.sqrt(d) if scale is None else scale, c.prefix_pages, prefix_len)
+    ref.check_attention(f64(o), f64(lse), want, f"{B}x{H}/{Hk} T={T} d={d} page={page} lens={lens} {window}")
+    return c, q, o, lse
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,Hk,T,page,lens,new", [
+    (1, 1, 1, 1, 16, [1], None),
+    (1, 1, 1, 1, 16, [2000], None),
+    (2, 2, 2, 1, 32, [63, 64], None),
+    (3, 4, 2, 1, 64, [65, 0, 127], None),
+    (4, 8, 1, 1, 128, [128, 129, 1, 500], None),
+    (2, 16, 1, 1, 16, [333, 16], None),
+    (2, 24, 1, 1, 16, [17, 200], None),              # 24 rows: two row blocks of 16
+    (3, 3, 3, 5, 16, [5, 77, 256], None),
+    (2, 8, 2, 7, 256, [7, 511], [7, 3]),
+    (3, 4, 4, 4, 16, [9, 130, 0], [2, 4, 0]),
+    (2, 10, 2, 33, 32, [33, 190], [1, 33]),
+    (1, 4, 1, 130, 64, [700], None),                  # 520 rows of one K/V head
+    (2, 2, 1, 70, 16, [3, 64], None),                 # shorter than the new rows: some hold no token
+    (70, 2, 1, 1, 16, [i * 3 % 50 for i in range(70)], None),
+    (150, 1, 1, 1, 16, [i % 7 for i in range(150)], None),
+])
+def test_paged(fa, B, H, Hk, T, d, page, lens, new):
+    paged_case(fa, 1 + B, B, H, Hk, T, d, page, lens, new)
+
+
+@pytest.mark.parametrize("token_major", [False, True])
+@pytest.mark.parametrize("B,H,Hk,T,d,page,lens,window", [
+    (2, 4, 2, 1, 64, 16, [300, 40], (0, 0)),
+    (2, 4, 2, 3, 128, 16, [300, 40], (20, 0)),
+    (3, 2, 1, 4, 64, 64, [1000, 64, 5], (63, 0)),
+    (2, 2, 2, 6, 64, 32, [100, 6], (10, 2)),
+    (2, 2, 2, 9, 128, 16, [100, 5], (-1, -1)),        # every cached key, more rows than keys
+    (2, 4, 1, 40, 64, 128, [500, 41], (64, -1)),
+    (1, 2, 1, 2, 64, 16, [50], (2 ** 31 - 1, 2 ** 31 - 1)),
+])
+def test_paged_windows(fa, B, H, Hk, T, d, page, lens, window, token_major):
+    paged_case(fa, 11, B, H, Hk, T, d, page, lens, None, window, token_major)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,H,Hk,T,page,prefix_len,lens,new,token_major", [
+    (1, 1, 1, 1, 16, 1, [1], None, False),
+    (2, 2, 1, 1, 16, 100, [1, 33], None, False),
+    (5, 4, 4, 1, 32, 64, [1, 2, 3, 64, 65], None, True),
+    (9, 8, 2, 1, 64, 1000, [i + 1 for i in range(9)], None, False),
+    (3, 6, 2, 4, 128, 129, [4, 140, 9], [4, 1, 3], False),
+    (4, 2, 1, 3, 16, 77, [3, 0, 2, 50], [3, 0, 3, 2], True),   # an empty entry; a row before its sequence
+    (40, 4, 1, 1, 256, 700, [1 + i * 7 % 90 for i in range(40)], None, False),
+    (33, 16, 2, 2, 16, 257, [2 + i % 5 for i in range(33)], None, False),
+])
+def test_prefix(fa, d, B, H, Hk, T, page, prefix_len, lens, new, token_major):
+    paged_case(fa, 21 + B, B, H, Hk, T, d, page, lens, new, (-1, 0), token_major, prefix_len)
+
+
+def test_paged_wide_scores_and_scale(fa):
+    """Logits spread over hundreds: the running maximum moves often, most weights vanish."""
+    paged_case(fa, 31, 2, 4, 2, 3, 128, 16, [400, 77], scale=1.0, q_scale=4.0)
+    paged_case(fa, 32, 2, 4, 2, 1, 64, 16, [400, 77], scale=2.0, q_scale=4.0, prefix_len=150)
+
+
+def test_paged_infinite_and_lowest_values(fa):
+    """Keys of the type's lowest value (finite, scores near -3e38): they weigh nothing beside others."""
+    c = Cache(5, 1, 1, 64, 16, 40)
+    c.fill(c.table[0], 40, 5)
+    q = rand(6, 1, 1, 1, 64).abs()
+    c.k[int(c.table[0, 1]), :, 3] = torch.finfo(torch.bfloat16).min / 64
+    o, lse = run_paged(fa, c, q, [40], None)
+    want = ref.paged(f64(q), f64(c.k), f64(c.v), c.table, [40], [1], -1, 0, 0.125)
+    ref.check_attention(f64(o), f64(lse), want)
+
+
+def test_paged_repeats_bit_for_bit_and_takes_buffers(fa):
+    B, H, Hk, T, d = 3, 8, 2, 2, 128
+    c = Cache(41, B, Hk, d, 16, 900)
+    lens = [900, 3, 411]
+    for b in range(B):
+        c.fill(c.table[b], lens[b], b)
+    q = rand(42, B, H, T, d)
+    o1, l1 = run_paged(fa, c, q, lens, None)
+    ws = torch.full((fa.fa_paged_workspace_bytes(B, H, Hk, T, d, 0),), 255, dtype=torch.uint8, device="cuda")
+    o2, l2 = torch.full_like(o1, math.nan), torch.full_like(l1, math.nan)
+    got = run_paged(fa, c, q, lens, None, out=o2, lse=l2, workspace=ws)
+    assert got[0] is o2 and got[1] is l2
+    assert torch.equal(o1, o2) and torch.equal(l1, l2)
+    with pytest.raises(fa.FaError) as e:
+        run_paged(fa, c, q, lens, None, workspace=ws[:1024])
+    assert e.value.status == 11
+
+
+def test_bad_pages_and_lengths_are_reported(fa):
+    """A page index outside the cache, or a length past the table: no access outside, FA_ERR_PAGE."""
+    B, H, Hk, T, d, page = 2, 2, 1, 1, 64, 16
+    c = Cache(51, B, Hk, d, page, 64)
+    lens = [40, 64]
+    for b in range(B):
+        c.fill(c.table[b], lens[b], b)
+    c.fill(list(range(c.k.shape[0])), c.k.shape[0] * page, 9)
+    q = rand(52, B, H, T, d)
+    good, _ = run_paged(fa, c, q, lens, None)
+    for bad in (-1, c.k.shape[0], 2 ** 31 - 1, -2 ** 31):
+        table = c.table.copy()
+        c.table[0, 1] = bad
+        o, lse = run_paged(fa, c, q, lens, None)
+        st, word = fa.fa_fwd_status(None, clear=True)
+        assert (st, word) == (12, 2)
+        assert torch.equal(o[1], good[1]) and bool(torch.isfinite(o).all())
+        k0 = c.k.clone()
+        fa.kv_append(None, rand(1, B, Hk, T, d), rand(2, B, Hk, T, d), c.k, c.v, c.device_table(), i32([17, 0]))
+        st, word = fa.fa_fwd_status(None, clear=True)
+        assert (st, word) == (12, 2)
+        assert torch.equal(c.k, k0)
+        c.table = table
+    o, _ = run_paged(fa, c, q, [65, 64], None)
+    assert fa.fa_fwd_status(None, clear=True)[0] == 12
+    assert torch.equal(o[1], good[1])
+    fa.kv_append(None, rand(1, B, Hk, T, d), rand(2, B, Hk, T, d), c.k, c.v, c.device_table(), i32([65, 0]))
+    assert fa.fa_fwd_status(None, clear=True)[0] == 12
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("d,H,Hk,page", [(64, 4, 4, 16), (128, 6, 2, 32)])
+def test_generation_matches_the_dense_forward(fa, d, H, Hk, page):
+    """A prompt in two chunks, then single tokens, through append and paged attention, against rope and the
+    dense causal forward over the whole sequence; then the same with the prompt as a shared prefix."""
+    B, N, cuts = 2, 120, [0, 50, 111, 112, 113, 120]
+    w, mag = fa.rope_freqs(d, scaling="by_parts", factor=2.0)
+    _, (q, k, v) = packed(60, B, N, H, Hk, d)
+    rq, rk = fa.rope(q, k, w, mag=mag)
+    wide = (lambda x: x.repeat_interleave(H // Hk, dim=1).contiguous())
+    want, want_l = fa.fwd(rq, wide(rk), wide(v.contiguous()), causal=True, n_splits=1)
+    c = Cache(61, B, Hk, d, page, N)
+    table = c.device_table()
+    for a, b in zip(cuts, cuts[1:]):
+        lens = i32([b] * B)
+        tq = fa.kv_append(q[:, :, a:b], k[:, :, a:b], v[:, :, a:b], c.k, c.v, table, lens, w, mag=mag)
+        assert torch.equal(tq, rq[:, :, a:b])
+        o, lse = fa.fwd_paged(tq, c.k, c.v, table, lens)
+        # both sides round the same P and O to bf16: two roundings of each
+        err = (o.float() - want[:, :, a:b].float()).abs()
+        assert bool((err <= 4 * ref.U * (want[:, :, a:b].float().abs() + v.float().abs().max())).all())
+        assert bool(((lse - want_l[:, :, a:b]).abs() <= 2.0 ** -11 * want_l[:, :, a:b].abs().clamp(min=1)).all())
+    # the first sequence's first 100 tokens as every sequence's prefix
+    n = 100
+    c = Cache(62, B, Hk, d, page, N - n, prefix_len=n)
+    one = torch.from_numpy(c.prefix_pages).cuda()[None]
+    fa.kv_append(None, k[:1, :, :n], v[:1, :, :n], c.k, c.v, one, i32([n]), w, mag=mag)
+    lens = i32([N - n] * B)
+    same = [x[:1, :, n:].expand(B, -1, -1, -1) for x in (q, k, v)]
+    tq = fa.kv_append(*same, c.k, c.v, c.device_table(), lens, w, offset=n, mag=mag)
+    o, lse = fa.fwd_prefix(tq, c.k, c.v, one[0], n, c.device_table(), lens)
+    for b in range(B):
+        err = (o[b].float() - want[0, :, n:].float()).abs()
+        assert bool((err <= 4 * ref.U * (want[0, :, n:].float().abs() + v.float().abs().max())).all())
+
+
+def test_training_step_through_rope(fa):
+    """rope, fwd, bwd, rope_bwd: the gradient of the packed projection against 64-bit autograd."""
+    B, H, N, d = 1, 2, 70, 64
+    w, _ = fa.rope_freqs(d)
+    x, (q, k, v) = packed(70, B, N, H, H, d)
+    g = rand(71, B, H, N, d)
+    rq, rk = fa.rope(q, k, w)
+    vc = v.contiguous()
+    o, lse = fa.fwd(rq, rk, vc, causal=True, n_splits=1)
+    dq, dk, dv = fa.bwd(rq, rk, vc, o, lse, g, causal=True)
+    dx = torch.empty_like(x)
+    oq, ok, ov = (dx[..., i * H * d:(i + 1) * H * d].unflatten(-1, (H, d)).transpose(1, 2) for i in range(3))
+    fa.rope_bwd(dq, dk, w, q_out=oq, k_out=ok)
+    ov.copy_(dv)
+    x64 = x.double().cpu().requires_grad_()
+    a = torch.outer(torch.arange(N, dtype=torch.float64), w.cpu())
+    turn = torch.polar(torch.ones_like(a), a)
+    parts = [x64[..., i * H * d:(i + 1) * H * d].unflatten(-1, (H, d)).transpose(1, 2) for i in range(3)]
+
+    def turned(y):
+        z = torch.complex(y[..., :d // 2], y[..., d // 2:]) * turn
+        return torch.cat([z.real, z.imag], -1)
+
+    s = turned(parts[0]) @ turned(parts[1]).transpose(-1, -2) / math.sqrt(d)
+    s = s.masked_fill(~torch.ones(N, N, dtype=torch.bool).tril(), -math.inf)
+    ((s.softmax(-1) @ parts[2]) * g.double().cpu()).sum().backward()
+    # bf16 q, k (rotated), P, dS, O and the gradients: about eight roundings of size u, taken of the largest entry
+    err = (dx.double().cpu() - x64.grad).abs().max() / x64.grad.abs().max()
+    assert err <= 8 * ref.U, float(err)
+
+
+def test_captured_steps_follow_growing_lengths(fa):
+    """One captured decode step (append, attention) replayed token after token, beside eager calls."""
+    B, H, Hk, d, page, N = 2, 4, 2, 64, 16, 40
+    w, _ = fa.rope_freqs(d)
+    _, (q, k, v) = packed(80, B, N, H, Hk, d)
+    caches = [Cache(81, B, Hk, d, page, N) for _ in range(2)]
+    table = caches[0].device_table()
+    lens = i32([1] * B)
+    sq, sk, sv = (x[:, :, :1].contiguous() for x in (q, k, v))
+    o, lse = torch.empty_like(sq), torch.empty(B, H, 1, device="cuda")
+
+    def step(c):
+        tq = fa.kv_append(sq, sk, sv, c.k, c.v, table, lens, w)
+        fa.fwd_paged(tq, c.k, c.v, table, lens, out=o, lse=lse)
+
+    step(caches[1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(caches[0])
+    for t in range(N):
+        lens.fill_(t + 1)
+        for s, x in ((sq, q), (sk, k), (sv, v)):
+            s.copy_(x[:, :, t:t + 1])
+        o.zero_()
+        graph.replay()
+        got = o.clone(), lse.clone()
+        step(caches[1])
+        assert torch.equal(got[0], o) and torch.equal(got[1], lse), t
+    assert torch.equal(caches[0].k.view(torch.int16), caches[1].k.view(torch.int16))
+
+
+def test_two_streams_at_once(fa):
+    """Calls on two streams, each with its own workspace, give what they give alone."""
+    B, H, Hk, T, d = 4, 8, 2, 1, 128
+    c = Cache(91, B, Hk, d, 16, 3000)
+    lens = [3000, 10, 700, 1500]
+    for b in range(B):
+        c.fill(c.table[b], lens[b], b)
+    qs = [rand(92 + i, B, H, T, d) for i in range(2)]
+    alone = [run_paged(fa, c, q, lens, None) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            got[i].append(run_paged(fa, c, qs[i], lens, None, stream=s))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, alone[i][0]) and torch.equal(lse, alone[i][1])
+
+
+def test_no_tokens_is_a_noop(fa):
+    c = Cache(95, 2, 1, 64, 16, 32)
+    e = torch.empty(2, 1, 0, 64, dtype=torch.bfloat16, device="cuda")
+    w, _ = fa.rope_freqs(64)
+    assert fa.rope(e, e, w)[0].shape == e.shape
+    assert fa.kv_append(e, e, e, c.k, c.v, c.device_table(), i32([3, 3]), w).shape == e.shape
+    o, lse = run_paged(fa, c, e, [3, 3], None)
+    assert o.shape == e.shape and lse.shape == (2, 1, 0)
