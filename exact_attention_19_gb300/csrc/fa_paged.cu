@@ -7,6 +7,7 @@
 #include "fa.h"
 #include "fa_host.h"
 #include "fa_paged_kernel.cuh"
+#include "fa_paged_tile.cuh"
 
 namespace {
 
@@ -16,8 +17,13 @@ std::atomic<bool> g_ready[fa_host::kMaxDevices];
 
 template <int D>
 bool opt_in() {
+  const int tile = static_cast<int>(fa::TileCfg<D>::kSmemBytes);
   return cudaFuncSetAttribute(fa::fa_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(fa::PagedCfg<D>::kSmemBytes)) == cudaSuccess;
+                              static_cast<int>(fa::PagedCfg<D>::kSmemBytes)) == cudaSuccess &&
+         cudaFuncSetAttribute(fa::fa_paged_tile_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, tile) ==
+             cudaSuccess &&
+         cudaFuncSetAttribute(fa::fa_paged_tile_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, tile) ==
+             cudaSuccess;
 }
 
 // The kernels' shared-memory opt-in, once per device (a repeated call is harmless).
@@ -47,29 +53,40 @@ bool make_cache_map(CUtensorMap* map, const void* ptr, int d, int page, int Hk, 
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
+// Rows per own row block: the warp-level kernel's 16 while the rows of one
+// (sequence, K/V head) fit one block, else the tcgen05 kernel's 128.
+int own_block_rows(int rows) { return rows <= 16 ? 16 : 128; }
+
 // Parts of the workspace, in order; every size is a multiple of 16 bytes.
 struct Layout {
-  size_t plan, piece_o, piece_l, whole_o, whole_l;
-  size_t bytes() const { return plan + piece_o + piece_l + whole_o + whole_l; }
+  size_t plan, piece_o[2], piece_l[2], whole_o[2], whole_l[2];
+  size_t bytes() const {
+    size_t n = plan;
+    for (int i = 0; i < 2; ++i) n += piece_o[i] + piece_l[i] + whole_o[i] + whole_l[i];
+    return n;
+  }
 };
-Layout layout(int B, int H, int T, int d, bool prefix, int sms) {
-  const size_t ctas = 2 * static_cast<size_t>(sms);
-  const size_t rows = static_cast<size_t>(B) * H * T;
-  Layout l;
+Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
+  const size_t all = static_cast<size_t>(B) * H * T;
+  const int rows = H / Hk * T;
+  Layout l = {};
   l.plan = up16((static_cast<size_t>(B) + 3) * sizeof(long long));
-  l.piece_o = 2 * ctas * 16 * d * sizeof(float);
-  l.piece_l = 2 * ctas * 16 * sizeof(float);
-  l.whole_o = prefix ? 2 * rows * d * sizeof(float) : 0;
-  l.whole_l = prefix ? up16(2 * rows * sizeof(float)) : 0;
+  for (int i = 0; i < (prefix_len > 0 ? 2 : 1); ++i) {
+    size_t ctas = 2 * static_cast<size_t>(sms);
+    if (i == 1)
+      ctas = static_cast<size_t>(fa::paged_ctas(
+          2ll * sms, 1ll * Hk * fa::prefix_blocks(B, rows, fa::kPrefixRows) * fa::prefix_tiles(prefix_len)));
+    const size_t pieces = 2 * ctas * (i == 0 ? own_block_rows(rows) : fa::kPrefixRows);
+    l.piece_o[i] = pieces * d * sizeof(float);
+    l.piece_l[i] = pieces * sizeof(float);
+    l.whole_o[i] = prefix_len > 0 ? all * d * sizeof(float) : 0;
+    l.whole_l[i] = prefix_len > 0 ? up16(all * sizeof(float)) : 0;
+  }
   return l;
 }
 
-template <int D>
-int launch(const CUtensorMap& mk, const CUtensorMap& mv, const fa::PagedParams& p, int ctas, long long rows,
-           cudaStream_t stream) {
-  using C = fa::PagedCfg<D>;
-  fa::fa_paged_kernel<D><<<static_cast<unsigned>(ctas), C::kThreads, C::kSmemBytes, stream>>>(mk, mv, p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
+template <int D, int RB>
+int launch_merge(const fa::PagedParams& p, long long rows, cudaStream_t stream) {
   // programmatic dependent launch: the merge's CTAs may be scheduled while the
   // last parts are computed and wait on the device for that grid's completion
   cudaLaunchConfig_t cfg = {};
@@ -81,8 +98,44 @@ int launch(const CUtensorMap& mk, const CUtensorMap& mv, const fa::PagedParams& 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, C::kRows, C::kTile>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, RB>, p);
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? FA_OK : FA_ERR_LAUNCH;
+}
+
+struct Caches {
+  const void *k, *v;
+  const long long* strides;
+  int d, page, Hk, n_pages;
+  bool maps(CUtensorMap* mk, CUtensorMap* mv, int box_rows) const {
+    const int rows = box_rows < page ? box_rows : page;
+    return make_cache_map(mk, k, d, page, Hk, n_pages, strides, rows) &&
+           make_cache_map(mv, v, d, page, Hk, n_pages, strides + 3, rows);
+  }
+};
+
+template <int D>
+int launch(const Caches& c, const fa::PagedParams& p, int sms, long long rows, cudaStream_t stream) {
+  using S = fa::PagedCfg<D>;
+  using T = fa::TileCfg<D>;
+  const bool tile = own_block_rows(p.rows) != 16;
+  CUtensorMap mk, mv;
+  if (tile || p.prefix_len > 0) {
+    if (!c.maps(&mk, &mv, T::kTile)) return FA_ERR_LAUNCH;
+  }
+  if (p.prefix_len > 0) {
+    fa::fa_paged_tile_kernel<D, true><<<static_cast<unsigned>(p.prefix_ctas), T::kThreads, T::kSmemBytes, stream>>>(
+        mk, mv, p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
+  }
+  if (tile) {
+    fa::fa_paged_tile_kernel<D, false><<<2 * sms, T::kThreads, T::kSmemBytes, stream>>>(mk, mv, p);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
+    return launch_merge<D, 128>(p, rows, stream);
+  }
+  if (!c.maps(&mk, &mv, S::kKeys)) return FA_ERR_LAUNCH;
+  fa::fa_paged_kernel<D><<<2 * sms, S::kThreads, S::kSmemBytes, stream>>>(mk, mv, p);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
+  return launch_merge<D, 16>(p, rows, stream);
 }
 
 int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, const int* prefix_pages,
@@ -115,7 +168,7 @@ int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
   int dev = -1, sms = 0;
   int st = fa_host::current_device(&dev, &sms);
   if (st != FA_OK) return st;
-  const Layout l = layout(B, H, T, d, prefix_len > 0, sms);
+  const Layout l = layout(B, H, Hk, T, d, prefix_len, sms);
   if (workspace_bytes < l.bytes()) return FA_ERR_WORKSPACE;
   const void* ptrs[] = {q, k_cache, v_cache, o, lse, workspace, block_table, seq_lens};
   for (const void* x : ptrs)
@@ -125,10 +178,6 @@ int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
     return FA_ERR_POINTER;
   st = ready(dev);
   if (st != FA_OK) return st;
-  CUtensorMap mk, mv;
-  if (!make_cache_map(&mk, k_cache, d, page_size, Hk, n_pages, strides, 16) ||
-      !make_cache_map(&mv, v_cache, d, page_size, Hk, n_pages, strides + 3, 16))
-    return FA_ERR_LAUNCH;
   fa::PagedParams p = {};
   p.q = static_cast<const uint16_t*>(q);
   p.out = static_cast<uint16_t*>(o);
@@ -149,15 +198,25 @@ int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
   p.left = left;
   p.right = right;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  if (prefix_len > 0) {
+    p.prefix_units =
+        1ll * Hk * fa::prefix_blocks(B, p.rows, fa::kPrefixRows) * fa::prefix_tiles(prefix_len);
+    p.prefix_ctas = fa::paged_ctas(2ll * sms, p.prefix_units);
+  }
   char* at = static_cast<char*>(workspace);
   p.plan = reinterpret_cast<long long*>(at);
-  p.piece_o = reinterpret_cast<float*>(at += l.plan);
-  p.piece_l = reinterpret_cast<float*>(at += l.piece_o);
-  p.whole_o = reinterpret_cast<float*>(at += l.piece_l);
-  p.whole_l = reinterpret_cast<float*>(at += l.whole_o);
+  at += l.plan;
+  for (int i = 0; i < 2; ++i) {
+    p.piece_o[i] = reinterpret_cast<float*>(at);
+    p.piece_l[i] = reinterpret_cast<float*>(at += l.piece_o[i]);
+    p.whole_o[i] = reinterpret_cast<float*>(at += l.piece_l[i]);
+    p.whole_l[i] = reinterpret_cast<float*>(at += l.whole_o[i]);
+    at += l.whole_l[i];
+  }
   p.status = fa_host::status_word(dev);
   if (!p.status) return FA_ERR_LAUNCH;
-  return d == 64 ? launch<64>(mk, mv, p, 2 * sms, rows, stream) : launch<128>(mk, mv, p, 2 * sms, rows, stream);
+  const Caches c = {k_cache, v_cache, strides, d, page_size, Hk, n_pages};
+  return d == 64 ? launch<64>(c, p, sms, rows, stream) : launch<128>(c, p, sms, rows, stream);
 }
 
 }  // namespace
@@ -165,10 +224,12 @@ int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
 extern "C" {
 
 size_t fa_paged_workspace_bytes(int B, int H, int Hk, int T, int d, int prefix_len) {
-  if (B <= 0 || H <= 0 || Hk <= 0 || H % Hk != 0 || T <= 0 || (d != 64 && d != 128) || prefix_len < 0) return 0;
+  if (B <= 0 || H <= 0 || Hk <= 0 || H % Hk != 0 || T <= 0 || (d != 64 && d != 128) || prefix_len < 0 ||
+      prefix_len > kMaxKeys)
+    return 0;
   int dev = -1, sms = 0;
   if (fa_host::current_device(&dev, &sms) != FA_OK) sms = 148;
-  return layout(B, H, T, d, prefix_len > 0, sms).bytes();
+  return layout(B, H, Hk, T, d, prefix_len, sms).bytes();
 }
 
 int fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, const int* block_table,

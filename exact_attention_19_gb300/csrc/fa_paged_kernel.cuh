@@ -8,16 +8,17 @@
 // position len - fresh + t and sees the own keys its window reaches, and every
 // prefix key at or before it.
 //
-// Schedule.  A work unit is one block of rows against one tile of keys.  All
-// units of a call form one line: first the prefix (its row blocks run over the
-// batch's rows of a K/V head, so its K/V is read once for the batch and not
-// once per sequence), then the sequences' own keys.  CTA c takes units
-// [c W / P, (c + 1) W / P): equal shares whatever the lengths, computed on the
-// device from the lengths there, so the host needs none of them and a captured
-// launch stays right as the sequences grow.  A CTA that holds all units of a
-// row block writes its output; else it writes its part (O normalised by its
-// own sum, and L, the base-2 log of that sum) and fa_paged_merge_kernel joins
-// the parts:  L = log2 sum 2^L_i,  O = sum 2^(L_i - L) O_i.
+// Schedule.  A work unit is one block of rows against one tile of 64 keys; a
+// launch covers either the sequences' own keys (row blocks of one sequence and
+// K/V head) or the shared prefix (row blocks over all the batch's rows of a K/V
+// head, so its K/V is read once for the batch and not once per sequence).  The
+// units of a launch form one line and CTA c takes [c W / P, (c + 1) W / P):
+// equal shares whatever the lengths, computed on the device from the lengths
+// there, so the host needs none of them and a captured launch stays right as
+// the sequences grow.  A CTA that holds all units of a row block writes its
+// output; else it writes its part (O normalised by its own sum, and L, the
+// base-2 log of that sum) and fa_paged_merge_kernel joins the parts:
+//   L = log2 sum 2^L_i,  O = sum 2^(L_i - L) O_i.
 #pragma once
 
 #include <cstdint>
@@ -46,11 +47,15 @@ struct PagedParams {
   int prefix_len;           // 0: no prefix
   int left, right;          // own window, -1 = open
   float scale_log2;         // scale * log2(e)
-  long long* plan;          // [0] units, [1] CTAs with work, [2 + b] first own unit of sequence b, [2 + B] units
-  float* piece_o;           // [2 * grid, row block, D] parts of the row blocks a CTA shares with others
-  float* piece_l;           // [2 * grid, row block]
-  float* whole_o;           // [2, B * H * T, D] with a prefix: row blocks one CTA finished (0 prefix, 1 own)
-  float* whole_l;           // [2, B * H * T]
+  long long* plan;          // own units: [0] units, [1] CTAs with work, [2 + b] first unit of sequence b
+  long long prefix_units;   // prefix units and the CTAs they are shared among
+  long long prefix_ctas;
+  // [0] own keys, [1] prefix: parts of row blocks that CTAs share, two per CTA ([2 * CTAs, row block, D]), and
+  // with a prefix the row blocks that one CTA finished ([B * H * T, D])
+  float* piece_o[2];
+  float* piece_l[2];
+  float* whole_o[2];
+  float* whole_l[2];
   unsigned int* status;
 };
 
@@ -81,40 +86,44 @@ __device__ __forceinline__ int row_prefix_keys(const PagedParams& p, const SeqKe
   return (t < s.fresh && s.len - s.fresh + t >= 0) ? p.prefix_len : 0;
 }
 
+constexpr int kPagedTile = 64;           // keys of a unit
+constexpr long long kPagedMinUnits = 2;  // units a CTA takes at least
+
+__host__ __device__ __forceinline__ long long paged_ctas(long long grid, long long units) {
+  const long long most = units / kPagedMinUnits;
+  return most < 1 ? 1 : (most < grid ? most : grid);
+}
+__device__ __forceinline__ long long cta_start(long long units, long long ctas, long long c) { return c * units / ctas; }
+__device__ __forceinline__ long long cta_of(long long units, long long ctas, long long x) {
+  return ((x + 1) * ctas - 1) / units;
+}
+__host__ __device__ __forceinline__ int own_blocks(int rows, int rb) { return (rows + rb - 1) / rb; }
+__host__ __device__ __forceinline__ int prefix_blocks(int B, int rows, int rb) {
+  return static_cast<int>((static_cast<long long>(B) * rows + rb - 1) / rb);
+}
+__host__ __device__ __forceinline__ int prefix_tiles(int prefix_len) { return (prefix_len + kPagedTile - 1) / kPagedTile; }
+
 // A row block against the tiles of its keys that this CTA holds.
 struct PagedWalk {
   long long g, gend;  // first unit of the current segment part, end of the CTA's units
-  bool own;           // prefix or own keys
-  int b, hk, rb;      // sequence (own), K/V head, row block
+  int b, hk, rb;      // sequence (own keys), K/V head, row block
   int tile0, n;       // first key tile of the row block and their number
   int j, jend;        // the part of them this CTA holds
   int lo, hi;         // keys that any row of the segment may see
 };
 
-template <int RB, int TILE>
+template <int RB, bool PREFIX>
 struct PagedSchedule {
-  static __device__ __forceinline__ int own_blocks(const PagedParams& p) { return (p.rows + RB - 1) / RB; }
-  static __device__ __forceinline__ int prefix_blocks(const PagedParams& p) {
-    return static_cast<int>((static_cast<long long>(p.B) * p.rows + RB - 1) / RB);
+  static __device__ __forceinline__ int blocks(const PagedParams& p) {
+    return PREFIX ? prefix_blocks(p.B, p.rows, RB) : own_blocks(p.rows, RB);
   }
-  static __device__ __forceinline__ int prefix_tiles(const PagedParams& p) { return (p.prefix_len + TILE - 1) / TILE; }
-  static __device__ __forceinline__ long long prefix_units(const PagedParams& p) {
-    return p.prefix_len > 0 ? static_cast<long long>(p.Hk) * prefix_blocks(p) * prefix_tiles(p) : 0ll;
-  }
-  static __device__ __forceinline__ long long cta_start(long long units, long long ctas, long long c) {
-    return c * units / ctas;
-  }
-  static __device__ __forceinline__ long long cta_of(long long units, long long ctas, long long x) {
-    return ((x + 1) * ctas - 1) / units;
-  }
-
   static __device__ __forceinline__ void enter_seq(const PagedParams& p, PagedWalk& w) {
     for (;; ++w.b) {  // w.g < w.gend, so a sequence with units follows
       const SeqKeys s = seq_keys(p, w.b);
       w.lo = s.lo;
       w.hi = s.hi;
-      w.tile0 = s.lo / TILE;
-      w.n = tiles_of(s.lo, s.hi, TILE);
+      w.tile0 = s.lo / kPagedTile;
+      w.n = tiles_of(s.lo, s.hi, kPagedTile);
       if (w.n > 0 || w.b + 1 >= p.B) return;
     }
   }
@@ -122,50 +131,71 @@ struct PagedSchedule {
     w.jend = static_cast<int>(min(static_cast<long long>(w.n), w.j + (w.gend - w.g)));
   }
   // first segment of the units [g, gend), g < gend; b, b_unit: the sequence that holds g and its first
-  // unit (own units only)
+  // unit (own keys)
   static __device__ __forceinline__ void begin(const PagedParams& p, PagedWalk& w, long long g, long long gend, int b,
                                                long long b_unit) {
     w.g = g;
     w.gend = gend;
-    const long long pu = prefix_units(p);
-    w.own = g >= pu;
-    if (!w.own) {
-      w.n = prefix_tiles(p);
+    w.b = b;
+    if constexpr (PREFIX) {
+      w.n = prefix_tiles(p.prefix_len);
       w.tile0 = 0;
       w.lo = 0;
       w.hi = p.prefix_len;
-      const long long i = g / w.n;
-      w.j = static_cast<int>(g - i * w.n);
-      w.hk = static_cast<int>(i / prefix_blocks(p));
-      w.rb = static_cast<int>(i % prefix_blocks(p));
-      w.b = 0;
     } else {
-      w.b = b;
       enter_seq(p, w);
-      const long long i = (g - b_unit) / w.n;
-      w.j = static_cast<int>((g - b_unit) - i * w.n);
-      w.hk = static_cast<int>(i / own_blocks(p));
-      w.rb = static_cast<int>(i % own_blocks(p));
     }
+    const long long i = (g - b_unit) / w.n;
+    w.j = static_cast<int>((g - b_unit) - i * w.n);
+    w.hk = static_cast<int>(i / blocks(p));
+    w.rb = static_cast<int>(i % blocks(p));
     part(w);
   }
-  // j0: the part's first tile as begin or next left it
-  static __device__ __forceinline__ bool next(const PagedParams& p, PagedWalk& w, int j0) {
-    w.g += w.jend - j0;
+  // the segment after the current one, w.j still its first tile; false: none left
+  static __device__ __forceinline__ bool next(const PagedParams& p, PagedWalk& w) {
+    w.g += w.jend - w.j;
     if (w.g >= w.gend) return false;
     w.j = 0;
-    const int blocks = w.own ? own_blocks(p) : prefix_blocks(p);
-    if (++w.rb == blocks) {
+    if (++w.rb == blocks(p)) {
       w.rb = 0;
       if (++w.hk == p.Hk) {
         w.hk = 0;
-        if (w.own) ++w.b;
-        w.own = true;
-        enter_seq(p, w);
+        ++w.b;
+        if (!PREFIX) enter_seq(p, w);
       }
     }
     part(w);
     return true;
+  }
+  // page indices of the segment's keys
+  static __device__ __forceinline__ const int* pages(const PagedParams& p, const PagedWalk& w) {
+    return PREFIX ? p.prefix_pages : p.table + static_cast<long long>(w.b) * p.max_pages;
+  }
+  // The row of [B * H * T] that row r of the segment's block is (-1: none) and the keys [lo, hi) it sees; a row
+  // that does not exist needs no mask, as nothing of it is stored.
+  static __device__ __forceinline__ long long row(const PagedParams& p, const PagedWalk& w, int r, int& lo, int& hi) {
+    int b = w.b, rr = w.rb * RB + r;
+    bool there = rr < p.rows;
+    if constexpr (PREFIX) {
+      b = rr / p.rows;
+      rr -= b * p.rows;
+      there = b < p.B;
+    }
+    lo = 0;
+    hi = 0x7fffffff;
+    if (!there) return -1;
+    const SeqKeys s = seq_keys(p, b);
+    if constexpr (PREFIX) hi = row_prefix_keys(p, s, rr % p.T);
+    else row_own_keys(p, s, rr % p.T, lo, hi);
+    return (static_cast<long long>(b) * p.Hk + w.hk) * p.rows + rr;
+  }
+  // where a row block's result goes: 0 the output, 1 whole_*, 2 piece_* (row = of the piece)
+  static __device__ __forceinline__ int target(const PagedParams& p, const PagedWalk& w, long long first_g, int r,
+                                               long long& row) {
+    if (w.jend - w.j == w.n) return p.prefix_len > 0 ? 1 : 0;
+    const long long slot = 2ll * blockIdx.x + (w.g == first_g ? 0 : 1);
+    row = slot * RB + r;
+    return 2;
   }
 };
 
@@ -227,82 +257,85 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Block-wide: units of the call, the CTA's share of them and the sequence its
-// first own unit lies in.  CTA 0 leaves the plan for the merge kernel.
-template <int RB, int TILE, int THREADS>
-__device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scratch /* shared, THREADS / 32 + 4 */,
-                                            long long min_units, PagedWalk& w) {
-  using S = PagedSchedule<RB, TILE>;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kWarps = THREADS / 32;
-  const long long per = static_cast<long long>(p.Hk) * S::own_blocks(p);
-  const long long pu = S::prefix_units(p);
-  long long total = pu, ctas = 1, g = 0, gend = 0;
-  // pass 0 sums, pass 1 finds the sequence that holds unit g
-  for (int pass = 0; pass < 2; ++pass) {
-    long long run = pu;
-    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
-      const int b = b0 + static_cast<int>(threadIdx.x);
-      long long mine = 0;
-      if (b < p.B) {
-        const SeqKeys s = seq_keys(p, b);
-        mine = per * tiles_of(s.lo, s.hi, TILE);
-        if (pass == 0 && blockIdx.x == 0 && __ldg(p.lens + b) > p.capacity) atomicOr(p.status, kPagedPage);
-      }
-      long long incl = mine;
+// Block-wide: the CTA's share of the launch's units, as the walk's first
+// segment; false when it has none.  For own keys the units come from the
+// lengths, and CTA 0 leaves the plan for the merge kernel.
+template <int RB, bool PREFIX, int THREADS>
+__device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scratch /* shared, THREADS / 32 + 2 */,
+                                            PagedWalk& w) {
+  using S = PagedSchedule<RB, PREFIX>;
+  if constexpr (PREFIX) {
+    if (static_cast<long long>(blockIdx.x) >= p.prefix_ctas) return false;
+    const long long g = cta_start(p.prefix_units, p.prefix_ctas, blockIdx.x);
+    S::begin(p, w, g, cta_start(p.prefix_units, p.prefix_ctas, blockIdx.x + 1ll), 0, 0);
+    return true;
+  } else {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kWarps = THREADS / 32;
+    const long long per = static_cast<long long>(p.Hk) * S::blocks(p);
+    long long g = 0, gend = 0;
+    // pass 0 sums, pass 1 finds the sequence that holds unit g
+    for (int pass = 0; pass < 2; ++pass) {
+      long long run = 0;
+      for (int b0 = 0; b0 < p.B; b0 += THREADS) {
+        const int b = b0 + static_cast<int>(threadIdx.x);
+        long long mine = 0;
+        if (b < p.B) {
+          const SeqKeys s = seq_keys(p, b);
+          mine = per * tiles_of(s.lo, s.hi, kPagedTile);
+          if (pass == 0 && blockIdx.x == 0 && __ldg(p.lens + b) > p.capacity) atomicOr(p.status, kPagedPage);
+        }
+        long long incl = mine;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += up;
-      }
-      if (lane == 31) scratch[warp] = incl;
-      __syncthreads();
-      long long before = run, all = 0;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += up;
+        }
+        if (lane == 31) scratch[warp] = incl;
+        __syncthreads();
+        long long before = run, all = 0;
 #pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        if (i < warp) before += scratch[i];
-        all += scratch[i];
+        for (int i = 0; i < kWarps; ++i) {
+          if (i < warp) before += scratch[i];
+          all += scratch[i];
+        }
+        const long long first = before + incl - mine;
+        if (pass == 0 && blockIdx.x == 0 && b < p.B) p.plan[2 + b] = first;
+        if (pass == 1 && mine > 0 && first <= g && g < first + mine) {
+          scratch[kWarps] = b;
+          scratch[kWarps + 1] = first;
+        }
+        run += all;
+        __syncthreads();
       }
-      const long long first = before + incl - mine;
-      if (pass == 0 && blockIdx.x == 0 && b < p.B) p.plan[2 + b] = first;
-      if (pass == 1 && mine > 0 && first <= g && g < first + mine) {
-        scratch[kWarps] = b;
-        scratch[kWarps + 1] = first;
+      if (pass == 0) {
+        const long long ctas = paged_ctas(gridDim.x, run);
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+          p.plan[0] = run;
+          p.plan[1] = ctas;
+          p.plan[2 + p.B] = run;
+        }
+        if (static_cast<long long>(blockIdx.x) >= ctas) return false;
+        g = cta_start(run, ctas, blockIdx.x);
+        gend = cta_start(run, ctas, blockIdx.x + 1ll);
+        if (g >= gend) return false;
       }
-      run += all;
-      __syncthreads();
     }
-    if (pass == 0) {
-      total = run;
-      ctas = min(static_cast<long long>(gridDim.x), max(1ll, total / min_units));
-      if (blockIdx.x == 0 && threadIdx.x == 0) {
-        p.plan[0] = total;
-        p.plan[1] = ctas;
-        p.plan[2 + p.B] = total;
-      }
-      if (static_cast<long long>(blockIdx.x) >= ctas) return false;
-      g = S::cta_start(total, ctas, blockIdx.x);
-      gend = S::cta_start(total, ctas, blockIdx.x + 1);
-      if (g >= gend) return false;
-      if (g < pu) break;
-    }
+    S::begin(p, w, g, gend, static_cast<int>(scratch[kWarps]), scratch[kWarps + 1]);
+    return true;
   }
-  S::begin(p, w, g, gend, g < pu ? 0 : static_cast<int>(scratch[kWarps]), g < pu ? 0 : scratch[kWarps + 1]);
-  return true;
 }
-
-constexpr long long kPagedMinUnits = 2;  // units a CTA takes at least
 
 template <int D>
 __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const PagedParams p) {
   using C = PagedCfg<D>;
-  using S = PagedSchedule<C::kRows, C::kTile>;
+  using S = PagedSchedule<C::kRows, false>;
   constexpr int kNT = D / 8;   // 8-column tiles of O
   constexpr int kKT = D / 16;  // 16-deep steps of Q K^T
   extern __shared__ uint8_t smem_raw[];
-  __shared__ long long scratch[C::kWarps + 4];
+  __shared__ long long scratch[C::kWarps + 2];
   const uint32_t raw_addr = smem_addr(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* const sbase = smem_raw + (base - raw_addr);
@@ -320,38 +353,34 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     mbar_init_fence();
   }
   PagedWalk w;
-  if (!paged_share<C::kRows, C::kTile, C::kThreads>(p, scratch, kPagedMinUnits, w)) return;
-  const PagedWalk first = w;
+  if (!paged_share<C::kRows, false, C::kThreads>(p, scratch, w)) return;
+  const long long first_g = w.g;
   __syncthreads();
 
   // ---- this warp's stream of TMA items -----------------------------------
   // The fetch side walks the same segments ahead of the products: K then V of
   // every 16-key piece in range, one page index read ahead.
   PagedWalk f = w;
-  int f_j0 = w.j;
+  int f_j = w.j;  // next tile of f
   int f_k0 = 0, f_hk = 0, f_page = 0, n_k0 = 0, n_hk = 0, n_page = 0;
   bool f_more = true, n_more = true, f_is_v = false;
   int f_slot = 0;  // ring slot of the next item
   auto seek = [&]() {  // n_*: the next 16-key piece of this warp, n_more false when none is left
     for (;;) {
-      while (f.j < f.jend) {
-        const int k0 = (f.tile0 + f.j) * C::kTile + warp * C::kKeys;
+      while (f_j < f.jend) {
+        const int k0 = (f.tile0 + f_j++) * C::kTile + warp * C::kKeys;
         if (k0 < f.hi && k0 + C::kKeys > f.lo) {
-          const int pi = k0 >> p.page_shift;
-          const int* src = f.own ? p.table + static_cast<long long>(f.b) * p.max_pages + pi : p.prefix_pages + pi;
-          n_page = __ldg(src);
+          n_page = __ldg(S::pages(p, f) + (k0 >> p.page_shift));
           n_k0 = k0;
           n_hk = f.hk;
-          ++f.j;
           return;
         }
-        ++f.j;
       }
-      if (!S::next(p, f, f_j0)) {
+      if (!S::next(p, f)) {
         n_more = false;
         return;
       }
-      f_j0 = 0;
+      f_j = f.j;
     }
   };
   auto take = [&]() {  // the piece sought becomes the one being fetched; seek the one after it
@@ -409,35 +438,16 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
 
   const float NEG_INF = -__int_as_float(0x7f800000);
   const int g8 = lane >> 2, q4 = lane & 3;  // this thread's rows g8, g8 + 8 and columns 2 q4, 2 q4 + 1
-  bool more = true;
-  int j0 = w.j;
-  while (more) {
+  do {
     // ---- the segment's rows ------------------------------------------------
-    const bool own = w.own;
     int lo[2], hi[2];
     uint32_t qf[kKT][4];
     long long out_row[2];  // row in [B * H * T], -1: none
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = w.rb * C::kRows + g8 + 8 * i;
-      int b = w.b, rr = r;
-      bool there = r < p.rows;
-      if (!own) {
-        b = r / p.rows;
-        rr = r - b * p.rows;
-        there = b < p.B;
-      }
-      lo[i] = 0;
-      hi[i] = 0x7fffffff;  // a row of the block that does not exist needs no mask: nothing of it is stored
-      out_row[i] = -1;
-      const uint32_t* src = nullptr;
-      if (there) {
-        const SeqKeys s = seq_keys(p, b);
-        if (own) row_own_keys(p, s, rr % p.T, lo[i], hi[i]);
-        else hi[i] = row_prefix_keys(p, s, rr % p.T);
-        out_row[i] = (static_cast<long long>(b) * p.Hk + w.hk) * p.rows + rr;
-        src = reinterpret_cast<const uint32_t*>(p.q + out_row[i] * D);
-      }
+      out_row[i] = S::row(p, w, g8 + 8 * i, lo[i], hi[i]);
+      const bool there = out_row[i] >= 0;
+      const uint32_t* const src = reinterpret_cast<const uint32_t*>(p.q + (there ? out_row[i] : 0) * D);
 #pragma unroll
       for (int kk = 0; kk < kKT; ++kk) {
         qf[kk][i] = there ? __ldg(src + kk * 8 + q4) : 0u;
@@ -588,32 +598,28 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     const int col = (warp & 1) * (D / 2) + (warp >> 1) * (D / 4) + 2 * q4;
 
     // ---- write the row block, or this CTA's part of it ---------------------
-    const bool whole = w.jend - w.j == w.n;
-    const long long slot = w.g == first.g ? 2ll * blockIdx.x : 2ll * blockIdx.x + 1;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (out_row[i] < 0) continue;
       const float inv = l[i] > 0.f ? 1.0f / l[i] : 0.f;
       const float lb = l[i] > 0.f ? m[i] + __log2f(l[i]) : NEG_INF;
-      if (whole && p.prefix_len == 0) {
-        uint16_t* const dst = p.out + out_row[i] * D + col;
+      long long row = out_row[i];
+      const int to = S::target(p, w, first_g, g8 + 8 * i, row);
+      if (to == 0) {
+        uint16_t* const dst = p.out + row * D + col;
 #pragma unroll
         for (int n = 0; n < kNT / 4; ++n)
           *reinterpret_cast<uint32_t*>(dst + n * 8) = pack_bf16(fin[n][2 * i] * inv, fin[n][2 * i + 1] * inv);
-        if (col == 0) p.lse[out_row[i]] = lb * 0.69314718055994530942f;
+        if (col == 0) p.lse[row] = lb * 0.69314718055994530942f;
       } else {
-        const long long prow = whole ? (own ? static_cast<long long>(p.B) * p.Hk * p.rows : 0ll) + out_row[i]
-                                     : slot * C::kRows + g8 + 8 * i;
-        float* const dst = (whole ? p.whole_o : p.piece_o) + prow * D + col;
+        float* const dst = (to == 1 ? p.whole_o[0] : p.piece_o[0]) + row * D + col;
 #pragma unroll
         for (int n = 0; n < kNT / 4; ++n)
           *reinterpret_cast<float2*>(dst + n * 8) = make_float2(fin[n][2 * i] * inv, fin[n][2 * i + 1] * inv);
-        if (col == 0) (whole ? p.whole_l : p.piece_l)[prow] = lb;
+        if (col == 0) (to == 1 ? p.whole_l[0] : p.piece_l[0])[row] = lb;
       }
     }
-    more = S::next(p, w, j0);
-    j0 = 0;
-  }
+  } while (S::next(p, w));
   if (!ok) {  // let every copy in flight land before the CTA's shared memory goes
     for (int i = consumed; i < issued; ++i)
       mbar_wait(bars + 8 * (i % C::kRing), static_cast<uint32_t>(i / C::kRing) & 1u, nullptr);
@@ -626,9 +632,11 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
 // four warps per row: the warps take the parts in turn, each lane D / 32
 // columns, and meet in shared memory.
 // ---------------------------------------------------------------------------
-template <int D, int RB, int TILE>
+// RB: rows of an own row block; prefix row blocks have kPrefixRows.
+constexpr int kPrefixRows = 128;
+
+template <int D, int RB>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p) {
-  using S = PagedSchedule<RB, TILE>;
   constexpr int kPer = D / 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long row = blockIdx.x;
@@ -636,45 +644,42 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
   const int rr = static_cast<int>(row - bh * p.rows), hk = static_cast<int>(bh % p.Hk), b = static_cast<int>(bh / p.Hk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float NEG_INF = -__int_as_float(0x7f800000);
-  const long long units = p.plan[0], ctas = p.plan[1];
-  const long long all_rows = static_cast<long long>(p.B) * p.Hk * p.rows;
 
-  // CTAs [c0, c1] that hold the row's own keys, [d0, d1] its prefix keys (empty: c0 > c1)
+  // CTAs [c0, c1] that hold the row's own keys, [d0, d1] its prefix keys (c0 > c1: none)
+  const long long units = p.plan[0], ctas = p.plan[1];
   const long long u0 = p.plan[2 + b];
-  const int blocks = S::own_blocks(p);
+  const int blocks = own_blocks(p.rows, RB);
   const long long n = (p.plan[3 + b] - u0) / (static_cast<long long>(p.Hk) * blocks);
   const long long x0 = u0 + (static_cast<long long>(hk) * blocks + rr / RB) * n;
   long long c0 = 1, c1 = 0, d0 = 1, d1 = 0, y0 = 0;
   if (n > 0) {
-    c0 = S::cta_of(units, ctas, x0);
-    c1 = S::cta_of(units, ctas, x0 + n - 1);
+    c0 = cta_of(units, ctas, x0);
+    c1 = cta_of(units, ctas, x0 + n - 1);
   }
   const long long pr = static_cast<long long>(b) * p.rows + rr;  // row among the K/V head's prefix rows
   if (p.prefix_len > 0) {
-    const int nt = S::prefix_tiles(p);
-    y0 = (static_cast<long long>(hk) * S::prefix_blocks(p) + pr / RB) * nt;
-    d0 = S::cta_of(units, ctas, y0);
-    d1 = S::cta_of(units, ctas, y0 + nt - 1);
+    const int nt = prefix_tiles(p.prefix_len);
+    y0 = (static_cast<long long>(hk) * prefix_blocks(p.B, p.rows, kPrefixRows) + pr / kPrefixRows) * nt;
+    d0 = cta_of(p.prefix_units, p.prefix_ctas, y0);
+    d1 = cta_of(p.prefix_units, p.prefix_ctas, y0 + nt - 1);
   } else if (n > 0 && c0 == c1) {
     return;  // written by the one CTA that held it
   }
   const int n_own = static_cast<int>(c1 - c0 + 1), n_all = n_own + static_cast<int>(d1 - d0 + 1);
   // part i of the row: O and L
   auto part = [&](int i, const float*& po, const float*& pl) {
-    const bool own = i < n_own;
-    const long long a = own ? c0 : d0, z = own ? c1 : d1, start = own ? x0 : y0;
-    if (a == z) {
-      const long long at = (own ? all_rows : 0ll) + row;
-      po = p.whole_o + at * D;
-      pl = p.whole_l + at;
-      return;
+    const int pre = i < n_own ? 0 : 1;
+    const long long a = pre ? d0 : c0, z = pre ? d1 : c1, start = pre ? y0 : x0;
+    long long at = row;
+    if (a != z) {
+      const long long c = a + (pre ? i - n_own : i);
+      // a CTA's first segment is its piece 0; the row block is that one unless it starts inside the CTA
+      const long long first = pre ? cta_start(p.prefix_units, p.prefix_ctas, c) : cta_start(units, ctas, c);
+      const long long slot = 2 * c + (first >= start ? 0 : 1);
+      at = pre ? slot * kPrefixRows + pr % kPrefixRows : slot * RB + rr % RB;
     }
-    const long long c = a + (own ? i : i - n_own);
-    // a CTA's first segment is its part 0; the row block is that one unless it starts inside the CTA
-    const long long slot = 2 * c + (S::cta_start(units, ctas, c) >= start ? 0 : 1);
-    const long long at = slot * RB + (own ? rr % RB : static_cast<int>(pr % RB));
-    po = p.piece_o + at * D;
-    pl = p.piece_l + at;
+    po = (a == z ? p.whole_o[pre] : p.piece_o[pre]) + at * D;
+    pl = (a == z ? p.whole_l[pre] : p.piece_l[pre]) + at;
   };
   float mx = NEG_INF, sum = 0.f, acc[kPer];
 #pragma unroll

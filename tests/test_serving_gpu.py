@@ -284,6 +284,10 @@ def paged_case(fa, seed, B, H, Hk, T, d, page, lens, new=None, window=(-1, 0), t
     (2, 2, 1, 70, 16, [3, 64], None),                 # shorter than the new rows: some hold no token
     (70, 2, 1, 1, 16, [i * 3 % 50 for i in range(70)], None),
     (150, 1, 1, 1, 16, [i % 7 for i in range(150)], None),
+    (60, 24, 1, 1, 32, [i * 5 % 200 for i in range(60)], None),
+    (250, 20, 1, 1, 16, [i * 7 % 90 for i in range(250)], None),  # several sequences to a CTA
+    (3, 4, 1, 300, 64, [300, 640, 1000], [300, 7, 299]),          # blocks of rows that see part of the keys
+    (1, 1, 1, 600, 256, [600], None),
 ])
 def test_paged(fa, B, H, Hk, T, d, page, lens, new):
     paged_case(fa, 1 + B, B, H, Hk, T, d, page, lens, new)
@@ -297,6 +301,8 @@ def test_paged(fa, B, H, Hk, T, d, page, lens, new):
     (2, 2, 2, 6, 64, 32, [100, 6], (10, 2)),
     (2, 2, 2, 9, 128, 16, [100, 5], (-1, -1)),        # every cached key, more rows than keys
     (2, 4, 1, 40, 64, 128, [500, 41], (64, -1)),
+    (2, 2, 1, 200, 128, 32, [700, 200], (30, 0)),     # rows of different blocks see different tiles
+    (1, 2, 1, 150, 64, 16, [400], (5, 70)),
     (1, 2, 1, 2, 64, 16, [50], (2 ** 31 - 1, 2 ** 31 - 1)),
 ])
 def test_paged_windows(fa, B, H, Hk, T, d, page, lens, window, token_major):
@@ -313,6 +319,8 @@ def test_paged_windows(fa, B, H, Hk, T, d, page, lens, window, token_major):
     (4, 2, 1, 3, 16, 77, [3, 0, 2, 50], [3, 0, 3, 2], True),   # an empty entry; a row before its sequence
     (40, 4, 1, 1, 256, 700, [1 + i * 7 % 90 for i in range(40)], None, False),
     (33, 16, 2, 2, 16, 257, [2 + i % 5 for i in range(33)], None, False),
+    (3, 40, 2, 3, 16, 90, [3, 30, 70], None, False),           # 60 own rows, 180 prefix rows of a K/V head
+    (2, 4, 2, 100, 32, 200, [100, 140], [100, 3], True),       # a chunk behind a prefix
 ])
 def test_prefix(fa, d, B, H, Hk, T, page, prefix_len, lens, new, token_major):
     paged_case(fa, 21 + B, B, H, Hk, T, d, page, lens, new, (-1, 0), token_major, prefix_len)
