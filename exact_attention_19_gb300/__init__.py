@@ -21,6 +21,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 
 __all__ = [
     "FaError", "STATUS", "NOALLOC_SCRATCH_BYTES", "library_path", "load",
@@ -185,7 +186,7 @@ def fa_bwd_workspace_bytes(B, H, Nq) -> int:
 
 def _longs(values):
     """A host array of long long for a strides argument (None stays None)."""
-    return None if values is None else (ctypes.c_longlong * len(values))(*values)
+    return None if values is None else struct.pack(f"{len(values)}q", *values)
 
 
 def fa_rope(q, k, q_out, k_out, inv_freq, positions, position_stride, offset, strides, B, H, Hk, N, d, rot, mag,
@@ -372,302 +373,14 @@ def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
     return dq, dk, dv
 
 
-# ---------------------------------------------------------------------------
-# rotary positions
-# ---------------------------------------------------------------------------
-def rope_freqs(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
-               original_len: int = 4096, fast: float = 32.0, slow: float = 1.0, device="cuda"):
-    """(inv_freq, mag) for ``rope`` and ``kv_append``: fp64 [rot / 2] radians per position, and the factor on
-    the rotated part.
-
-    ``scaling`` for contexts ``factor`` times longer than trained on:
-    ``"linear"``: every frequency divided by ``factor``;
-    ``"base"``: the base stretched by factor^(rot / (rot - 2)), which divides the slowest frequency by
-    ``factor`` and keeps the fastest;
-    ``"by_parts"``: pairs that turn at least ``fast`` times within ``original_len`` positions keep their
-    frequency, pairs below ``slow`` turns are divided by ``factor``, with a linear ramp in the number of turns
-    between, and mag = 0.1 ln(factor) + 1.
-    """
-    import torch
-
-    if rot < 2 or rot % 2:
-        raise ValueError("rot must be a positive even number")
-    if not (math.isfinite(base) and base > 0 and math.isfinite(factor) and factor >= 1):
-        raise ValueError("base must be finite and > 0, factor finite and >= 1")
-    expo = -torch.arange(0, rot, 2, dtype=torch.float64) / rot
-    if scaling == "base":
-        if rot < 4:
-            raise ValueError("a stretched base needs rot >= 4")
-        base = base * factor ** (rot / (rot - 2))
-    w = torch.full_like(expo, base).pow(expo)
-    mag = 1.0
-    if scaling == "linear":
-        w = w / factor
-    elif scaling == "by_parts":
-        if not (original_len > 0 and fast > slow >= 0):
-            raise ValueError("by_parts needs original_len > 0 and fast > slow >= 0")
-        turns = original_len * w / (2.0 * math.pi)
-        keep = ((turns - slow) / (fast - slow)).clamp(0.0, 1.0)
-        w = w * keep + (w / factor) * (1.0 - keep)
-        mag = 0.1 * math.log(factor) + 1.0
-    elif scaling not in (None, "base"):
-        raise ValueError(f"unknown scaling {scaling!r}")
-    return w.to(device), mag
+_SERVING = ("rope_freqs", "rope", "rope_bwd", "kv_append", "fwd_paged", "fwd_prefix")
 
 
-def _empty(shape, dtype, like, stream):
-    """Memory that ``stream`` may write at once: from its own allocator pool when it is not the current stream."""
-    import torch
+def __getattr__(name):
+    """The torch entry points of ``serving`` are loaded at their first use, like torch itself."""
+    if name in _SERVING:
+        from . import serving
 
-    if stream is None or stream == torch.cuda.current_stream(like.device):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _handle(stream, like):
-    import torch
-
-    return (torch.cuda.current_stream(like.device) if stream is None else stream).cuda_stream
-
-
-def _need(name, t, dtype, dim=None):
-    import torch
-
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
-    if dim is not None and t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions, has {t.dim()}")
-
-
-def _strides3(name, t):
-    """Strides of a 4-D view's first three dimensions; a dimension of size 1 gets a stride that is valid anywhere."""
-    n0, n1, n2, d = t.shape
-    s0, s1, s2, s3 = t.stride()
-    if s3 != 1 and t.numel():
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return (s0 if n0 > 1 else d, s1 if n1 > 1 else d, s2 if n2 > 1 else d)
-
-
-def _rope_like(name, t, out, stream):
-    """``out`` or a new contiguous tensor shaped like the bf16 [B, heads, N, d] view ``t``."""
-    import torch
-
-    if out is None:
-        return _empty(t.shape, torch.bfloat16, t, stream)
-    _need(name, out, torch.bfloat16, 4)
-    if out.shape != t.shape:
-        raise ValueError(f"{name} must be shaped like its input, {tuple(t.shape)}")
-    return out
-
-
-def _rope(where, backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream):
-    import torch
-
-    _need("q", q, torch.bfloat16, 4)
-    B, H, N, d = q.shape
-    _need("inv_freq", inv_freq, torch.float64, 1)
-    if not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be contiguous")
-    Hk = 0
-    if k is not None:
-        _need("k", k, torch.bfloat16, 4)
-        Hk = k.shape[1]
-        if k.shape[0] != B or k.shape[2] != N or k.shape[3] != d or Hk == 0:
-            raise ValueError(f"shape mismatch: q{tuple(q.shape)} k{tuple(k.shape)}")
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    p_stride = 0
-    if positions is not None:
-        _need("positions", positions, torch.int32)
-        if positions.shape == (B, N):
-            p_stride = positions.stride(0) if B > 1 else 0
-        elif positions.shape != (N,):
-            raise ValueError(f"positions must be [{B}, {N}] or [{N}], is {tuple(positions.shape)}")
-        if N > 1 and positions.stride(-1) != 1:
-            raise ValueError("positions must be contiguous along the last dimension")
-    q_out = _rope_like("q_out", q, q_out, stream)
-    k_out = _rope_like("k_out", k, k_out, stream) if Hk else None
-    strides = None
-    if not (q.is_contiguous() and q_out.is_contiguous() and (not Hk or (k.is_contiguous() and k_out.is_contiguous()))):
-        none = (d, d, d)
-        strides = (_strides3("q", q) + (_strides3("k", k) if Hk else none) + _strides3("q_out", q_out) +
-                   (_strides3("k_out", k_out) if Hk else none))
-    st = fa_rope(q.data_ptr(), k.data_ptr() if Hk else None, q_out.data_ptr(), k_out.data_ptr() if Hk else None,
-                 inv_freq.data_ptr(), None if positions is None else positions.data_ptr(), p_stride, offset, strides,
-                 B, H, Hk, N, d, 2 * inv_freq.shape[0], mag, int(interleaved), backward, _handle(stream, q))
-    if st != 0:
-        raise FaError(st, where)
-    return q_out, k_out
-
-
-def rope(q, k, inv_freq, positions=None, offset: int = 0, interleaved: bool = False, mag: float = 1.0, q_out=None,
-         k_out=None, stream=None):
-    """(q, k) turned by their positions, ready for ``fwd``; ``k`` may be None and may have fewer heads.
-
-    q: [B, H, N, d], k: [B, Hk, N, d] CUDA bf16, d contiguous and the other strides free (multiples of 8
-    elements), so views of a packed projection need no copy; the outputs default to contiguous tensors and may
-    be the inputs themselves.  ``inv_freq``: fp64 [rot / 2] on the GPU (``rope_freqs``); the first rot elements
-    of a head turn, the others are copied.  ``positions``: int32 [B, N] or [N]; None: 0, 1, 2, ...;
-    ``offset`` is added.  ``interleaved``: pairs (2i, 2i + 1) instead of (i, i + rot / 2).  ``mag`` multiplies
-    the turned part.
-    """
-    return _rope("fa_rope", 0, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream)
-
-
-def rope_bwd(dq, dk, inv_freq, positions=None, offset: int = 0, interleaved: bool = False, mag: float = 1.0,
-             q_out=None, k_out=None, stream=None):
-    """Gradients of ``rope``'s inputs from those of its outputs (from ``bwd``): the transposed rotation, same
-    arguments; ``q_out`` and ``k_out`` may be views of a packed gradient."""
-    return _rope("fa_rope", 1, dq, dk, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream)
-
-
-# ---------------------------------------------------------------------------
-# the paged K/V cache
-# ---------------------------------------------------------------------------
-def _cache_args(k_cache, v_cache, block_table, seq_lens, new_lens, B, d):
-    """Checks shared by the cache's calls; the strides of both caches."""
-    import torch
-
-    _need("k_cache", k_cache, torch.bfloat16, 4)
-    _need("v_cache", v_cache, torch.bfloat16, 4)
-    if v_cache.shape != k_cache.shape or k_cache.shape[3] != d:
-        raise ValueError(f"shape mismatch: k_cache{tuple(k_cache.shape)} v_cache{tuple(v_cache.shape)}, d = {d}")
-    _need("block_table", block_table, torch.int32, 2)
-    _need("seq_lens", seq_lens, torch.int32, 1)
-    if block_table.shape[0] != B or not block_table.is_contiguous():
-        raise ValueError(f"block_table must be a contiguous [{B}, max_pages] tensor")
-    if seq_lens.shape[0] != B or not seq_lens.is_contiguous():
-        raise ValueError(f"seq_lens must be a contiguous [{B}] tensor")
-    if new_lens is not None:
-        _need("new_lens", new_lens, torch.int32, 1)
-        if new_lens.shape[0] != B or not new_lens.is_contiguous():
-            raise ValueError(f"new_lens must be a contiguous [{B}] tensor")
-    return _strides3("k_cache", k_cache) + _strides3("v_cache", v_cache)
-
-
-def kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq=None, new_lens=None, offset: int = 0,
-              interleaved: bool = False, mag: float = 1.0, q_out=None, stream=None):
-    """Put the new tokens' k (turned by position) and v into the paged cache and return their q, turned.
-
-    q: [B, H, T, d] or None; k, v: [B, Hk, T, d] CUDA bf16, d contiguous, other strides free.
-    k_cache, v_cache: [n_pages, Hk, page_size, d] views, page_size 16..256 (a power of two), d contiguous;
-    token-major pages are ``pages.transpose(1, 2)``.  block_table: int32 [B, max_pages].  seq_lens: int32 [B],
-    each sequence's cached tokens WITH the new ones; new_lens: int32 [B], how many of the T rows are tokens
-    (None: all).  Row t is the token at own position seq_lens - new_lens + t; its rotation uses ``offset`` + that
-    (``inv_freq`` None: no rotation).  Padding rows are not written (q_out included).  Asynchronous; a page index
-    outside the cache is skipped and reported by ``fa_fwd_status``.
-    """
-    import torch
-
-    _need("k", k, torch.bfloat16, 4)
-    _need("v", v, torch.bfloat16, 4)
-    B, Hk, T, d = k.shape
-    if v.shape != k.shape:
-        raise ValueError(f"shape mismatch: k{tuple(k.shape)} v{tuple(v.shape)}")
-    caches = _cache_args(k_cache, v_cache, block_table, seq_lens, new_lens, B, d)
-    if k_cache.shape[1] != Hk:
-        raise ValueError(f"the cache has {k_cache.shape[1]} heads, k has {Hk}")
-    H = 0
-    qs = os_ = (d, d, d)
-    if q is not None:
-        _need("q", q, torch.bfloat16, 4)
-        H = q.shape[1]
-        if q.shape[0] != B or q.shape[2] != T or q.shape[3] != d or H == 0:
-            raise ValueError(f"shape mismatch: q{tuple(q.shape)} k{tuple(k.shape)}")
-        q_out = _rope_like("q_out", q, q_out, stream)
-        qs, os_ = _strides3("q", q), _strides3("q_out", q_out)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    rot = 0
-    if inv_freq is not None:
-        _need("inv_freq", inv_freq, torch.float64, 1)
-        if not inv_freq.is_contiguous():
-            raise ValueError("inv_freq must be contiguous")
-        rot = 2 * inv_freq.shape[0]
-    st = fa_kv_append(q.data_ptr() if H else None, k.data_ptr(), v.data_ptr(), q_out.data_ptr() if H else None,
-                      k_cache.data_ptr(), v_cache.data_ptr(), inv_freq.data_ptr() if rot else None,
-                      block_table.data_ptr(), seq_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(),
-                      qs + _strides3("k", k) + _strides3("v", v) + os_ + caches, B, H, Hk, T, d, rot,
-                      k_cache.shape[0], k_cache.shape[2], block_table.shape[1], offset, mag, int(interleaved),
-                      _handle(stream, k))
-    if st != 0:
-        raise FaError(st, "fa_kv_append")
-    return q_out
-
-
-def _paged_args(q, k_cache, v_cache, block_table, seq_lens, new_lens, scale, out, lse, workspace, stream, prefix_len):
-    import torch
-
-    _need("q", q, torch.bfloat16, 4)
-    if not q.is_contiguous():
-        raise ValueError("q must be a contiguous [B, H, T, d] tensor")
-    B, H, T, d = q.shape
-    strides = _cache_args(k_cache, v_cache, block_table, seq_lens, new_lens, B, d)
-    if out is None:
-        out = _empty(q.shape, torch.bfloat16, q, stream)
-    elif out.shape != q.shape or out.dtype != torch.bfloat16 or not out.is_cuda or not out.is_contiguous():
-        raise ValueError("out must be a contiguous CUDA bf16 tensor shaped like q")
-    if lse is None:
-        lse = _empty((B, H, T), torch.float32, q, stream)
-    elif lse.shape != (B, H, T) or lse.dtype != torch.float32 or not lse.is_cuda or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous CUDA fp32 [B, H, T] tensor")
-    if workspace is None:
-        need = load().fa_paged_workspace_bytes(B, H, k_cache.shape[1], T, d, prefix_len)
-        workspace = _empty((need,), torch.uint8, q, stream)
-        ws_bytes = need
-    else:
-        if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    dims = (B, H, k_cache.shape[1], T, d, k_cache.shape[0], k_cache.shape[2], block_table.shape[1])
-    return out, lse, workspace, ws_bytes, strides, dims, 1.0 / math.sqrt(d) if scale is None else scale
-
-
-def fwd_paged(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = None, new_lens=None,
-              window: tuple = (-1, 0), out=None, lse=None, workspace=None, stream=None):
-    """(O, LSE) of the new tokens' queries over their sequences' cached keys.
-
-    q: [B, H, T, d] contiguous CUDA bf16 (as ``kv_append`` returns it), T from 1 (decoding) to a prompt's chunk;
-    H a multiple of the cache's heads (query head h reads K/V head h // (H / Hk)).  The cache, block_table,
-    seq_lens (with the new tokens) and new_lens as in ``kv_append``.  ``window=(left, right)`` as in ``fwd``,
-    around the token's own position: (-1, 0) is causal, (-1, -1) every cached key.  Padding rows and rows
-    that see no key get O = 0 and LSE = -inf.  The lengths are read on the GPU, so a captured call stays
-    right as they grow.  ``workspace`` (``fa_paged_workspace_bytes(B, H, Hk, T, d, 0)`` bytes) may be given; calls
-    that may overlap need one each.
-    """
-    out, lse, workspace, ws_bytes, strides, dims, scale = _paged_args(
-        q, k_cache, v_cache, block_table, seq_lens, new_lens, scale, out, lse, workspace, stream, 0)
-    st = fa_fwd_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                      block_table.data_ptr(), seq_lens.data_ptr(), None if new_lens is None else new_lens.data_ptr(),
-                      strides, *dims, scale, window[0], window[1], workspace.data_ptr(), ws_bytes, _handle(stream, q))
-    if st != 0:
-        raise FaError(st, "fa_fwd_paged")
-    return out, lse
-
-
-def fwd_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_table, seq_lens, scale: float | None = None,
-               new_lens=None, out=None, lse=None, workspace=None, stream=None):
-    """(O, LSE) of ``fwd_paged`` (causal) for sequences that all begin with the same ``prefix_len`` tokens, whose
-    K and V (``prefix_pages``: int32 page indices, in the same cache) are read once for the whole batch.
-
-    block_table and seq_lens describe the sequences' own tokens after the prefix (``kv_append`` with
-    ``offset=prefix_len`` puts them there).  An entry with seq_lens <= 0 is empty: O = 0, LSE = -inf.
-    ``workspace``: ``fa_paged_workspace_bytes(B, H, Hk, T, d, prefix_len)`` bytes.
-    """
-    import torch
-
-    _need("prefix_pages", prefix_pages, torch.int32, 1)
-    if prefix_len <= 0:
-        raise ValueError("prefix_len must be > 0 (without a prefix: fwd_paged)")
-    out, lse, workspace, ws_bytes, strides, dims, scale = _paged_args(
-        q, k_cache, v_cache, block_table, seq_lens, new_lens, scale, out, lse, workspace, stream, prefix_len)
-    if not prefix_pages.is_contiguous() or prefix_pages.shape[0] * dims[6] < prefix_len:
-        raise ValueError(f"prefix_pages must be contiguous and hold {prefix_len} tokens of {dims[6]} to a page")
-    st = fa_fwd_prefix(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                       prefix_pages.data_ptr(), prefix_len, block_table.data_ptr(), seq_lens.data_ptr(),
-                       None if new_lens is None else new_lens.data_ptr(), strides, *dims, scale, workspace.data_ptr(),
-                       ws_bytes, _handle(stream, q))
-    if st != 0:
-        raise FaError(st, "fa_fwd_prefix")
-    return out, lse
+        globals().update({n: getattr(serving, n) for n in _SERVING})
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

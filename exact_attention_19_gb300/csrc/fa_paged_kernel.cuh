@@ -274,12 +274,22 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
     constexpr int kWarps = THREADS / 32;
     const long long per = static_cast<long long>(p.Hk) * S::blocks(p);
     long long g = 0, gend = 0;
-    // pass 0 sums, pass 1 finds the sequence that holds unit g
+    // pass 0 sums, pass 1 finds the sequence that holds unit g (from what pass 0 left in the registers
+    // when every sequence has a thread)
+    long long first = 0, mine = 0;
     for (int pass = 0; pass < 2; ++pass) {
       long long run = 0;
       for (int b0 = 0; b0 < p.B; b0 += THREADS) {
         const int b = b0 + static_cast<int>(threadIdx.x);
-        long long mine = 0;
+        if (pass == 1 && p.B <= THREADS) {
+          if (mine > 0 && first <= g && g < first + mine) {
+            scratch[kWarps] = b;
+            scratch[kWarps + 1] = first;
+          }
+          __syncthreads();
+          break;
+        }
+        mine = 0;
         if (b < p.B) {
           const SeqKeys s = seq_keys(p, b);
           mine = per * tiles_of(s.lo, s.hi, kPagedTile);
@@ -299,7 +309,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
           if (i < warp) before += scratch[i];
           all += scratch[i];
         }
-        const long long first = before + incl - mine;
+        first = before + incl - mine;
         if (pass == 0 && blockIdx.x == 0 && b < p.B) p.plan[2 + b] = first;
         if (pass == 1 && mine > 0 && first <= g && g < first + mine) {
           scratch[kWarps] = b;

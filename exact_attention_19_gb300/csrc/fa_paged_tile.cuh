@@ -43,7 +43,7 @@ struct TileCfg {
 
 // barrier slots (8 bytes each); the rest of the 512-byte block: scratch of
 // paged_share at 256, TMEM base at 448, abort flag at 452
-enum : int { kTBarQ = 0, kTBarS = 1, kTBarP = 3, kTBarO = 5, kTBarDrain = 6, kTBarRing = 7 };
+enum : int { kTBarQ = 0, kTBarS = 1, kTBarP = 3, kTBarO = 5, kTBarFinal = 6, kTBarDrain = 7, kTBarRing = 8 };
 constexpr uint32_t kTileScratchOff = 256, kTileTmemOff = 448, kTileAbortOff = 452;
 
 // The tiles [jlo, jhi) of the CTA's part that some row of the block sees.
@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 2)
       mbar_init(bar(kTBarS + i), 1);
       mbar_init(bar(kTBarP + i), 128);
     }
-    mbar_init(bar(kTBarO), 1);
+    mbar_init(bar(kTBarO), 1);      // after every product: one may lag behind, so it names the tile before
+    mbar_init(bar(kTBarFinal), 1);  // after a segment's last product
     mbar_init(bar(kTBarDrain), 1);
     for (int i = 0; i < 2 * C::kRing; ++i) mbar_init(bar(kTBarRing + i), 1);
     *abort_flag = 0;
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 2)
         tc_fence_after();
         product(t & 1, item % C::kRing, i > 0);
         mma_commit_elect(bar(kTBarO));
+        if (i == n - 1) mma_commit_elect(bar(kTBarFinal));
         mma_commit_elect(empty(item % C::kRing));
         ++item;
         if (i + 2 < n) ok = next_scores(t + 2);
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 2)
     const uint32_t tO = lane_base + C::kTmO;
     const float c = p.scale_log2;
     const float NEG_INF = -__int_as_float(0x7f800000);
-    int t = 0, item = 0;  // tiles and ring items of the segments so far
+    int t = 0, item = 0, seg = 0;  // tiles, ring items and segments with tiles so far
     bool ok = true;
     do {
       int jlo, jhi, lo, hi;
@@ -363,10 +365,8 @@ __global__ void __launch_bounds__(TileCfg<D>::kThreads, 2)
       if (!ok) break;
       item += 2 * n;
       if (n > 0) {
-        // the last S covers the products up to two tiles back; the two after them in turn, so that each
-        // parity names one phase
-        ok = (n < 2 || uniform(mbar_wait(bar(kTBarO), (t - 2) & 1, abort_flag))) &&
-             uniform(mbar_wait(bar(kTBarO), (t - 1) & 1, abort_flag));
+        ok = uniform(mbar_wait(bar(kTBarFinal), seg & 1, abort_flag));
+        ++seg;
         if (!ok) break;
         tc_fence_after();
       }
