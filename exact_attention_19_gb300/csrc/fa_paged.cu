@@ -85,12 +85,16 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
   return l;
 }
 
+// Rows from which the merge gives each one warp instead of four.
+constexpr long long kMergeOneWarpRows = 2048;
+
 template <int D, int RB>
 int launch_merge(const fa::PagedParams& p, long long rows, cudaStream_t stream) {
+  const bool one = rows >= kMergeOneWarpRows;
   // programmatic dependent launch: the merge's CTAs may be scheduled while the
   // last parts are computed and wait on the device for that grid's completion
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(rows));
+  cfg.gridDim = dim3(static_cast<unsigned>(one ? (rows + 3) / 4 : rows));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -98,7 +102,8 @@ int launch_merge(const fa::PagedParams& p, long long rows, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, RB>, p);
+  const cudaError_t e = one ? cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, RB, 1>, p)
+                            : cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, RB, 4>, p);
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? FA_OK : FA_ERR_LAUNCH;
 }
 

@@ -93,9 +93,16 @@ __host__ __device__ __forceinline__ long long paged_ctas(long long grid, long lo
   const long long most = units / kPagedMinUnits;
   return most < 1 ? 1 : (most < grid ? most : grid);
 }
-__device__ __forceinline__ long long cta_start(long long units, long long ctas, long long c) { return c * units / ctas; }
+// a / b for a >= 0, b > 0: a 32-bit division where both fit (a 64-bit one is a long instruction sequence)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if ((static_cast<unsigned long long>(a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+__device__ __forceinline__ long long cta_start(long long units, long long ctas, long long c) {
+  return quotient(c * units, ctas);
+}
 __device__ __forceinline__ long long cta_of(long long units, long long ctas, long long x) {
-  return ((x + 1) * ctas - 1) / units;
+  return quotient((x + 1) * ctas - 1, units);
 }
 __host__ __device__ __forceinline__ int own_blocks(int rows, int rb) { return (rows + rb - 1) / rb; }
 __host__ __device__ __forceinline__ int prefix_blocks(int B, int rows, int rb) {
@@ -638,28 +645,33 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
 
 // ---------------------------------------------------------------------------
 // Joins the parts of every row that more than one CTA (or the prefix and the
-// own keys) contributed to, and writes the rows that saw no key.  One CTA of
-// four warps per row: the warps take the parts in turn, each lane D / 32
-// columns, and meet in shared memory.
-// ---------------------------------------------------------------------------
+// own keys) contributed to, and writes the rows that saw no key.  WARPS warps
+// per row: one while there are rows enough to fill the GPU, four below that.
+// Each lane finds one part and its L, the warp weighs them at once, and then
+// sums the parts' O with D / 32 columns to a lane and four loads in flight.
 // RB: rows of an own row block; prefix row blocks have kPrefixRows.
+// ---------------------------------------------------------------------------
 constexpr int kPrefixRows = 128;
 
-template <int D, int RB>
+template <int D, int RB, int WARPS>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p) {
   constexpr int kPer = D / 32;
+  static_assert(WARPS == 1 || WARPS == 4, "warps per row");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long row = blockIdx.x;
-  const long long bh = row / p.rows;
-  const int rr = static_cast<int>(row - bh * p.rows), hk = static_cast<int>(bh % p.Hk), b = static_cast<int>(bh / p.Hk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * (4 / WARPS) + (WARPS == 1 ? warp : 0);
+  const int sub = WARPS == 1 ? 0 : warp;
+  if (row >= static_cast<long long>(p.B) * p.Hk * p.rows) return;
+  const long long bh = quotient(row, p.rows);
+  const int rr = static_cast<int>(row - bh * p.rows);
+  const int b = static_cast<int>(quotient(bh, p.Hk)), hk = static_cast<int>(bh - static_cast<long long>(b) * p.Hk);
   const float NEG_INF = -__int_as_float(0x7f800000);
 
   // CTAs [c0, c1] that hold the row's own keys, [d0, d1] its prefix keys (c0 > c1: none)
   const long long units = p.plan[0], ctas = p.plan[1];
   const long long u0 = p.plan[2 + b];
   const int blocks = own_blocks(p.rows, RB);
-  const long long n = (p.plan[3 + b] - u0) / (static_cast<long long>(p.Hk) * blocks);
+  const long long n = quotient(p.plan[3 + b] - u0, static_cast<long long>(p.Hk) * blocks);
   const long long x0 = u0 + (static_cast<long long>(hk) * blocks + rr / RB) * n;
   long long c0 = 1, c1 = 0, d0 = 1, d1 = 0, y0 = 0;
   if (n > 0) {
@@ -676,74 +688,94 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
     return;  // written by the one CTA that held it
   }
   const int n_own = static_cast<int>(c1 - c0 + 1), n_all = n_own + static_cast<int>(d1 - d0 + 1);
-  // part i of the row: O and L
-  auto part = [&](int i, const float*& po, const float*& pl) {
-    const int pre = i < n_own ? 0 : 1;
-    const long long a = pre ? d0 : c0, z = pre ? d1 : c1, start = pre ? y0 : x0;
-    long long at = row;
-    if (a != z) {
-      const long long c = a + (pre ? i - n_own : i);
-      // a CTA's first segment is its piece 0; the row block is that one unless it starts inside the CTA
-      const long long first = pre ? cta_start(p.prefix_units, p.prefix_ctas, c) : cta_start(units, ctas, c);
-      const long long slot = 2 * c + (first >= start ? 0 : 1);
-      at = pre ? slot * kPrefixRows + pr % kPrefixRows : slot * RB + rr % RB;
-    }
-    po = (a == z ? p.whole_o[pre] : p.piece_o[pre]) + at * D;
-    pl = (a == z ? p.whole_l[pre] : p.piece_l[pre]) + at;
-  };
   float mx = NEG_INF, sum = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int i = warp; i < n_all; i += 4) {
-    const float *po, *pl;
-    part(i, po, pl);
-    const float L = *pl;
-    float v[kPer];
-    if constexpr (kPer == 4) {
-      const float4 t = *reinterpret_cast<const float4*>(po + lane * 4);
-      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-    } else {
-      const float2 t = *reinterpret_cast<const float2*>(po + lane * 2);
-      v[0] = t.x; v[1] = t.y;
+  for (int base = sub; base < n_all; base += 32 * WARPS) {
+    // this lane's part: its O row and L
+    const int i = base + lane * WARPS;
+    const float* po = nullptr;
+    float L = NEG_INF;
+    if (i < n_all) {
+      const int pre = i < n_own ? 0 : 1;
+      const long long a = pre ? d0 : c0, z = pre ? d1 : c1, start = pre ? y0 : x0;
+      long long at = row;
+      if (a != z) {
+        const long long c = a + (pre ? i - n_own : i);
+        // a CTA's first segment is its piece 0; the row block is that one unless it starts inside the CTA
+        const long long first = pre ? cta_start(p.prefix_units, p.prefix_ctas, c) : cta_start(units, ctas, c);
+        const long long slot = 2 * c + (first >= start ? 0 : 1);
+        at = pre ? slot * kPrefixRows + pr % kPrefixRows : slot * RB + rr % RB;
+      }
+      po = (a == z ? p.whole_o[pre] : p.piece_o[pre]) + at * D;
+      L = ((a == z ? p.whole_l[pre] : p.piece_l[pre]))[at];
     }
-    if (L == NEG_INF) continue;
-    const float m_new = fmaxf(mx, L);
-    const float a = mx == NEG_INF ? 0.f : ex2(mx - m_new), c = ex2(L - m_new);
-    mx = m_new;
-    sum = a * sum + c;
+    float top = fmaxf(mx, L);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = a * acc[e] + c * v[e];
-  }
-  __shared__ float sh[4][D + 2];
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == NEG_INF) continue;
+    const float a = mx == NEG_INF ? 0.f : ex2(mx - top);
+    const float wt = L == NEG_INF ? 0.f : ex2(L - top);
+    float ws = wt;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) sh[warp][lane * kPer + e] = acc[e];
-  if (lane == 0) {
-    sh[warp][D] = mx;
-    sh[warp][D + 1] = sum;
-  }
-  __syncthreads();
-  if (warp != 0) return;
-  float top = NEG_INF, tot = 0.f, fin[kPer];
+    for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
+    mx = top;
+    sum = a * sum + ws;
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) fin[e] = 0.f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top = fmaxf(top, sh[i][D]);
-  if (top != NEG_INF) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float c = sh[i][D] == NEG_INF ? 0.f : ex2(sh[i][D] - top);
-      tot += c * sh[i][D + 1];
-#pragma unroll
-      for (int e = 0; e < kPer; ++e) fin[e] += c * sh[i][lane * kPer + e];
+    for (int e = 0; e < kPer; ++e) acc[e] *= a;
+    const int count = min(32, (n_all - base + WARPS - 1) / WARPS);
+#pragma unroll 4
+    for (int k = 0; k < count; ++k) {
+      const float* src = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), k));
+      const float c = __shfl_sync(0xffffffffu, wt, k);
+      if constexpr (kPer == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(src + lane * 4);
+        acc[0] = fmaf(c, t.x, acc[0]);
+        acc[1] = fmaf(c, t.y, acc[1]);
+        acc[2] = fmaf(c, t.z, acc[2]);
+        acc[3] = fmaf(c, t.w, acc[3]);
+      } else {
+        const float2 t = *reinterpret_cast<const float2*>(src + lane * 2);
+        acc[0] = fmaf(c, t.x, acc[0]);
+        acc[1] = fmaf(c, t.y, acc[1]);
+      }
     }
   }
-  const float inv = tot > 0.f ? 1.0f / tot : 0.f;
+  if constexpr (WARPS == 4) {
+    __shared__ float sh[4][D + 2];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) sh[warp][lane * kPer + e] = acc[e];
+    if (lane == 0) {
+      sh[warp][D] = mx;
+      sh[warp][D + 1] = sum;
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    float top = NEG_INF;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = fmaxf(top, sh[i][D]);
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    if (top != NEG_INF) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float c = sh[i][D] == NEG_INF ? 0.f : ex2(sh[i][D] - top);
+        sum += c * sh[i][D + 1];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[e] += c * sh[i][lane * kPer + e];
+      }
+    }
+    mx = top;
+  }
+  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
   uint16_t* const dst = p.out + row * D + lane * kPer;
   if constexpr (kPer == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(fin[0] * inv, fin[1] * inv), pack_bf16(fin[2] * inv, fin[3] * inv));
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
   else
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(fin[0] * inv, fin[1] * inv);
-  if (lane == 0) p.lse[row] = tot > 0.f ? (top + __log2f(tot)) * 0.69314718055994530942f : NEG_INF;
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+  if (lane == 0) p.lse[row] = sum > 0.f ? (mx + __log2f(sum)) * 0.69314718055994530942f : NEG_INF;
 }
 
 }  // namespace fa
