@@ -15,15 +15,27 @@ constexpr int kMaxKeys = 1 << 30;  // tokens of a sequence or a prefix: tile ari
 
 std::atomic<bool> g_ready[fa_host::kMaxDevices];
 
+template <typename K>
+bool allow(K kernel, size_t smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) ==
+         cudaSuccess;
+}
+
+// The tile kernels move registers between warpgroups, which assumes the count
+// they are launched with; a build with another count is refused.
+template <int D, bool PREFIX, bool PAIR>
+bool allow_tile() {
+  using C = fa::TileCfg<D, PAIR>;
+  cudaFuncAttributes a;
+  return cudaFuncGetAttributes(&a, fa::fa_paged_tile_kernel<D, PREFIX, PAIR>) == cudaSuccess &&
+         a.numRegs == C::kRegLaunch && allow(fa::fa_paged_tile_kernel<D, PREFIX, PAIR>, C::kSmemBytes);
+}
+
 template <int D>
 bool opt_in() {
-  const int tile = static_cast<int>(fa::TileCfg<D>::kSmemBytes);
-  return cudaFuncSetAttribute(fa::fa_paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(fa::PagedCfg<D>::kSmemBytes)) == cudaSuccess &&
-         cudaFuncSetAttribute(fa::fa_paged_tile_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, tile) ==
-             cudaSuccess &&
-         cudaFuncSetAttribute(fa::fa_paged_tile_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, tile) ==
-             cudaSuccess;
+  return allow(fa::fa_paged_kernel<D, false>, fa::PagedCfg<D>::kSmemBytes) &&
+         allow(fa::fa_paged_kernel<D, true>, fa::PagedCfg<D>::kSmemBytes) && allow_tile<D, false, false>() &&
+         allow_tile<D, false, true>() && allow_tile<D, true, false>() && allow_tile<D, true, true>();
 }
 
 // The kernels' shared-memory opt-in, once per device (a repeated call is harmless).
@@ -53,12 +65,18 @@ bool make_cache_map(CUtensorMap* map, const void* ptr, int d, int page, int Hk, 
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
-// Rows per own row block: the warp-level kernel's 16 while the rows of one
-// (sequence, K/V head) fit one block, else the tcgen05 kernel's 128.
-int own_block_rows(int rows) { return rows <= 16 ? 16 : 128; }
+// Rows per row block, by the rows that share each K/V byte: the warp-level
+// kernel's 16, or the tcgen05 kernel's 128 or 256.
+int block_rows(long long rows) { return rows <= 16 ? 16 : (rows <= 128 ? 128 : 256); }
+int tile_keys(int block_rows) { return block_rows == 16 ? 64 : 128; }
+int grid_of(int block_rows, int sms) { return block_rows == 16 ? 2 * sms : sms; }  // all CTAs resident
 
-// Parts of the workspace, in order; every size is a multiple of 16 bytes.
+// The row blocks, tiles and CTAs of a call, and the parts of its workspace, in
+// order; every size is a multiple of 16 bytes.
 struct Layout {
+  int rb[2], grid[2];
+  int prefix_blocks, prefix_tiles;
+  long long prefix_units, prefix_ctas;
   size_t plan, piece_o[2], piece_l[2], whole_o[2], whole_l[2];
   size_t bytes() const {
     size_t n = plan;
@@ -68,15 +86,20 @@ struct Layout {
 };
 Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
   const size_t all = static_cast<size_t>(B) * H * T;
-  const int rows = H / Hk * T;
+  const long long rows = static_cast<long long>(H / Hk) * T;
   Layout l = {};
   l.plan = up16((static_cast<size_t>(B) + 3) * sizeof(long long));
   for (int i = 0; i < (prefix_len > 0 ? 2 : 1); ++i) {
-    size_t ctas = 2 * static_cast<size_t>(sms);
-    if (i == 1)
-      ctas = static_cast<size_t>(fa::paged_ctas(
-          2ll * sms, 1ll * Hk * fa::prefix_blocks(B, rows, fa::kPrefixRows) * fa::prefix_tiles(prefix_len)));
-    const size_t pieces = 2 * ctas * (i == 0 ? own_block_rows(rows) : fa::kPrefixRows);
+    l.rb[i] = block_rows(i == 0 ? rows : rows * B);
+    l.grid[i] = grid_of(l.rb[i], sms);
+    if (i == 1) {
+      l.prefix_blocks = fa::row_blocks(rows * B, l.rb[1]);
+      l.prefix_tiles = (prefix_len + tile_keys(l.rb[1]) - 1) / tile_keys(l.rb[1]);
+      l.prefix_units = 1ll * Hk * l.prefix_blocks * l.prefix_tiles;
+      l.prefix_ctas = fa::paged_ctas(l.grid[1], l.prefix_units);
+      l.grid[1] = static_cast<int>(l.prefix_ctas);
+    }
+    const size_t pieces = 2 * static_cast<size_t>(l.grid[i]) * l.rb[i];
     l.piece_o[i] = pieces * d * sizeof(float);
     l.piece_l[i] = pieces * sizeof(float);
     l.whole_o[i] = prefix_len > 0 ? all * d * sizeof(float) : 0;
@@ -88,7 +111,7 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
 // Rows from which the merge gives each one warp instead of four.
 constexpr long long kMergeOneWarpRows = 2048;
 
-template <int D, int RB>
+template <int D>
 int launch_merge(const fa::PagedParams& p, long long rows, cudaStream_t stream) {
   const bool one = rows >= kMergeOneWarpRows;
   // programmatic dependent launch: the merge's CTAs may be scheduled while the
@@ -102,8 +125,8 @@ int launch_merge(const fa::PagedParams& p, long long rows, cudaStream_t stream) 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = one ? cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, RB, 1>, p)
-                            : cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, RB, 4>, p);
+  const cudaError_t e = one ? cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, 1>, p)
+                            : cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, 4>, p);
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -118,29 +141,30 @@ struct Caches {
   }
 };
 
-template <int D>
-int launch(const Caches& c, const fa::PagedParams& p, int sms, long long rows, cudaStream_t stream) {
-  using S = fa::PagedCfg<D>;
-  using T = fa::TileCfg<D>;
-  const bool tile = own_block_rows(p.rows) != 16;
+// One part of a call: the prefix or the sequences' own keys.
+template <int D, bool PREFIX>
+int launch_part(const Caches& c, const fa::PagedParams& p, int grid, cudaStream_t stream) {
+  const int rb = p.rb[PREFIX];
   CUtensorMap mk, mv;
-  if (tile || p.prefix_len > 0) {
-    if (!c.maps(&mk, &mv, T::kTile)) return FA_ERR_LAUNCH;
+  if (!c.maps(&mk, &mv, rb == 16 ? fa::PagedCfg<D>::kKeys : tile_keys(rb))) return FA_ERR_LAUNCH;
+  if (rb == 16) {
+    using S = fa::PagedCfg<D>;
+    fa::fa_paged_kernel<D, PREFIX><<<grid, S::kThreads, S::kSmemBytes, stream>>>(mk, mv, p);
+  } else if (rb == 128) {
+    using T = fa::TileCfg<D, false>;
+    fa::fa_paged_tile_kernel<D, PREFIX, false><<<grid, T::kThreads, T::kSmemBytes, stream>>>(mk, mv, p);
+  } else {
+    using T = fa::TileCfg<D, true>;
+    fa::fa_paged_tile_kernel<D, PREFIX, true><<<grid, T::kThreads, T::kSmemBytes, stream>>>(mk, mv, p);
   }
-  if (p.prefix_len > 0) {
-    fa::fa_paged_tile_kernel<D, true><<<static_cast<unsigned>(p.prefix_ctas), T::kThreads, T::kSmemBytes, stream>>>(
-        mk, mv, p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-  }
-  if (tile) {
-    fa::fa_paged_tile_kernel<D, false><<<2 * sms, T::kThreads, T::kSmemBytes, stream>>>(mk, mv, p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-    return launch_merge<D, 128>(p, rows, stream);
-  }
-  if (!c.maps(&mk, &mv, S::kKeys)) return FA_ERR_LAUNCH;
-  fa::fa_paged_kernel<D><<<2 * sms, S::kThreads, S::kSmemBytes, stream>>>(mk, mv, p);
-  if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-  return launch_merge<D, 16>(p, rows, stream);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+template <int D>
+int launch(const Caches& c, const fa::PagedParams& p, const Layout& l, long long rows, cudaStream_t stream) {
+  int st = p.prefix_len > 0 ? launch_part<D, true>(c, p, l.grid[1], stream) : FA_OK;
+  if (st == FA_OK) st = launch_part<D, false>(c, p, l.grid[0], stream);
+  return st == FA_OK ? launch_merge<D>(p, rows, stream) : st;
 }
 
 int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse, const int* prefix_pages,
@@ -203,11 +227,12 @@ int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
   p.left = left;
   p.right = right;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
-  if (prefix_len > 0) {
-    p.prefix_units =
-        1ll * Hk * fa::prefix_blocks(B, p.rows, fa::kPrefixRows) * fa::prefix_tiles(prefix_len);
-    p.prefix_ctas = fa::paged_ctas(2ll * sms, p.prefix_units);
-  }
+  p.rb[0] = l.rb[0];
+  p.rb[1] = l.rb[1];
+  p.prefix_blocks = l.prefix_blocks;
+  p.prefix_tiles = l.prefix_tiles;
+  p.prefix_units = l.prefix_units;
+  p.prefix_ctas = l.prefix_ctas;
   char* at = static_cast<char*>(workspace);
   p.plan = reinterpret_cast<long long*>(at);
   at += l.plan;
@@ -221,7 +246,7 @@ int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
   p.status = fa_host::status_word(dev);
   if (!p.status) return FA_ERR_LAUNCH;
   const Caches c = {k_cache, v_cache, strides, d, page_size, Hk, n_pages};
-  return d == 64 ? launch<64>(c, p, sms, rows, stream) : launch<128>(c, p, sms, rows, stream);
+  return d == 64 ? launch<64>(c, p, l, rows, stream) : launch<128>(c, p, l, rows, stream);
 }
 
 }  // namespace

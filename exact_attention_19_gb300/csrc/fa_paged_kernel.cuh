@@ -8,7 +8,7 @@
 // position len - fresh + t and sees the own keys its window reaches, and every
 // prefix key at or before it.
 //
-// Schedule.  A work unit is one block of rows against one tile of 64 keys; a
+// Schedule.  A work unit is one block of rows against one tile of keys; a
 // launch covers either the sequences' own keys (row blocks of one sequence and
 // K/V head) or the shared prefix (row blocks over all the batch's rows of a K/V
 // head, so its K/V is read once for the batch and not once per sequence).  The
@@ -48,8 +48,10 @@ struct PagedParams {
   int left, right;          // own window, -1 = open
   float scale_log2;         // scale * log2(e)
   long long* plan;          // own units: [0] units, [1] CTAs with work, [2 + b] first unit of sequence b
-  long long prefix_units;   // prefix units and the CTAs they are shared among
-  long long prefix_ctas;
+  int rb[2];                // rows of a row block: own keys, prefix
+  int prefix_blocks;        // row blocks of a K/V head, key tiles, units and CTAs of the prefix
+  int prefix_tiles;
+  long long prefix_units, prefix_ctas;
   // [0] own keys, [1] prefix: parts of row blocks that CTAs share, two per CTA ([2 * CTAs, row block, D]), and
   // with a prefix the row blocks that one CTA finished ([B * H * T, D])
   float* piece_o[2];
@@ -86,11 +88,9 @@ __device__ __forceinline__ int row_prefix_keys(const PagedParams& p, const SeqKe
   return (t < s.fresh && s.len - s.fresh + t >= 0) ? p.prefix_len : 0;
 }
 
-constexpr int kPagedTile = 64;           // keys of a unit
-constexpr long long kPagedMinUnits = 2;  // units a CTA takes at least
-
+// CTAs that `units` units are shared among: at least two units each.
 __host__ __device__ __forceinline__ long long paged_ctas(long long grid, long long units) {
-  const long long most = units / kPagedMinUnits;
+  const long long most = units / 2;
   return most < 1 ? 1 : (most < grid ? most : grid);
 }
 // a / b for a >= 0, b > 0: a 32-bit division where both fit (a 64-bit one is a long instruction sequence)
@@ -104,11 +104,7 @@ __device__ __forceinline__ long long cta_start(long long units, long long ctas, 
 __device__ __forceinline__ long long cta_of(long long units, long long ctas, long long x) {
   return quotient((x + 1) * ctas - 1, units);
 }
-__host__ __device__ __forceinline__ int own_blocks(int rows, int rb) { return (rows + rb - 1) / rb; }
-__host__ __device__ __forceinline__ int prefix_blocks(int B, int rows, int rb) {
-  return static_cast<int>((static_cast<long long>(B) * rows + rb - 1) / rb);
-}
-__host__ __device__ __forceinline__ int prefix_tiles(int prefix_len) { return (prefix_len + kPagedTile - 1) / kPagedTile; }
+__host__ __device__ __forceinline__ int row_blocks(long long rows, int rb) { return static_cast<int>((rows + rb - 1) / rb); }
 
 // A row block against the tiles of its keys that this CTA holds.
 struct PagedWalk {
@@ -119,18 +115,18 @@ struct PagedWalk {
   int lo, hi;         // keys that any row of the segment may see
 };
 
-template <int RB, bool PREFIX>
+template <int RB, int TILE, bool PREFIX>
 struct PagedSchedule {
   static __device__ __forceinline__ int blocks(const PagedParams& p) {
-    return PREFIX ? prefix_blocks(p.B, p.rows, RB) : own_blocks(p.rows, RB);
+    return PREFIX ? p.prefix_blocks : row_blocks(p.rows, RB);
   }
   static __device__ __forceinline__ void enter_seq(const PagedParams& p, PagedWalk& w) {
     for (;; ++w.b) {  // w.g < w.gend, so a sequence with units follows
       const SeqKeys s = seq_keys(p, w.b);
       w.lo = s.lo;
       w.hi = s.hi;
-      w.tile0 = s.lo / kPagedTile;
-      w.n = tiles_of(s.lo, s.hi, kPagedTile);
+      w.tile0 = s.lo / TILE;
+      w.n = tiles_of(s.lo, s.hi, TILE);
       if (w.n > 0 || w.b + 1 >= p.B) return;
     }
   }
@@ -145,7 +141,7 @@ struct PagedSchedule {
     w.gend = gend;
     w.b = b;
     if constexpr (PREFIX) {
-      w.n = prefix_tiles(p.prefix_len);
+      w.n = p.prefix_tiles;
       w.tile0 = 0;
       w.lo = 0;
       w.hi = p.prefix_len;
@@ -196,11 +192,12 @@ struct PagedSchedule {
     else row_own_keys(p, s, rr % p.T, lo, hi);
     return (static_cast<long long>(b) * p.Hk + w.hk) * p.rows + rr;
   }
-  // where a row block's result goes: 0 the output, 1 whole_*, 2 piece_* (row = of the piece)
-  static __device__ __forceinline__ int target(const PagedParams& p, const PagedWalk& w, long long first_g, int r,
+  // where a row block's result goes: 0 the output, 1 whole_*, 2 piece_* (row = of the piece); first: the
+  // segment is the CTA's first
+  static __device__ __forceinline__ int target(const PagedParams& p, const PagedWalk& w, bool first, int r,
                                                long long& row) {
     if (w.jend - w.j == w.n) return p.prefix_len > 0 ? 1 : 0;
-    const long long slot = 2ll * blockIdx.x + (w.g == first_g ? 0 : 1);
+    const long long slot = 2ll * blockIdx.x + (first ? 0 : 1);
     row = slot * RB + r;
     return 2;
   }
@@ -267,10 +264,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // Block-wide: the CTA's share of the launch's units, as the walk's first
 // segment; false when it has none.  For own keys the units come from the
 // lengths, and CTA 0 leaves the plan for the merge kernel.
-template <int RB, bool PREFIX, int THREADS>
+template <int RB, int TILE, bool PREFIX, int THREADS>
 __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scratch /* shared, THREADS / 32 + 2 */,
                                             PagedWalk& w) {
-  using S = PagedSchedule<RB, PREFIX>;
+  using S = PagedSchedule<RB, TILE, PREFIX>;
   if constexpr (PREFIX) {
     if (static_cast<long long>(blockIdx.x) >= p.prefix_ctas) return false;
     const long long g = cta_start(p.prefix_units, p.prefix_ctas, blockIdx.x);
@@ -299,7 +296,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
         mine = 0;
         if (b < p.B) {
           const SeqKeys s = seq_keys(p, b);
-          mine = per * tiles_of(s.lo, s.hi, kPagedTile);
+          mine = per * tiles_of(s.lo, s.hi, TILE);
           if (pass == 0 && blockIdx.x == 0 && __ldg(p.lens + b) > p.capacity) atomicOr(p.status, kPagedPage);
         }
         long long incl = mine;
@@ -343,12 +340,12 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
   }
 }
 
-template <int D>
+template <int D, bool PREFIX>
 __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                     const PagedParams p) {
   using C = PagedCfg<D>;
-  using S = PagedSchedule<C::kRows, false>;
+  using S = PagedSchedule<C::kRows, C::kTile, PREFIX>;
   constexpr int kNT = D / 8;   // 8-column tiles of O
   constexpr int kKT = D / 16;  // 16-deep steps of Q K^T
   extern __shared__ uint8_t smem_raw[];
@@ -370,7 +367,7 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     mbar_init_fence();
   }
   PagedWalk w;
-  if (!paged_share<C::kRows, false, C::kThreads>(p, scratch, w)) return;
+  if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(p, scratch, w)) return;
   const long long first_g = w.g;
   __syncthreads();
 
@@ -621,7 +618,7 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
       const float inv = l[i] > 0.f ? 1.0f / l[i] : 0.f;
       const float lb = l[i] > 0.f ? m[i] + __log2f(l[i]) : NEG_INF;
       long long row = out_row[i];
-      const int to = S::target(p, w, first_g, g8 + 8 * i, row);
+      const int to = S::target(p, w, w.g == first_g, g8 + 8 * i, row);
       if (to == 0) {
         uint16_t* const dst = p.out + row * D + col;
 #pragma unroll
@@ -629,11 +626,11 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
           *reinterpret_cast<uint32_t*>(dst + n * 8) = pack_bf16(fin[n][2 * i] * inv, fin[n][2 * i + 1] * inv);
         if (col == 0) p.lse[row] = lb * 0.69314718055994530942f;
       } else {
-        float* const dst = (to == 1 ? p.whole_o[0] : p.piece_o[0]) + row * D + col;
+        float* const dst = (to == 1 ? p.whole_o[PREFIX] : p.piece_o[PREFIX]) + row * D + col;
 #pragma unroll
         for (int n = 0; n < kNT / 4; ++n)
           *reinterpret_cast<float2*>(dst + n * 8) = make_float2(fin[n][2 * i] * inv, fin[n][2 * i + 1] * inv);
-        if (col == 0) (to == 1 ? p.whole_l[0] : p.piece_l[0])[row] = lb;
+        if (col == 0) (to == 1 ? p.whole_l[PREFIX] : p.piece_l[PREFIX])[row] = lb;
       }
     }
   } while (S::next(p, w));
@@ -649,11 +646,8 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
 // per row: one while there are rows enough to fill the GPU, four below that.
 // Each lane finds one part and its L, the warp weighs them at once, and then
 // sums the parts' O with D / 32 columns to a lane and four loads in flight.
-// RB: rows of an own row block; prefix row blocks have kPrefixRows.
 // ---------------------------------------------------------------------------
-constexpr int kPrefixRows = 128;
-
-template <int D, int RB, int WARPS>
+template <int D, int WARPS>
 __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p) {
   constexpr int kPer = D / 32;
   static_assert(WARPS == 1 || WARPS == 4, "warps per row");
@@ -670,9 +664,9 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
   // CTAs [c0, c1] that hold the row's own keys, [d0, d1] its prefix keys (c0 > c1: none)
   const long long units = p.plan[0], ctas = p.plan[1];
   const long long u0 = p.plan[2 + b];
-  const int blocks = own_blocks(p.rows, RB);
+  const int blocks = row_blocks(p.rows, p.rb[0]);
   const long long n = quotient(p.plan[3 + b] - u0, static_cast<long long>(p.Hk) * blocks);
-  const long long x0 = u0 + (static_cast<long long>(hk) * blocks + rr / RB) * n;
+  const long long x0 = u0 + (static_cast<long long>(hk) * blocks + rr / p.rb[0]) * n;
   long long c0 = 1, c1 = 0, d0 = 1, d1 = 0, y0 = 0;
   if (n > 0) {
     c0 = cta_of(units, ctas, x0);
@@ -680,8 +674,8 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
   }
   const long long pr = static_cast<long long>(b) * p.rows + rr;  // row among the K/V head's prefix rows
   if (p.prefix_len > 0) {
-    const int nt = prefix_tiles(p.prefix_len);
-    y0 = (static_cast<long long>(hk) * prefix_blocks(p.B, p.rows, kPrefixRows) + pr / kPrefixRows) * nt;
+    const int nt = p.prefix_tiles;
+    y0 = (static_cast<long long>(hk) * p.prefix_blocks + quotient(pr, p.rb[1])) * nt;
     d0 = cta_of(p.prefix_units, p.prefix_ctas, y0);
     d1 = cta_of(p.prefix_units, p.prefix_ctas, y0 + nt - 1);
   } else if (n > 0 && c0 == c1) {
@@ -705,7 +699,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
         // a CTA's first segment is its piece 0; the row block is that one unless it starts inside the CTA
         const long long first = pre ? cta_start(p.prefix_units, p.prefix_ctas, c) : cta_start(units, ctas, c);
         const long long slot = 2 * c + (first >= start ? 0 : 1);
-        at = pre ? slot * kPrefixRows + pr % kPrefixRows : slot * RB + rr % RB;
+        at = slot * p.rb[pre] + (pre ? static_cast<unsigned>(pr) % p.rb[1] : rr % p.rb[0]);
       }
       po = (a == z ? p.whole_o[pre] : p.piece_o[pre]) + at * D;
       L = ((a == z ? p.whole_l[pre] : p.piece_l[pre]))[at];
