@@ -63,7 +63,7 @@ bool make_cache_map(CUtensorMap* map, const void* ptr, int d, int page, int Hk, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 // Rows per row block, by the rows that share each K/V byte: the warp-level
 // kernel's 16, or the tcgen05 kernel's 128 or 256.
@@ -72,14 +72,14 @@ int tile_keys(int block_rows) { return block_rows == 16 ? 64 : 128; }
 int grid_of(int block_rows, int sms) { return block_rows == 16 ? 2 * sms : sms; }  // all CTAs resident
 
 // The row blocks, tiles and CTAs of a call, and the parts of its workspace, in
-// order; every size is a multiple of 16 bytes.
+// order; every part begins on a 256-byte boundary.
 struct Layout {
   int rb[2], grid[2];
   int prefix_blocks, prefix_tiles;
   long long prefix_units, prefix_ctas;
   size_t plan, piece_o[2], piece_l[2], whole_o[2], whole_l[2];
   size_t bytes() const {
-    size_t n = plan;
+    size_t n = plan + 240;  // the caller aligns the workspace to 16 bytes, its parts to 256
     for (int i = 0; i < 2; ++i) n += piece_o[i] + piece_l[i] + whole_o[i] + whole_l[i];
     return n;
   }
@@ -88,7 +88,7 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
   const size_t all = static_cast<size_t>(B) * H * T;
   const long long rows = static_cast<long long>(H / Hk) * T;
   Layout l = {};
-  l.plan = up16((static_cast<size_t>(B) + 3) * sizeof(long long));
+  l.plan = up((static_cast<size_t>(B) + 3) * sizeof(long long));
   for (int i = 0; i < (prefix_len > 0 ? 2 : 1); ++i) {
     l.rb[i] = block_rows(i == 0 ? rows : rows * B);
     l.grid[i] = grid_of(l.rb[i], sms);
@@ -100,34 +100,40 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
       l.grid[1] = static_cast<int>(l.prefix_ctas);
     }
     const size_t pieces = 2 * static_cast<size_t>(l.grid[i]) * l.rb[i];
-    l.piece_o[i] = pieces * d * sizeof(float);
-    l.piece_l[i] = pieces * sizeof(float);
-    l.whole_o[i] = prefix_len > 0 ? all * d * sizeof(float) : 0;
-    l.whole_l[i] = prefix_len > 0 ? up16(all * sizeof(float)) : 0;
+    l.piece_o[i] = up(pieces * d * sizeof(float));
+    l.piece_l[i] = up(pieces * sizeof(float));
+    l.whole_o[i] = prefix_len > 0 ? up(all * d * sizeof(float)) : 0;
+    l.whole_l[i] = prefix_len > 0 ? up(all * sizeof(float)) : 0;
   }
   return l;
 }
 
-// Rows from which the merge gives each one warp instead of four.
-constexpr long long kMergeOneWarpRows = 2048;
+// Rows from which one warp of the merge joins four rows; below, four warps join one.
+constexpr long long kMergeRows = 2048;
 
-template <int D>
-int launch_merge(const fa::PagedParams& p, long long rows, cudaStream_t stream) {
-  const bool one = rows >= kMergeOneWarpRows;
-  // programmatic dependent launch: the merge's CTAs may be scheduled while the
-  // last parts are computed and wait on the device for that grid's completion
+// Programmatic dependent launch: the kernel may be scheduled while the one ahead
+// of it on the stream still runs, and waits on the device (paged_begin) for what
+// it needs of it.
+template <typename K, typename... A>
+int launch_kernel(K kernel, long long grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(one ? (rows + 3) / 4 : rows));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = one ? cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, 1>, p)
-                            : cudaLaunchKernelEx(&cfg, fa::fa_paged_merge_kernel<D, 4>, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
   return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? FA_OK : FA_ERR_LAUNCH;
+}
+
+template <int D>
+int launch_merge(const fa::PagedParams& p, long long rows, cudaStream_t stream) {
+  if (rows >= kMergeRows) return launch_kernel(fa::fa_paged_merge_rows_kernel<D>, (rows + 15) / 16, 128, 0, stream, p);
+  return launch_kernel(fa::fa_paged_merge_row_kernel<D>, rows, 128, 0, stream, p);
 }
 
 struct Caches {
@@ -149,15 +155,15 @@ int launch_part(const Caches& c, const fa::PagedParams& p, int grid, cudaStream_
   if (!c.maps(&mk, &mv, rb == 16 ? fa::PagedCfg<D>::kKeys : tile_keys(rb))) return FA_ERR_LAUNCH;
   if (rb == 16) {
     using S = fa::PagedCfg<D>;
-    fa::fa_paged_kernel<D, PREFIX><<<grid, S::kThreads, S::kSmemBytes, stream>>>(mk, mv, p);
-  } else if (rb == 128) {
-    using T = fa::TileCfg<D, false>;
-    fa::fa_paged_tile_kernel<D, PREFIX, false><<<grid, T::kThreads, T::kSmemBytes, stream>>>(mk, mv, p);
-  } else {
-    using T = fa::TileCfg<D, true>;
-    fa::fa_paged_tile_kernel<D, PREFIX, true><<<grid, T::kThreads, T::kSmemBytes, stream>>>(mk, mv, p);
+    return launch_kernel(fa::fa_paged_kernel<D, PREFIX>, grid, S::kThreads, S::kSmemBytes, stream, mk, mv, p);
   }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  if (rb == 128) {
+    using T = fa::TileCfg<D, false>;
+    return launch_kernel(fa::fa_paged_tile_kernel<D, PREFIX, false>, grid, T::kThreads, T::kSmemBytes, stream, mk, mv,
+                         p);
+  }
+  using T = fa::TileCfg<D, true>;
+  return launch_kernel(fa::fa_paged_tile_kernel<D, PREFIX, true>, grid, T::kThreads, T::kSmemBytes, stream, mk, mv, p);
 }
 
 template <int D>
@@ -233,7 +239,7 @@ int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
   p.prefix_tiles = l.prefix_tiles;
   p.prefix_units = l.prefix_units;
   p.prefix_ctas = l.prefix_ctas;
-  char* at = static_cast<char*>(workspace);
+  char* at = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
   p.plan = reinterpret_cast<long long*>(at);
   at += l.plan;
   for (int i = 0; i < 2; ++i) {

@@ -106,6 +106,25 @@ __device__ __forceinline__ long long cta_of(long long units, long long ctas, lon
 }
 __host__ __device__ __forceinline__ int row_blocks(long long rows, int rb) { return static_cast<int>((rows + rb - 1) / rb); }
 
+// Programmatic dependent launch.  Every kernel here is launched so that it may
+// be scheduled before the one ahead of it on the stream has finished, and
+// paged_begin waits for that (inputs and workspace are then as stream order
+// has them) before it lets the next one be scheduled.  The own-key kernel behind
+// a prefix kernel needs nothing of it and runs beside it (all work before the
+// prefix kernel is done, or that kernel would not have let this one start); it
+// waits before it ends, so that the merge, which waits for it, sees both.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <bool PREFIX>
+__device__ __forceinline__ void paged_begin(const PagedParams& p) {
+  if (PREFIX || p.prefix_len == 0) grid_wait();
+  grid_release();
+}
+template <bool PREFIX>
+__device__ __forceinline__ void paged_end(const PagedParams& p) {
+  if (!PREFIX && p.prefix_len > 0) grid_wait();
+}
+
 // A row block against the tiles of its keys that this CTA holds.
 struct PagedWalk {
   long long g, gend;  // first unit of the current segment part, end of the CTA's units
@@ -148,10 +167,10 @@ struct PagedSchedule {
     } else {
       enter_seq(p, w);
     }
-    const long long i = (g - b_unit) / w.n;
+    const long long i = quotient(g - b_unit, w.n);
     w.j = static_cast<int>((g - b_unit) - i * w.n);
-    w.hk = static_cast<int>(i / blocks(p));
-    w.rb = static_cast<int>(i % blocks(p));
+    w.hk = static_cast<int>(quotient(i, blocks(p)));
+    w.rb = static_cast<int>(i - static_cast<long long>(w.hk) * blocks(p));
     part(w);
   }
   // the segment after the current one, w.j still its first tile; false: none left
@@ -360,14 +379,19 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
   float* const merge = reinterpret_cast<float*>(sbase + C::kMergeOff);
   float* const stat = reinterpret_cast<float*>(sbase + C::kStatOff);  // [warp][16 rows][m, l]
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 0) {
     for (int i = 0; i < C::kRing; ++i) mbar_init(bars + 8 * i, 1);
     if (warp == 0) *abort_flag = 0;
     mbar_init_fence();
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
   }
+  paged_begin<PREFIX>(p);
   PagedWalk w;
-  if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(p, scratch, w)) return;
+  if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(p, scratch, w)) {
+    paged_end<PREFIX>(p);
+    return;
+  }
   const long long first_g = w.g;
   __syncthreads();
 
@@ -638,72 +662,120 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     for (int i = consumed; i < issued; ++i)
       mbar_wait(bars + 8 * (i % C::kRing), static_cast<uint32_t>(i / C::kRing) & 1u, nullptr);
   }
+  paged_end<PREFIX>(p);
 }
 
 // ---------------------------------------------------------------------------
 // Joins the parts of every row that more than one CTA (or the prefix and the
-// own keys) contributed to, and writes the rows that saw no key.  WARPS warps
-// per row: one while there are rows enough to fill the GPU, four below that.
-// Each lane finds one part and its L, the warp weighs them at once, and then
-// sums the parts' O with D / 32 columns to a lane and four loads in flight.
+// own keys) contributed to, and writes the rows that saw no key.
 // ---------------------------------------------------------------------------
-template <int D, int WARPS>
-__global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p) {
-  constexpr int kPer = D / 32;
-  static_assert(WARPS == 1 || WARPS == 4, "warps per row");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * (4 / WARPS) + (WARPS == 1 ? warp : 0);
-  const int sub = WARPS == 1 ? 0 : warp;
-  if (row >= static_cast<long long>(p.B) * p.Hk * p.rows) return;
-  const long long bh = quotient(row, p.rows);
-  const int rr = static_cast<int>(row - bh * p.rows);
-  const int b = static_cast<int>(quotient(bh, p.Hk)), hk = static_cast<int>(bh - static_cast<long long>(b) * p.Hk);
-  const float NEG_INF = -__int_as_float(0x7f800000);
+// The parts of one row, in order: own keys of CTAs [c0, c1], prefix of [d0, d1].
+struct RowParts {
+  long long row, c0, x0, d0, y0, units, ctas;
+  int n_own, n_all, in_own, in_prefix;  // row inside its row block
+  __device__ __forceinline__ void find(const PagedParams& p, long long r) {
+    row = r;
+    const long long bh = quotient(row, p.rows);
+    const int rr = static_cast<int>(row - bh * p.rows);
+    const int b = static_cast<int>(quotient(bh, p.Hk)), hk = static_cast<int>(bh - static_cast<long long>(b) * p.Hk);
+    units = p.plan[0];
+    ctas = p.plan[1];
+    const long long u0 = p.plan[2 + b], u1 = p.plan[3 + b];
+    const int blocks = row_blocks(p.rows, p.rb[0]);
+    const long long n = quotient(u1 - u0, static_cast<long long>(p.Hk) * blocks);
+    x0 = u0 + (static_cast<long long>(hk) * blocks + rr / p.rb[0]) * n;
+    in_own = rr % p.rb[0];
+    n_own = 0;
+    c0 = 0;
+    if (n > 0) {
+      c0 = cta_of(units, ctas, x0);
+      n_own = static_cast<int>(cta_of(units, ctas, x0 + n - 1) - c0) + 1;
+    }
+    n_all = n_own;
+    d0 = y0 = 0;
+    in_prefix = 0;
+    if (p.prefix_len > 0) {
+      const long long pr = static_cast<long long>(b) * p.rows + rr;  // row among the K/V head's prefix rows
+      const long long block = quotient(pr, p.rb[1]);
+      in_prefix = static_cast<int>(pr - block * p.rb[1]);
+      y0 = (static_cast<long long>(hk) * p.prefix_blocks + block) * p.prefix_tiles;
+      d0 = cta_of(p.prefix_units, p.prefix_ctas, y0);
+      n_all += static_cast<int>(cta_of(p.prefix_units, p.prefix_ctas, y0 + p.prefix_tiles - 1) - d0) + 1;
+    }
+  }
+  // written by the one CTA that held it
+  __device__ __forceinline__ bool done(const PagedParams& p) const { return p.prefix_len == 0 && n_own == 1; }
+  // O and L of part i
+  __device__ __forceinline__ void at(const PagedParams& p, int d, int i, const float*& o, const float*& l) const {
+    const int pre = i < n_own ? 0 : 1, k = pre ? i - n_own : i;
+    if ((pre ? n_all - n_own : n_own) == 1) {
+      o = p.whole_o[pre] + row * d;
+      l = p.whole_l[pre] + row;
+      return;
+    }
+    const long long c = (pre ? d0 : c0) + k;
+    // a CTA's first segment is its piece 0; the row block is that one unless it starts inside the CTA
+    const long long first = pre ? cta_start(p.prefix_units, p.prefix_ctas, c) : cta_start(units, ctas, c);
+    const long long slot = 2 * c + (first >= (pre ? y0 : x0) ? 0 : 1);
+    const long long r = slot * p.rb[pre] + (pre ? in_prefix : in_own);
+    o = p.piece_o[pre] + r * d;
+    l = p.piece_l[pre] + r;
+  }
+};
 
-  // CTAs [c0, c1] that hold the row's own keys, [d0, d1] its prefix keys (c0 > c1: none)
-  const long long units = p.plan[0], ctas = p.plan[1];
-  const long long u0 = p.plan[2 + b];
-  const int blocks = row_blocks(p.rows, p.rb[0]);
-  const long long n = quotient(p.plan[3 + b] - u0, static_cast<long long>(p.Hk) * blocks);
-  const long long x0 = u0 + (static_cast<long long>(hk) * blocks + rr / p.rb[0]) * n;
-  long long c0 = 1, c1 = 0, d0 = 1, d1 = 0, y0 = 0;
-  if (n > 0) {
-    c0 = cta_of(units, ctas, x0);
-    c1 = cta_of(units, ctas, x0 + n - 1);
+template <int D>
+__device__ __forceinline__ void merge_load(const float* src, int lane, float (&v)[D / 32]) {
+  if constexpr (D == 128) {
+    const float4 t = *reinterpret_cast<const float4*>(src + lane * 4);
+    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+  } else {
+    const float2 t = *reinterpret_cast<const float2*>(src + lane * 2);
+    v[0] = t.x; v[1] = t.y;
   }
-  const long long pr = static_cast<long long>(b) * p.rows + rr;  // row among the K/V head's prefix rows
-  if (p.prefix_len > 0) {
-    const int nt = p.prefix_tiles;
-    y0 = (static_cast<long long>(hk) * p.prefix_blocks + quotient(pr, p.rb[1])) * nt;
-    d0 = cta_of(p.prefix_units, p.prefix_ctas, y0);
-    d1 = cta_of(p.prefix_units, p.prefix_ctas, y0 + nt - 1);
-  } else if (n > 0 && c0 == c1) {
-    return;  // written by the one CTA that held it
-  }
-  const int n_own = static_cast<int>(c1 - c0 + 1), n_all = n_own + static_cast<int>(d1 - d0 + 1);
+}
+template <int D>
+__device__ __forceinline__ void merge_store(const PagedParams& p, long long row, int lane, const float (&acc)[D / 32],
+                                            float top, float sum) {
+  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+  uint16_t* const dst = p.out + row * D + lane * (D / 32);
+  if constexpr (D == 128)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+  if (lane == 0) p.lse[row] = sum > 0.f ? (top + __log2f(sum)) * 0.69314718055994530942f : -__int_as_float(0x7f800000);
+}
+
+// Few rows: four warps per row take its parts in turn, each lane finds one part
+// and its L, and the warps meet in shared memory.
+template <int D>
+__global__ void __launch_bounds__(128) fa_paged_merge_row_kernel(const PagedParams p) {
+  constexpr int kPer = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  grid_wait();
+  grid_release();
+  RowParts parts;
+  parts.find(p, blockIdx.x);
+  if (parts.done(p)) return;
   float mx = NEG_INF, sum = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int base = sub; base < n_all; base += 32 * WARPS) {
-    // this lane's part: its O row and L
-    const int i = base + lane * WARPS;
+  for (int base = warp; base < parts.n_all; base += 128) {
+    const int i = base + lane * 4;
     const float* po = nullptr;
     float L = NEG_INF;
-    if (i < n_all) {
-      const int pre = i < n_own ? 0 : 1;
-      const long long a = pre ? d0 : c0, z = pre ? d1 : c1, start = pre ? y0 : x0;
-      long long at = row;
-      if (a != z) {
-        const long long c = a + (pre ? i - n_own : i);
-        // a CTA's first segment is its piece 0; the row block is that one unless it starts inside the CTA
-        const long long first = pre ? cta_start(p.prefix_units, p.prefix_ctas, c) : cta_start(units, ctas, c);
-        const long long slot = 2 * c + (first >= start ? 0 : 1);
-        at = slot * p.rb[pre] + (pre ? static_cast<unsigned>(pr) % p.rb[1] : rr % p.rb[0]);
-      }
-      po = (a == z ? p.whole_o[pre] : p.piece_o[pre]) + at * D;
-      L = ((a == z ? p.whole_l[pre] : p.piece_l[pre]))[at];
+    if (i < parts.n_all) {
+      const float* pl;
+      parts.at(p, D, i, po, pl);
+      L = *pl;
     }
+    const int count = min(32, (parts.n_all - base + 3) / 4);
+    auto src = [&](int k) -> const float* {
+      return reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), k));
+    };
+    // the first part's O travels beside the Ls
+    float v0[kPer];
+    merge_load<D>(src(0), lane, v0);
     float top = fmaxf(mx, L);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -715,61 +787,119 @@ __global__ void __launch_bounds__(128) fa_paged_merge_kernel(const PagedParams p
     for (int o = 16; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
     mx = top;
     sum = a * sum + ws;
+    const float w0 = __shfl_sync(0xffffffffu, wt, 0);
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] *= a;
-    const int count = min(32, (n_all - base + WARPS - 1) / WARPS);
+    for (int e = 0; e < kPer; ++e) acc[e] = a * acc[e] + w0 * v0[e];
 #pragma unroll 4
-    for (int k = 0; k < count; ++k) {
-      const float* src = reinterpret_cast<const float*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), k));
+    for (int k = 1; k < count; ++k) {
+      float v[kPer];
+      merge_load<D>(src(k), lane, v);
       const float c = __shfl_sync(0xffffffffu, wt, k);
-      if constexpr (kPer == 4) {
-        const float4 t = *reinterpret_cast<const float4*>(src + lane * 4);
-        acc[0] = fmaf(c, t.x, acc[0]);
-        acc[1] = fmaf(c, t.y, acc[1]);
-        acc[2] = fmaf(c, t.z, acc[2]);
-        acc[3] = fmaf(c, t.w, acc[3]);
-      } else {
-        const float2 t = *reinterpret_cast<const float2*>(src + lane * 2);
-        acc[0] = fmaf(c, t.x, acc[0]);
-        acc[1] = fmaf(c, t.y, acc[1]);
-      }
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] = fmaf(c, v[e], acc[e]);
     }
   }
-  if constexpr (WARPS == 4) {
-    __shared__ float sh[4][D + 2];
+  __shared__ float sh[4][D + 2];
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) sh[warp][lane * kPer + e] = acc[e];
-    if (lane == 0) {
-      sh[warp][D] = mx;
-      sh[warp][D + 1] = sum;
+  for (int e = 0; e < kPer; ++e) sh[warp][lane * kPer + e] = acc[e];
+  if (lane == 0) {
+    sh[warp][D] = mx;
+    sh[warp][D + 1] = sum;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  float top = NEG_INF;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = fmaxf(top, sh[i][D]);
+  sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+  if (top != NEG_INF) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float c = sh[i][D] == NEG_INF ? 0.f : ex2(sh[i][D] - top);
+      sum += c * sh[i][D + 1];
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) acc[e] += c * sh[i][lane * kPer + e];
     }
-    __syncthreads();
-    if (warp != 0) return;
-    float top = NEG_INF;
+  }
+  merge_store<D>(p, parts.row, lane, acc, top, sum);
+}
+
+// Many rows: one warp joins four of them at once.  Eight lanes find the parts
+// and Ls of each row, then the whole warp sums O row by row with D / 32 columns
+// to a lane, the four rows' loads in flight together.
+template <int D>
+__global__ void __launch_bounds__(128) fa_paged_merge_rows_kernel(const PagedParams p) {
+  constexpr int kPer = D / 32, kRows = 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float NEG_INF = -__int_as_float(0x7f800000);
+  const long long all = static_cast<long long>(p.B) * p.Hk * p.rows;
+  const long long row0 = (static_cast<long long>(blockIdx.x) * 4 + warp) * kRows;
+  grid_wait();
+  grid_release();
+  if (row0 >= all) return;
+  const int group = lane >> 3;
+  RowParts parts;
+  parts.find(p, min(row0 + group, all - 1));
+  const int n_mine = (row0 + group < all && !parts.done(p)) ? parts.n_all : 0;
+  const bool write = row0 + group < all && !parts.done(p);
+  const int most = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(n_mine));
+  float mx = NEG_INF, sum = 0.f;  // of this lane's row
+  float acc[kRows][kPer];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = fmaxf(top, sh[i][D]);
-    sum = 0.f;
+  for (int r = 0; r < kRows; ++r)
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    if (top != NEG_INF) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float c = sh[i][D] == NEG_INF ? 0.f : ex2(sh[i][D] - top);
-        sum += c * sh[i][D + 1];
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] += c * sh[i][lane * kPer + e];
-      }
+    for (int e = 0; e < kPer; ++e) acc[r][e] = 0.f;
+  for (int base = 0; base < most; base += 8) {
+    const int i = base + (lane & 7);
+    const float* po = p.whole_o[0];  // never read through for a missing part
+    float L = NEG_INF;
+    if (i < n_mine) {
+      const float* pl;
+      parts.at(p, D, i, po, pl);
+      L = *pl;
     }
+    float top = fmaxf(mx, L);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float a = mx == NEG_INF ? 0.f : ex2(mx - top);
+    const float wt = L == NEG_INF ? 0.f : ex2(L - top);
+    float ws = wt;
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, o);
     mx = top;
+    sum = a * sum + ws;
+    if (base > 0) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float ar = __shfl_sync(0xffffffffu, a, r * 8);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) acc[r][e] *= ar;
+      }
+    }
+    const int count = min(8, most - base);
+#pragma unroll 2
+    for (int k = 0; k < count; ++k) {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const float c = __shfl_sync(0xffffffffu, wt, r * 8 + k);
+        const float* const src = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), r * 8 + k));
+        if (c > 0.f) {
+          float v[kPer];
+          merge_load<D>(src, lane, v);
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) acc[r][e] = fmaf(c, v[e], acc[r][e]);
+        }
+      }
+    }
   }
-  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
-  uint16_t* const dst = p.out + row * D + lane * kPer;
-  if constexpr (kPer == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) p.lse[row] = sum > 0.f ? (mx + __log2f(sum)) * 0.69314718055994530942f : NEG_INF;
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const float top = __shfl_sync(0xffffffffu, mx, r * 8), tot = __shfl_sync(0xffffffffu, sum, r * 8);
+    if (__shfl_sync(0xffffffffu, static_cast<int>(write), r * 8)) merge_store<D>(p, row0 + r, lane, acc[r], top, tot);
+  }
 }
 
 }  // namespace fa

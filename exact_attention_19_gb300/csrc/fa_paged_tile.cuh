@@ -67,6 +67,11 @@ enum : int {
 constexpr uint32_t kTileScratchOff = 256, kTileTmemOff = 448, kTileAbortOff = 452;
 constexpr uint32_t kTileWalkOff = 512;  // the softmax warps' walks, after the 512-byte block
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(src)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // The tiles [jlo, jhi) of the CTA's part that some row of the block sees.
 template <int RB, int TILE, bool PREFIX>
 __device__ __forceinline__ void seen_tiles(const PagedParams& p, const PagedWalk& w, int& jlo, int& jhi) {
@@ -117,15 +122,6 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
   };
   auto uniform = [](bool v) -> bool { return __all_sync(0xffffffffu, v); };
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (base & 1023u) {  // the swizzled layouts need it; the launch places it so
-    if (threadIdx.x == 0) atomicOr(p.status, kPagedTimeout | (16u << 8));
-    return;
-  }
-  PagedWalk w;
-  if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(
-          p, reinterpret_cast<long long*>(tile_smem + C::kBarOff + kTileScratchOff), w))
-    return;
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kTBarQ + i), 64);
@@ -140,6 +136,20 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
     for (int i = 0; i < 2 * C::kRing; ++i) mbar_init(bar(kTBarRing + i), 1);
     *abort_flag = 0;
     mbar_init_fence();
+    tma_prefetch_map(&tmK);
+    tma_prefetch_map(&tmV);
+  }
+  paged_begin<PREFIX>(p);
+  if (base & 1023u) {  // the swizzled layouts need it; the launch places it so
+    if (threadIdx.x == 0) atomicOr(p.status, kPagedTimeout | (16u << 8));
+    paged_end<PREFIX>(p);
+    return;
+  }
+  PagedWalk w;
+  if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(
+          p, reinterpret_cast<long long*>(tile_smem + C::kBarOff + kTileScratchOff), w)) {
+    paged_end<PREFIX>(p);
+    return;
   }
   if (warp == C::kWarpMma) {
     tmem_alloc(smem_addr(tmem_slot), C::kTmemCols);
@@ -154,8 +164,6 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
     regs_dec<C::kRegMisc>();
     if (warp == C::kWarpProd) {
       // ======================= TMA producer =================================
-      tma_prefetch_map(&tmK);
-      tma_prefetch_map(&tmV);
       const int chunk_rows = min(1 << p.page_shift, C::kTile);  // keys of one box: smaller pages take several
       const int piece = lane / C::kBoxes, x = lane % C::kBoxes;
       const bool mine = lane < C::kTile / chunk_rows * C::kBoxes;
@@ -339,21 +347,24 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
         const int use = PAIR ? seg : seg >> 1;      // earlier segments that used it
         ok = uniform(mbar_wait(bar(kTBarQFree + q), (use & 1) ^ 1, abort_flag));
         if (!ok) break;
-#pragma unroll 1
-        for (int r = tid; r < C::kRows; r += 64) {
+        // asynchronous 16-byte copies: every row of the block is in flight at once
+        long long row[C::kRows / 64];
+#pragma unroll
+        for (int i = 0; i < C::kRows / 64; ++i) {
           int lo, hi;
-          const long long row = S::row(p, w, r, lo, hi);
-          if (row >= 0) {  // other rows of the tile keep what they hold: nothing of them is used
-            const uint4* const src = reinterpret_cast<const uint4*>(p.q + row * D);
-            const uint32_t dst = base + (PAIR ? r >> 7 : q) * C::kTileBytes + (r & 127) * 128;
-            uint4 v[D / 8];
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) v[i] = __ldg(src + i);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              st_shared_v4(dst + (i >> 3) * C::kBox + (((i & 7) ^ (r & 7)) << 4), v[i].x, v[i].y, v[i].z, v[i].w);
-          }
+          row[i] = S::row(p, w, tid + 64 * i, lo, hi);
         }
+#pragma unroll
+        for (int i = 0; i < C::kRows / 64; ++i) {
+          if (row[i] < 0) continue;  // such a row keeps what it holds: nothing of it is used
+          const int r = tid + 64 * i;
+          const uint16_t* const src = p.q + row[i] * D;
+          const uint32_t dst = base + (PAIR ? r >> 7 : q) * C::kTileBytes + (r & 127) * 128;
+#pragma unroll
+          for (int e = 0; e < D / 8; ++e)
+            cp_async16(dst + (e >> 3) * C::kBox + (((e & 7) ^ (r & 7)) << 4), src + e * 8);
+        }
+        cp_async_wait_all();
         fence_proxy_async_smem();
         mbar_arrive(bar(kTBarQ + q));
         if (PAIR) mbar_arrive(bar(kTBarQ + 1));
@@ -592,9 +603,12 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
                                pack_bf16(f[8 * h + 4], f[8 * h + 5]), pack_bf16(f[8 * h + 6], f[8 * h + 7]));
             } else {
 #pragma unroll
-              for (int h = 0; h < 8; ++h)
-                *reinterpret_cast<float4*>(dst32 + cc * 32 + h * 4) =
-                    make_float4(f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]);
+              for (int h = 0; h < 4; ++h) {  // whole 32-byte sectors: the workspace's parts are 256-byte aligned
+                uint32_t v8[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v8[e] = __float_as_uint(f[8 * h + e]);
+                st_global_v8(dst32 + cc * 32 + h * 8, v8);
+              }
             }
           }
         }
@@ -622,6 +636,7 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  paged_end<PREFIX>(p);
 }
 
 }  // namespace fa
