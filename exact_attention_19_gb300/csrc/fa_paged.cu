@@ -96,7 +96,7 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
       l.prefix_blocks = fa::row_blocks(rows * B, l.rb[1]);
       l.prefix_tiles = (prefix_len + tile_keys(l.rb[1]) - 1) / tile_keys(l.rb[1]);
       l.prefix_units = 1ll * Hk * l.prefix_blocks * l.prefix_tiles;
-      l.prefix_ctas = fa::paged_ctas(l.grid[1], l.prefix_units);
+      l.prefix_ctas = fa::paged_ctas(l.grid[1], l.prefix_units, l.rb[1]);
       l.grid[1] = static_cast<int>(l.prefix_ctas);
     }
     const size_t pieces = 2 * static_cast<size_t>(l.grid[i]) * l.rb[i];
@@ -109,7 +109,7 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
 }
 
 // Rows from which one warp of the merge joins four rows; below, four warps join one.
-constexpr long long kMergeRows = 2048;
+constexpr long long kMergeRows = 8192;
 
 // Programmatic dependent launch: the kernel may be scheduled while the one ahead
 // of it on the stream still runs, and waits on the device (paged_begin) for what

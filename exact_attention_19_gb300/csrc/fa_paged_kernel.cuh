@@ -88,9 +88,11 @@ __device__ __forceinline__ int row_prefix_keys(const PagedParams& p, const SeqKe
   return (t < s.fresh && s.len - s.fresh + t >= 0) ? p.prefix_len : 0;
 }
 
-// CTAs that `units` units are shared among: at least two units each.
-__host__ __device__ __forceinline__ long long paged_ctas(long long grid, long long units) {
-  const long long most = units / 2;
+// CTAs that `units` units of a row block of rb rows are shared among: at least so
+// many units each that the parts' O (rb * D * 4 bytes, written and read again)
+// stays small beside the keys they read (256 D bytes a key tile of 64, 512 of 128).
+__host__ __device__ __forceinline__ long long paged_ctas(long long grid, long long units, int rb) {
+  const long long most = units / (rb == 16 ? 2 : rb == 128 ? 4 : 8);
   return most < 1 ? 1 : (most < grid ? most : grid);
 }
 // a / b for a >= 0, b > 0: a 32-bit division where both fit (a 64-bit one is a long instruction sequence)
@@ -342,7 +344,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
         __syncthreads();
       }
       if (pass == 0) {
-        const long long ctas = paged_ctas(gridDim.x, run);
+        const long long ctas = paged_ctas(gridDim.x, run, RB);
         if (blockIdx.x == 0 && threadIdx.x == 0) {
           p.plan[0] = run;
           p.plan[1] = ctas;

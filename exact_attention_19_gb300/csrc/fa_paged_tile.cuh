@@ -347,22 +347,28 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
         const int use = PAIR ? seg : seg >> 1;      // earlier segments that used it
         ok = uniform(mbar_wait(bar(kTBarQFree + q), (use & 1) ^ 1, abort_flag));
         if (!ok) break;
-        // asynchronous 16-byte copies: every row of the block is in flight at once
+        // asynchronous 16-byte copies, all of the block's rows in flight at once.  Each lane finds its rows
+        // (32 to a warp and turn), then D / 8 lanes together copy one row, so that a copy instruction touches
+        // whole 128-byte lines (one row per lane touched 32 lines each: Q took 4.6 us to arrive, not 1.9).
+        constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+        const int half = tid >> 5;
         long long row[C::kRows / 64];
 #pragma unroll
         for (int i = 0; i < C::kRows / 64; ++i) {
           int lo, hi;
-          row[i] = S::row(p, w, tid + 64 * i, lo, hi);
+          row[i] = S::row(p, w, 64 * i + tid, lo, hi);
         }
 #pragma unroll
         for (int i = 0; i < C::kRows / 64; ++i) {
-          if (row[i] < 0) continue;  // such a row keeps what it holds: nothing of it is used
-          const int r = tid + 64 * i;
-          const uint16_t* const src = p.q + row[i] * D;
-          const uint32_t dst = base + (PAIR ? r >> 7 : q) * C::kTileBytes + (r & 127) * 128;
-#pragma unroll
-          for (int e = 0; e < D / 8; ++e)
-            cp_async16(dst + (e >> 3) * C::kBox + (((e & 7) ^ (r & 7)) << 4), src + e * 8);
+#pragma unroll 4
+          for (int s = 0; s < 32; s += kAtOnce) {
+            const int from = s + lane / kLanes, e = lane % kLanes, r = 64 * i + 32 * half + from;
+            const long long src = __shfl_sync(0xffffffffu, row[i], from);
+            if (src >= 0)  // a row that does not exist keeps what it holds: nothing of it is used
+              cp_async16(base + (PAIR ? r >> 7 : q) * C::kTileBytes + (r & 127) * 128 + (e >> 3) * C::kBox +
+                             (((e & 7) ^ (r & 7)) << 4),
+                         p.q + src * D + e * 8);
+          }
         }
         cp_async_wait_all();
         fence_proxy_async_smem();
