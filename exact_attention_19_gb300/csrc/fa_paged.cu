@@ -68,7 +68,7 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 // Rows per row block, by the rows that share each K/V byte: the warp-level
 // kernel's 16, or the tcgen05 kernel's 128 or 256.
 int block_rows(long long rows) { return rows <= 16 ? 16 : (rows <= 128 ? 128 : 256); }
-int tile_keys(int block_rows) { return block_rows == 16 ? 64 : 128; }
+constexpr int kTileKeys = 128;  // keys of a unit in either kernel
 int grid_of(int block_rows, int sms) { return block_rows == 16 ? 2 * sms : sms; }  // all CTAs resident
 
 // The row blocks, tiles and CTAs of a call, and the parts of its workspace, in
@@ -94,7 +94,7 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
     l.grid[i] = grid_of(l.rb[i], sms);
     if (i == 1) {
       l.prefix_blocks = fa::row_blocks(rows * B, l.rb[1]);
-      l.prefix_tiles = (prefix_len + tile_keys(l.rb[1]) - 1) / tile_keys(l.rb[1]);
+      l.prefix_tiles = (prefix_len + kTileKeys - 1) / kTileKeys;
       l.prefix_units = 1ll * Hk * l.prefix_blocks * l.prefix_tiles;
       l.prefix_ctas = fa::paged_ctas(l.grid[1], l.prefix_units, l.rb[1]);
       l.grid[1] = static_cast<int>(l.prefix_ctas);
@@ -152,7 +152,7 @@ template <int D, bool PREFIX>
 int launch_part(const Caches& c, const fa::PagedParams& p, int grid, cudaStream_t stream) {
   const int rb = p.rb[PREFIX];
   CUtensorMap mk, mv;
-  if (!c.maps(&mk, &mv, rb == 16 ? fa::PagedCfg<D>::kKeys : tile_keys(rb))) return FA_ERR_LAUNCH;
+  if (!c.maps(&mk, &mv, rb == 16 ? fa::PagedCfg<D>::kKeys : kTileKeys)) return FA_ERR_LAUNCH;
   if (rb == 16) {
     using S = fa::PagedCfg<D>;
     return launch_kernel(fa::fa_paged_kernel<D, PREFIX>, grid, S::kThreads, S::kSmemBytes, stream, mk, mv, p);

@@ -90,9 +90,9 @@ __device__ __forceinline__ int row_prefix_keys(const PagedParams& p, const SeqKe
 
 // CTAs that `units` units of a row block of rb rows are shared among: at least so
 // many units each that the parts' O (rb * D * 4 bytes, written and read again)
-// stays small beside the keys they read (256 D bytes a key tile of 64, 512 of 128).
+// stays small beside the keys they read (512 D bytes a tile of 128).
 __host__ __device__ __forceinline__ long long paged_ctas(long long grid, long long units, int rb) {
-  const long long most = units / (rb == 16 ? 2 : rb == 128 ? 4 : 8);
+  const long long most = units / (rb == 16 ? 1 : rb == 128 ? 4 : 8);
   return most < 1 ? 1 : (most < grid ? most : grid);
 }
 // a / b for a >= 0, b > 0: a 32-bit division where both fit (a 64-bit one is a long instruction sequence)
@@ -230,20 +230,23 @@ struct PagedSchedule {
 // Decoding is bound by reading K and V once: 2 D multiply-adds per row and
 // 2-byte element leave a block of 16 rows far below the tensor rate, so the
 // warp-level m16n8k16 MMA (fed from registers) carries it, and each warp runs
-// alone: it streams its own 16 keys of every 64-key tile through its own ring
-// of TMA boxes (4 KB each at D = 128), holds its own running maximum, sum and O
-// accumulator, and meets the other warps only at the end of a row block.  No
-// barrier between warps stands in the loop, so their waits overlap.
+// alone: it streams its own 32 keys of every 128-key tile through its own ring
+// of TMA boxes, holds its own running maximum, sum and O accumulator, and meets
+// the other warps only at the end of a row block.  No barrier between warps
+// stands in the loop, so their waits overlap.  With eight warps on an SM the
+// instructions per key matter: 32 keys to a step, not 16, and the page indices
+// of 32 steps held by the lanes.
 template <int D>
 struct PagedCfg {
   static constexpr int kWarps = 4, kThreads = 128;
-  static constexpr int kRows = 16, kKeys = 16, kTile = kWarps * kKeys;
+  static constexpr int kRows = 16, kKeys = 32, kTile = kWarps * kKeys;
   static constexpr int kBoxes = D / 64;
   static constexpr uint32_t kBoxBytes = kKeys * 128u;
-  static constexpr uint32_t kItemBytes = kBoxes * kBoxBytes;  // 16 keys of K or of V
-  static constexpr int kRing = D == 128 ? 5 : 10;             // items per warp: 20 KB in flight
+  static constexpr uint32_t kItemBytes = kBoxes * kBoxBytes;  // 32 keys of K or of V
+  static constexpr int kRing = D == 128 ? 3 : 6;              // items per warp: 24 KB
   static constexpr uint32_t kRingBytes = kWarps * kRing * kItemBytes;
-  static constexpr int kMergeStride = D / 2 + 8;  // floats; + 8 spreads the rows over the banks
+  static constexpr int kMergeStride = 40;  // floats of a row in the merge buffer: 32 columns at a time, + 8 spreads
+                                           // the rows over the banks
   static constexpr uint32_t kMergeOff = kRingBytes;
   static constexpr uint32_t kStatOff = kMergeOff + kWarps * 16 * kMergeStride * 4;
   static constexpr uint32_t kBarOff = kStatOff + kWarps * 16 * 8;
@@ -397,59 +400,91 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
   const long long first_g = w.g;
   __syncthreads();
 
+  // the tiles [j0, j1) of a segment part in which this warp has keys
+  auto mine = [&](const PagedWalk& v, int from, int& j0, int& j1) {
+    const int k = v.tile0 * C::kTile + warp * C::kKeys;  // first key in the segment's first tile
+    j0 = max(from, k + C::kKeys > v.lo ? 0 : 1);
+    j1 = min(v.jend, (max(v.hi - k, 0) + C::kTile - 1) / C::kTile);
+  };
+
   // ---- this warp's stream of TMA items -----------------------------------
-  // The fetch side walks the same segments ahead of the products: K then V of
-  // every 16-key piece in range, one page index read ahead.
+  // The fetch side walks the same segments ahead of the products, up to 32
+  // steps (of one K and one V item) at a time: lane i holds the page indices of
+  // step i, and those of the 32 after them are being read meanwhile.
+  const int chunk = min(1 << p.page_shift, C::kKeys);  // keys of a box: a step takes two of pages of 16
+  const int half = lane / C::kBoxes, box = lane % C::kBoxes;
+  const bool issues = lane < C::kKeys / chunk * C::kBoxes;
   PagedWalk f = w;
-  int f_j = w.j;  // next tile of f
-  int f_k0 = 0, f_hk = 0, f_page = 0, n_k0 = 0, n_hk = 0, n_page = 0;
-  bool f_more = true, n_more = true, f_is_v = false;
-  int f_slot = 0;  // ring slot of the next item
-  auto seek = [&]() {  // n_*: the next 16-key piece of this warp, n_more false when none is left
-    for (;;) {
-      while (f_j < f.jend) {
-        const int k0 = (f.tile0 + f_j++) * C::kTile + warp * C::kKeys;
-        if (k0 < f.hi && k0 + C::kKeys > f.lo) {
-          n_page = __ldg(S::pages(p, f) + (k0 >> p.page_shift));
-          n_k0 = k0;
-          n_hk = f.hk;
-          return;
+  int f_from = w.j;
+  int f_i = 0, f_n = 0, f_key = 0, f_hk = 0, f_lo = 0, f_hi = 0, f_page = 0, f_page2 = 0;  // steps being fetched
+  int n_n = 0, n_key = 0, n_hk = 0, n_lo = 0, n_hi = 0, n_page = 0, n_page2 = 0;           // the ones after them
+  bool f_more = true;
+  auto advance = [&]() {
+    f_i = 0;
+    f_n = n_n;
+    f_key = n_key;
+    f_hk = n_hk;
+    f_lo = n_lo;
+    f_hi = n_hi;
+    f_page = n_page;
+    f_page2 = n_page2;
+    n_n = 0;
+    while (f_more) {
+      int j0, j1;
+      mine(f, f_from, j0, j1);
+      if (j0 < j1) {
+        n_n = min(32, j1 - j0);
+        n_key = (f.tile0 + j0) * C::kTile + warp * C::kKeys;
+        n_hk = f.hk;
+        n_lo = f.lo;
+        n_hi = f.hi;
+        f_from = j0 + n_n;
+        const int k = n_key + lane * C::kTile;
+        const int* const pages = S::pages(p, f);
+        n_page = n_page2 = -1;
+        if (lane < n_n) {
+          if (k + chunk > f.lo) n_page = __ldg(pages + (k >> p.page_shift));
+          if (chunk < C::kKeys && k + chunk < f.hi) n_page2 = __ldg(pages + (k >> p.page_shift) + 1);
         }
-      }
-      if (!S::next(p, f)) {
-        n_more = false;
         return;
       }
-      f_j = f.j;
+      f_more = S::next(p, f);
+      f_from = f.j;
     }
   };
-  auto take = [&]() {  // the piece sought becomes the one being fetched; seek the one after it
-    f_more = n_more;
-    f_k0 = n_k0;
-    f_hk = n_hk;
-    f_page = n_page;
-    if (n_more) seek();
-  };
-  int issued = 0, consumed = 0;
-  auto issue = [&]() {  // one item into f_slot, which is free
-    if (!f_more) return;
-    if (lane == 0) {
-      const uint32_t bar = bars + 8 * f_slot, dst = ring + f_slot * C::kItemBytes;
-      if (!f_is_v && static_cast<unsigned>(f_page) >= static_cast<unsigned>(p.n_pages)) atomicOr(p.status, kPagedPage);
-      mbar_arrive_expect_tx(bar, C::kItemBytes);
-      const int slot = f_k0 & ((1 << p.page_shift) - 1);
-#pragma unroll
-      for (int x = 0; x < C::kBoxes; ++x)
-        tma_load_4d(dst + x * C::kBoxBytes, f_is_v ? &tmV : &tmK, bar, x * 64, slot, f_hk, f_page);
+  int f_slot = 0, issued = 0, consumed = 0;
+  auto fetch = [&](auto what) {  // the next item into f_slot, which is free
+    constexpr bool is_v = decltype(what)::value;
+    if (f_i >= f_n) return;
+    const uint32_t bar = bars + 8 * f_slot;
+    const int page_a = __shfl_sync(0xffffffffu, f_page, f_i), page_b = __shfl_sync(0xffffffffu, f_page2, f_i);
+    const int key = f_key + f_i * C::kTile + half * chunk, page = half ? page_b : page_a;
+    const bool wanted = issues && key < f_hi && key + chunk > f_lo;
+    const unsigned boxes = __popc(__ballot_sync(0xffffffffu, wanted));
+    if (lane == 0) mbar_arrive_expect_tx(bar, boxes * chunk * 128u);
+    if (wanted) {
+      if (!is_v && static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) atomicOr(p.status, kPagedPage);
+      tma_load_4d(ring + f_slot * C::kItemBytes + box * C::kBoxBytes + half * chunk * 128, is_v ? &tmV : &tmK, bar,
+                  box * 64, key & ((1 << p.page_shift) - 1), f_hk, page);
     }
     ++issued;
     f_slot = f_slot + 1 == C::kRing ? 0 : f_slot + 1;
-    if (f_is_v) take();
-    f_is_v = !f_is_v;
+    if constexpr (is_v) {
+      if (++f_i == f_n) advance();
+    }
   };
-  seek();
-  take();
-  for (int i = 0; i < C::kRing; ++i) issue();
+  constexpr std::false_type kItemK{};
+  constexpr std::true_type kItemV{};
+  advance();
+  advance();
+  // the ring is filled in the order K V K V ...; the products free a K item, then a V item, so with an odd
+  // ring a freed K makes room for a V and the other way round
+#pragma unroll 1
+  for (int i = 0; i < C::kRing / 2; ++i) {
+    fetch(kItemK);
+    fetch(kItemV);
+  }
+  if constexpr (C::kRing % 2) fetch(kItemK);
 
   int c_slot = 0;
   uint32_t c_phase = 0;
@@ -464,11 +499,11 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     }
     return ring + c_slot * C::kItemBytes;
   };
-  auto free_item = [&]() {
+  auto free_item = [&](auto next_is_v) {
     if (ok) {
       ++consumed;
       __syncwarp();
-      issue();
+      fetch(next_is_v);
     }
     if (++c_slot == C::kRing) {
       c_slot = 0;
@@ -499,49 +534,59 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     for (int i = 0; i < kNT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float m[2] = {NEG_INF, NEG_INF}, l[2] = {0.f, 0.f};  // base-2 scaled units; l: this thread's share
 
-    for (int j = w.j; j < w.jend; ++j) {
+    int j0, j1;
+    mine(w, w.j, j0, j1);
+    for (int j = j0; j < j1; ++j) {
       const int k0 = (w.tile0 + j) * C::kTile + warp * C::kKeys;
-      if (!(k0 < w.hi && k0 + C::kKeys > w.lo)) continue;
-      // S = Q K^T over 16 keys
+      // S = Q K^T over 32 keys
       const uint32_t kt = wait_item();
-      float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      float s[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
       const int mi = lane >> 3, r8 = lane & 7;
       if (ok) {
-        const int row = (mi >> 1) * 8 + r8;  // key
+        const int row = (mi >> 1) * 8 + r8;  // key (and key + 16)
 #pragma unroll
         for (int kk = 0; kk < kKT; ++kk) {
+          const uint32_t chunk16 = static_cast<uint32_t>((kk & 3) * 2 + (mi & 1));
+          const uint32_t at = kt + (kk >> 2) * C::kBoxBytes + row * 128 + ((chunk16 ^ static_cast<uint32_t>(row & 7)) << 4);
           uint32_t b0, b1, b2, b3;
-          const uint32_t chunk = static_cast<uint32_t>((kk & 3) * 2 + (mi & 1));
-          ldmatrix4(kt + (kk >> 2) * C::kBoxBytes + row * 128 + ((chunk ^ static_cast<uint32_t>(row & 7)) << 4), b0, b1,
-                    b2, b3);
+          ldmatrix4(at, b0, b1, b2, b3);
           mma16816(s[0], qf[kk], b0, b1);
           mma16816(s[1], qf[kk], b2, b3);
+          ldmatrix4(at + 16 * 128, b0, b1, b2, b3);
+          mma16816(s[2], qf[kk], b0, b1);
+          mma16816(s[3], qf[kk], b2, b3);
         }
       }
-      free_item();
+      free_item(std::integral_constant<bool, C::kRing % 2 != 0>{});
       // masks: rows' own bounds
       const bool cut = k0 < max(lo[0], lo[1]) || k0 + C::kKeys > min(hi[0], hi[1]);
       if (__any_sync(0xffffffffu, cut)) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int key = k0 + i * 8 + q4 * 2 + (e & 1);
             if (key < lo[e >> 1] || key >= hi[e >> 1]) s[i][e] = NEG_INF;
           }
       }
-      uint32_t pf[4];
+      float m_new[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+        float mx = fmaxf(fmax3(s[0][2 * i], s[0][2 * i + 1], s[1][2 * i]), fmax3(s[1][2 * i + 1], s[2][2 * i], s[2][2 * i + 1]));
+        mx = fmax3(mx, s[3][2 * i], s[3][2 * i + 1]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float m_new = fmaxf(m[i], mx * p.scale_log2);
-        // the running maximum is exact here (no threshold), so the largest
-        // probability of a row is 1 and its bf16 rounding is exact
-        if (__any_sync(0xffffffffu, m_new > m[i])) {
-          const float alpha = m[i] == NEG_INF ? 0.f : ex2(m[i] - m_new);
-          m[i] = m_new;
+        m_new[i] = fmaxf(m[i], mx * p.scale_log2);
+      }
+      // the running maximum is exact here (no threshold), so the largest
+      // probability of a row is 1 and its bf16 rounding is exact
+      if (__any_sync(0xffffffffu, m_new[0] > m[0] || m_new[1] > m[1])) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float alpha = m[i] == NEG_INF ? 0.f : ex2(m[i] - m_new[i]);
+          m[i] = m_new[i];
           l[i] *= alpha;
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
@@ -549,39 +594,55 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
             o[n][2 * i + 1] *= alpha;
           }
         }
+      }
+      uint32_t pf[2][4];  // P in bf16 for the product, as in fa_fwd
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
         const float ref = m[i] == NEG_INF ? 0.f : -m[i];
-        const float e0 = ex2(fmaf(s[0][2 * i], p.scale_log2, ref)), e1 = ex2(fmaf(s[0][2 * i + 1], p.scale_log2, ref));
-        const float e2 = ex2(fmaf(s[1][2 * i], p.scale_log2, ref)), e3 = ex2(fmaf(s[1][2 * i + 1], p.scale_log2, ref));
-        l[i] += (e0 + e1) + (e2 + e3);
-        pf[i] = pack_bf16(e0, e1);  // P in bf16 for the product, as in fa_fwd
-        pf[2 + i] = pack_bf16(e2, e3);
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const float e0 = ex2(fmaf(s[n][2 * i], p.scale_log2, ref)), e1 = ex2(fmaf(s[n][2 * i + 1], p.scale_log2, ref));
+          sum += e0 + e1;
+          pf[n >> 1][(n & 1) * 2 + i] = pack_bf16(e0, e1);
+        }
+        l[i] += sum;
       }
       // O += P V; keys outside the segment's range may hold anything (the end
       // of a page, a page given back): their V counts as zero, as 0 * NaN would not
       const uint32_t vt = wait_item();
       if (ok) {
-        const int row = (mi & 1) * 8 + r8;  // key
-        const bool edge = k0 < w.lo || k0 + C::kKeys > w.hi;
-        uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-        if (edge) {
+        const int row = (mi & 1) * 8 + r8;  // key (and key + 16)
+        auto product = [&](auto edge) {
+          constexpr bool masked = decltype(edge)::value;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int key = k0 + i * 8 + q4 * 2;
-            keep[i] = ((key >= w.lo && key < w.hi) ? 0xffffu : 0u) |
-                      ((key + 1 >= w.lo && key + 1 < w.hi) ? 0xffff0000u : 0u);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
+            if constexpr (masked) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const int key = k0 + h * 16 + i * 8 + q4 * 2;
+                keep[i] = ((key >= w.lo && key < w.hi) ? 0xffffu : 0u) |
+                          ((key + 1 >= w.lo && key + 1 < w.hi) ? 0xffff0000u : 0u);
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < kNT; n += 2) {
+              uint32_t b0, b1, b2, b3;
+              const uint32_t chunk16 = static_cast<uint32_t>((n & 7) + (mi >> 1));
+              ldmatrix4_t(vt + (n >> 3) * C::kBoxBytes + (h * 16 + row) * 128 +
+                              ((chunk16 ^ static_cast<uint32_t>(row & 7)) << 4),
+                          b0, b1, b2, b3);
+              if constexpr (masked) b0 &= keep[0], b1 &= keep[1], b2 &= keep[0], b3 &= keep[1];
+              mma16816(o[n], pf[h], b0, b1);
+              mma16816(o[n + 1], pf[h], b2, b3);
+            }
           }
-        }
-#pragma unroll
-        for (int n = 0; n < kNT; n += 2) {
-          uint32_t b0, b1, b2, b3;
-          const uint32_t chunk = static_cast<uint32_t>((n & 7) + (mi >> 1));
-          ldmatrix4_t(vt + (n >> 3) * C::kBoxBytes + row * 128 + ((chunk ^ static_cast<uint32_t>(row & 7)) << 4), b0,
-                      b1, b2, b3);
-          mma16816(o[n], pf, b0 & keep[0], b1 & keep[1]);
-          mma16816(o[n + 1], pf, b2 & keep[0], b3 & keep[1]);
-        }
+        };
+        if (k0 < w.lo || k0 + C::kKeys > w.hi) product(std::true_type{});
+        else product(std::false_type{});
       }
-      free_item();
+      free_item(std::integral_constant<bool, C::kRing % 2 == 0>{});
     }
 
     // ---- join the four warps: each ends with D / 4 columns of all rows ----
@@ -590,48 +651,56 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
     }
-    float acc[kNT / 2][4];
-    auto exchange = [&](const int other, const bool upper, auto& from, auto& to, auto half) {
-      // this warp keeps the upper (or lower) half of its columns and gets the
-      // other warp's values of the same columns
-      constexpr int kHalf = decltype(half)::value;
-      float* const mine = merge + warp * 16 * C::kMergeStride;
-      __syncthreads();  // the buffer is free
+    // This warp keeps the upper (or lower) half of its columns and gets the
+    // other warp's values of them, 32 columns at a time.
+    auto exchange = [&](const int other, const bool upper, auto& from, auto& to, auto half_tiles) {
+      constexpr int kHalf = decltype(half_tiles)::value, kStep = kHalf < 4 ? kHalf : 4;
+      float* const out = merge + warp * 16 * C::kMergeStride;
+      const float* const theirs = merge + other * 16 * C::kMergeStride;
+      float a[2], c[2];
 #pragma unroll
-      for (int n = 0; n < kHalf; ++n) {
+      for (int n0 = 0; n0 < kHalf; n0 += kStep) {
+        __syncthreads();  // the buffer is free
+#pragma unroll
+        for (int n = 0; n < kStep; ++n) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float x = upper ? from[n0 + n][2 * i] : from[kHalf + n0 + n][2 * i];
+            const float y = upper ? from[n0 + n][2 * i + 1] : from[kHalf + n0 + n][2 * i + 1];
+            *reinterpret_cast<float2*>(out + (g8 + 8 * i) * C::kMergeStride + n * 8 + 2 * q4) = make_float2(x, y);
+          }
+        }
+        if (n0 == 0 && q4 == 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            *reinterpret_cast<float2*>(stat + (warp * 16 + g8 + 8 * i) * 2) = make_float2(m[i], l[i]);
+        }
+        __syncthreads();
+        if (n0 == 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 ml = *reinterpret_cast<const float2*>(stat + (other * 16 + g8 + 8 * i) * 2);
+            const float m_new = fmaxf(m[i], ml.x);
+            a[i] = m[i] == NEG_INF ? 0.f : ex2(m[i] - m_new);
+            c[i] = ml.x == NEG_INF ? 0.f : ex2(ml.x - m_new);
+            m[i] = m_new;
+            l[i] = a[i] * l[i] + c[i] * ml.y;
+          }
+        }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float x = upper ? from[n][2 * i] : from[kHalf + n][2 * i];
-          const float y = upper ? from[n][2 * i + 1] : from[kHalf + n][2 * i + 1];
-          *reinterpret_cast<float2*>(mine + (g8 + 8 * i) * C::kMergeStride + n * 8 + 2 * q4) = make_float2(x, y);
-        }
-      }
-      if (q4 == 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          *reinterpret_cast<float2*>(stat + (warp * 16 + g8 + 8 * i) * 2) = make_float2(m[i], l[i]);
-      }
-      __syncthreads();
-      const float* const theirs = merge + other * 16 * C::kMergeStride;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 ml = *reinterpret_cast<const float2*>(stat + (other * 16 + g8 + 8 * i) * 2);
-        const float m_new = fmaxf(m[i], ml.x);
-        const float a = m[i] == NEG_INF ? 0.f : ex2(m[i] - m_new);
-        const float c = ml.x == NEG_INF ? 0.f : ex2(ml.x - m_new);
-        m[i] = m_new;
-        l[i] = a * l[i] + c * ml.y;
-#pragma unroll
-        for (int n = 0; n < kHalf; ++n) {
-          const float2 t =
-              *reinterpret_cast<const float2*>(theirs + (g8 + 8 * i) * C::kMergeStride + n * 8 + 2 * q4);
-          const float x = upper ? from[kHalf + n][2 * i] : from[n][2 * i];
-          const float y = upper ? from[kHalf + n][2 * i + 1] : from[n][2 * i + 1];
-          to[n][2 * i] = a * x + c * t.x;
-          to[n][2 * i + 1] = a * y + c * t.y;
+          for (int n = 0; n < kStep; ++n) {
+            const float2 t = *reinterpret_cast<const float2*>(theirs + (g8 + 8 * i) * C::kMergeStride + n * 8 + 2 * q4);
+            const float x = upper ? from[kHalf + n0 + n][2 * i] : from[n0 + n][2 * i];
+            const float y = upper ? from[kHalf + n0 + n][2 * i + 1] : from[n0 + n][2 * i + 1];
+            to[n0 + n][2 * i] = a[i] * x + c[i] * t.x;
+            to[n0 + n][2 * i + 1] = a[i] * y + c[i] * t.y;
+          }
         }
       }
     };
+    float acc[kNT / 2][4];
     exchange(warp ^ 1, (warp & 1) != 0, o, acc, std::integral_constant<int, kNT / 2>{});
     float fin[kNT / 4][4];
     exchange(warp ^ 2, (warp & 2) != 0, acc, fin, std::integral_constant<int, kNT / 4>{});
