@@ -4,7 +4,9 @@ Five translation units: fa_api.cu (the C-ABI front end with every dense
 forward, split-KV merge and backward kernel instantiation), fa_rope.cu (rotary
 positions and the paged cache's append), fa_paged.cu (attention over the paged
 cache), fa_probe.cu (the exp2-throughput probe) and fa_selftest.cu (the
-bounded-wait self-test), compiled in parallel by one nvcc call.
+bounded-wait self-test), compiled in parallel by one nvcc call; beside them
+fa_torch.so, the host-side fast path of the torch entry points (fa_torch.cpp,
+the host compiler against torch's headers).
 """
 from __future__ import annotations
 
@@ -25,6 +27,10 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_ptx.cuh", "fa_host.h", "fa
                                                        "fa_paged_kernel.cuh", "fa_paged_tile.cuh")] + [
     os.path.join(INCLUDE, "fa.h")]
 
+TORCH_LIB_PATH = os.path.join(LIB_DIR, "fa_torch.so")
+TORCH_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
+TORCH_DEPS = [TORCH_SOURCE, os.path.join(INCLUDE, "fa.h")]
+
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -43,23 +49,52 @@ def command(out: str = LIB_PATH, verbose_ptxas: bool = False) -> list[str]:
     return cmd
 
 
+def torch_command(out: str = TORCH_LIB_PATH) -> list[str]:
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")]
+    lib = os.path.join(root, "lib")
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+            *[x for d in inc for x in ("-isystem", d)], "-o", out, TORCH_SOURCE, "-L", lib, f"-Wl,-rpath,{lib}",
+            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+
+
+def _stale(out: str, deps: list[str]) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(f) > os.path.getmtime(out) for f in deps)
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB_PATH):
-        return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(f) > t for f in DEPS)
+    return _stale(LIB_PATH, DEPS) or _stale(TORCH_LIB_PATH, TORCH_DEPS)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if force or needs_build():
-        os.makedirs(LIB_DIR, exist_ok=True)
-        tmp = LIB_PATH + f".tmp{os.getpid()}"
-        res = subprocess.run(command(tmp, verbose_ptxas), capture_output=True, text=True)
-        if res.returncode != 0:
-            raise RuntimeError(f"nvcc failed:\n{res.stdout}\n{res.stderr}")
+    """Compile what is out of date (both libraries at once); the path of libfa_gb300.so."""
+    jobs = []
+    for out, deps, make in ((LIB_PATH, DEPS, lambda o: command(o, verbose_ptxas)),
+                            (TORCH_LIB_PATH, TORCH_DEPS, torch_command)):
+        if force or _stale(out, deps):
+            os.makedirs(LIB_DIR, exist_ok=True)
+            tmp = out + f".tmp{os.getpid()}"
+            cmd = make(tmp)
+            jobs.append((out, tmp, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
+                                                         text=True)))
+    failed = []
+    for out, tmp, cmd, job in jobs:
+        stdout, stderr = job.communicate()
+        if job.returncode != 0:
+            failed.append(f"{cmd[0]} failed:\n{stdout}\n{stderr}")
+            continue
         if verbose_ptxas:
-            sys.stderr.write(res.stderr)
-        os.replace(tmp, LIB_PATH)
+            sys.stderr.write(stderr)
+        os.replace(tmp, out)
+    if failed:
+        raise RuntimeError("\n".join(failed))
     return LIB_PATH
 
 

@@ -3,13 +3,19 @@
 the package).
 
 Argument checks and marshalling only; the kernels do the work.  A decoding step
-makes these calls for a few microseconds of GPU work each, so the checks are
-written to cost little: plain attribute tests, no copies, no device queries.
+makes these calls for a few microseconds of GPU work each, so the usual case
+(everything in order, the current stream) goes through ``fa_torch`` (C++, the same
+checks); what that does not take comes to the code here, which also raises the
+errors.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
+import importlib.machinery
+import importlib.util
 import math
+import os
 import struct
 
 import torch
@@ -20,6 +26,24 @@ _BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.in
 _Tensor = torch.Tensor
 _pack6, _pack12, _pack18 = (struct.Struct(f"{n}q").pack for n in (6, 12, 18))
 _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _load_native():
+    """The fa_torch module, bound to the loaded library's functions."""
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "fa_torch.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+    loader = importlib.machinery.ExtensionFileLoader("fa_torch", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("fa_torch", path, loader=loader))
+    loader.exec_module(module)
+    lib = load()
+    module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
+                  for f in ("fa_rope", "fa_kv_append", "fa_fwd_paged", "fa_fwd_prefix", "fa_paged_workspace_bytes")))
+    return module
+
+
+_native = _load_native()
+_native_rope, _native_append, _native_paged = _native.rope, _native.kv_append, _native.paged
 
 
 def rope_freqs(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -106,6 +130,10 @@ def _rot(inv_freq):
 
 
 def _rope(backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream):
+    if stream is None:
+        done = _native_rope(backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out)
+        if done is not None:
+            return done
     _need("q", q, _BF16, 4)
     q_shape = q.shape
     B, H, N, d = q_shape
@@ -141,7 +169,7 @@ def _rope(backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, 
         ks = ko = none
     strides = _pack12(*_strides3("q", q, q_shape), *ks, *_strides3("q_out", q_out, q_shape), *ko)
     st = load().fa_rope(q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, inv_freq.data_ptr(), p_ptr, p_stride, offset,
-                        strides, B, H, Hk, N, d, rot, mag, interleaved, backward, _handle(stream, q))
+                        strides, B, H, Hk, N, d, rot, mag, bool(interleaved), backward, _handle(stream, q))
     if st != 0:
         raise FaError(st, "fa_rope")
     return q_out, k_out
@@ -158,14 +186,14 @@ def rope(q, k, inv_freq, positions=None, offset: int = 0, interleaved: bool = Fa
     ``offset`` is added.  ``interleaved``: pairs (2i, 2i + 1) instead of (i, i + rot / 2).  ``mag`` multiplies
     the turned part.  Runs on ``stream`` (default: the current torch stream), asynchronously.
     """
-    return _rope(0, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream)
+    return _rope(False, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream)
 
 
 def rope_bwd(dq, dk, inv_freq, positions=None, offset: int = 0, interleaved: bool = False, mag: float = 1.0,
              q_out=None, k_out=None, stream=None):
     """Gradients of ``rope``'s inputs from those of its outputs (from ``bwd``): the transposed rotation, same
     arguments; ``q_out`` and ``k_out`` may be views of a packed gradient."""
-    return _rope(1, dq, dk, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream)
+    return _rope(True, dq, dk, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -206,6 +234,11 @@ def kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq=None, n
     (``inv_freq`` None: no rotation).  Padding rows are not written (q_out included).  Two tokens must not share
     a slot.  Asynchronous; a page index outside the cache is skipped and reported by ``fa_fwd_status``.
     """
+    if stream is None:
+        done = _native_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq, new_lens, offset,
+                              interleaved, mag, q_out)
+        if done is not None:
+            return done
     _need("k", k, _BF16, 4)
     _need("v", v, _BF16, 4)
     k_shape = k.shape
@@ -235,7 +268,7 @@ def kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq=None, n
     strides = _pack18(*qs, *_strides3("k", k, k_shape), *_strides3("v", v, k_shape), *qo, *caches)
     st = load().fa_kv_append(q_ptr, k.data_ptr(), v.data_ptr(), qo_ptr, k_cache.data_ptr(), v_cache.data_ptr(), w_ptr,
                              block_table.data_ptr(), seq_lens.data_ptr(), new, strides, B, H, Hk, T, d, rot, shape[0],
-                             shape[2], max_pages, offset, mag, interleaved, _handle(stream, k))
+                             shape[2], max_pages, offset, mag, bool(interleaved), _handle(stream, k))
     if st != 0:
         raise FaError(st, "fa_kv_append")
     return q_out
@@ -290,6 +323,11 @@ def fwd_paged(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = 
     right as they grow.  ``workspace`` (``fa_paged_workspace_bytes(B, H, Hk, T, d, 0)`` bytes) may be given; calls
     that may overlap need one each.  Runs on ``stream`` (default: the current torch stream), asynchronously.
     """
+    if stream is None:
+        done = _native_paged(q, k_cache, v_cache, None, 0, block_table, seq_lens, scale, new_lens, window[0], window[1],
+                             out, lse, workspace)
+        if done is not None:
+            return done
     out, lse, workspace, ws_bytes, new, rest = _paged_args(
         q, k_cache, v_cache, block_table, seq_lens, new_lens, scale, out, lse, workspace, stream, 0)
     st = load().fa_fwd_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
@@ -309,6 +347,11 @@ def fwd_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_table, 
     ``offset=prefix_len`` puts them there).  An entry with seq_lens <= 0 is empty: O = 0, LSE = -inf.
     ``workspace``: ``fa_paged_workspace_bytes(B, H, Hk, T, d, prefix_len)`` bytes.
     """
+    if stream is None and prefix_pages is not None:
+        done = _native_paged(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens, scale, new_lens, -1,
+                             0, out, lse, workspace)
+        if done is not None:
+            return done
     _need("prefix_pages", prefix_pages, _I32, 1)
     if prefix_len <= 0:
         raise ValueError("prefix_len must be > 0 (without a prefix: fwd_paged)")
