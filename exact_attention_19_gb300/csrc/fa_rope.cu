@@ -22,17 +22,21 @@ fa::RopeView contiguous(int heads, int n, int d) {
   return {static_cast<long long>(heads) * n * d, static_cast<long long>(n) * d, d};
 }
 
-// Heads per CTA: every head of a token in one CTA once the tiles of tokens
-// alone give each multiprocessor kTilesPerSm CTAs (the angles are then computed
-// once per token); below that the heads are cut into groups to fill the GPU.
-constexpr long long kTilesPerSm = 4;
+// Heads per CTA: the angles are computed once per token and CTA, so a CTA takes
+// several heads; but enough CTAs are wanted that the last wave of them is short.
+constexpr long long kCtasPerSm = 24;
+constexpr long long kLeastHeads = 4;
+constexpr long long kLeastCtasPerSm = 4;
 
 template <int D, bool PAGED>
 int launch(fa::RopeParams& p, int interleaved, int sms, cudaStream_t stream) {
   constexpr int kTokens = fa::kRopeThreads / (D / 16);
   const long long tiles = (p.tokens + kTokens - 1) / kTokens;
   const long long heads = static_cast<long long>(p.heads[0]) + p.heads[1] + (PAGED ? p.heads[2] : 0);
-  long long groups = (kTilesPerSm * sms + tiles - 1) / tiles;
+  long long groups = (kCtasPerSm * sms + tiles - 1) / tiles;
+  if (groups > heads / kLeastHeads) groups = heads / kLeastHeads;
+  const long long least = (kLeastCtasPerSm * sms + tiles - 1) / tiles;
+  if (groups < least) groups = least;
   if (groups > heads) groups = heads;
   if (groups > 65535) groups = 65535;  // grid y
   p.heads_per_cta = static_cast<int>((heads + groups - 1) / groups);

@@ -74,11 +74,6 @@ __device__ __forceinline__ unsigned long long turns_per_position(double w) {
   return (bits >> 63) ? 0ull - f : f;
 }
 
-// 16-byte load, streamed: every element is read once
-__device__ __forceinline__ uint4 ld_stream16(const uint16_t* p) {
-  return __ldcs(reinterpret_cast<const uint4*>(p));
-}
-
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 // round to nearest even; `lo` in bits 0-15
@@ -107,7 +102,7 @@ __device__ __forceinline__ void rotate16(uint4& a, uint4& b, const float (&c)[8]
   }
 }
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 // grid: x = tiles of kRopeThreads / (D / 16) tokens, y = groups of heads.
 // PAGED: k and v go to the cache slots of their sequence's pages, q to dst[0];
@@ -157,10 +152,10 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
     for (int i = 0; i < 8; ++i) {
       const unsigned long long phase =
           static_cast<unsigned long long>(pos) * turns_per_position(__ldg(p.inv_freq + 8 * u + i));
-      // the upper 32 bits as a signed fraction of a turn, in [-1/2, 1/2); angle / pi = 2 turns
-      const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 0x1p-31f;
-      float sn, cs;
-      sincospif(half_turns, &sn, &cs);
+      // the upper 32 bits as a signed fraction of a turn: an angle in [-pi, pi), where the special-function
+      // unit's sine and cosine are off by at most 2^-21.2, an eighth of a thousandth of a bf16 step
+      const float angle = static_cast<float>(static_cast<int>(phase >> 32)) * 1.46291807926715968e-9f;  // pi 2^-31
+      const float sn = __sinf(angle), cs = __cosf(angle);
       c[i] = cs * p.mag;
       s[i] = sn * (p.mag * p.sin_sign);
     }
@@ -186,8 +181,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
 #pragma unroll
       for (int i = 0; i < kU; ++i)
         if (h + i < hi) {
-          a[i] = ld_stream16(src + (h + i) * p.src_s[t].h + c0);
-          e[i] = ld_stream16(src + (h + i) * p.src_s[t].h + c1);
+          a[i] = *reinterpret_cast<const uint4*>(src + (h + i) * p.src_s[t].h + c0);
+          e[i] = *reinterpret_cast<const uint4*>(src + (h + i) * p.src_s[t].h + c1);
         }
 #pragma unroll
       for (int i = 0; i < kU; ++i)
