@@ -97,7 +97,7 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
     if (i == 1) {
       l.prefix_blocks = fa::row_blocks(rows * B, l.rb[1]);
       l.prefix_tiles = (prefix_len + kTileKeys - 1) / kTileKeys;
-      l.prefix_units = 1ll * Hk * l.prefix_blocks * l.prefix_tiles;
+      l.prefix_units = 1ll * Hk * l.prefix_blocks * (l.prefix_tiles + fa::extra_units(l.rb[1]));
       l.prefix_ctas = fa::paged_ctas(l.grid[1], l.prefix_units, l.rb[1]);
       l.grid[1] = static_cast<int>(l.prefix_ctas);
     }

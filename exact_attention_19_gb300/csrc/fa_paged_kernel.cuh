@@ -127,6 +127,11 @@ __device__ __forceinline__ void paged_end(const PagedParams& p) {
   if (!PREFIX && p.prefix_len > 0) grid_wait();
 }
 
+// What a row block costs beside its tiles (its rows, its first wait, its
+// output), in tiles: the line of units holds so many empty ones behind each row
+// block's, so that shares of many short row blocks are not the last to finish.
+__host__ __device__ constexpr int extra_units(int rb) { return rb == 16 ? 1 : 4; }
+
 // A row block against the tiles of its keys that this CTA holds.
 struct PagedWalk {
   long long g, gend;  // first unit of the current segment part, end of the CTA's units
@@ -138,6 +143,9 @@ struct PagedWalk {
 
 template <int RB, int TILE, bool PREFIX>
 struct PagedSchedule {
+  static constexpr int kExtra = extra_units(RB);
+  // units of a row block of n tiles
+  static __device__ __forceinline__ int units(int n) { return n > 0 ? n + kExtra : 0; }
   static __device__ __forceinline__ int blocks(const PagedParams& p) {
     return PREFIX ? p.prefix_blocks : row_blocks(p.rows, RB);
   }
@@ -154,10 +162,21 @@ struct PagedSchedule {
   static __device__ __forceinline__ void part(PagedWalk& w) {
     w.jend = static_cast<int>(min(static_cast<long long>(w.n), w.j + (w.gend - w.g)));
   }
+  static __device__ __forceinline__ void next_block(const PagedParams& p, PagedWalk& w) {
+    w.j = 0;
+    if (++w.rb == blocks(p)) {
+      w.rb = 0;
+      if (++w.hk == p.Hk) {
+        w.hk = 0;
+        ++w.b;
+        if (!PREFIX) enter_seq(p, w);
+      }
+    }
+  }
   // first segment of the units [g, gend), g < gend; b, b_unit: the sequence that holds g and its first
-  // unit (own keys)
-  static __device__ __forceinline__ void begin(const PagedParams& p, PagedWalk& w, long long g, long long gend, int b,
-                                               long long b_unit) {
+  // unit (own keys).  starts: it holds unit g.  False: the units are empty ones.
+  static __device__ __forceinline__ bool begin(const PagedParams& p, PagedWalk& w, long long g, long long gend, int b,
+                                               long long b_unit, bool& starts) {
     w.g = g;
     w.gend = gend;
     w.b = b;
@@ -169,25 +188,25 @@ struct PagedSchedule {
     } else {
       enter_seq(p, w);
     }
-    const long long i = quotient(g - b_unit, w.n);
-    w.j = static_cast<int>((g - b_unit) - i * w.n);
+    const int each = units(w.n);
+    const long long i = quotient(g - b_unit, each);
+    w.j = static_cast<int>((g - b_unit) - i * each);
     w.hk = static_cast<int>(quotient(i, blocks(p)));
     w.rb = static_cast<int>(i - static_cast<long long>(w.hk) * blocks(p));
+    starts = w.j < w.n;
+    if (!starts) {
+      w.g += each - w.j;
+      if (w.g >= w.gend) return false;
+      next_block(p, w);
+    }
     part(w);
+    return true;
   }
   // the segment after the current one, w.j still its first tile; false: none left
   static __device__ __forceinline__ bool next(const PagedParams& p, PagedWalk& w) {
-    w.g += w.jend - w.j;
+    w.g += w.jend - w.j + (w.jend == w.n ? kExtra : 0);
     if (w.g >= w.gend) return false;
-    w.j = 0;
-    if (++w.rb == blocks(p)) {
-      w.rb = 0;
-      if (++w.hk == p.Hk) {
-        w.hk = 0;
-        ++w.b;
-        if (!PREFIX) enter_seq(p, w);
-      }
-    }
+    next_block(p, w);
     part(w);
     return true;
   }
@@ -214,7 +233,7 @@ struct PagedSchedule {
     return (static_cast<long long>(b) * p.Hk + w.hk) * p.rows + rr;
   }
   // where a row block's result goes: 0 the output, 1 whole_*, 2 piece_* (row = of the piece); first: the
-  // segment is the CTA's first
+  // segment holds the CTA's first unit
   static __device__ __forceinline__ int target(const PagedParams& p, const PagedWalk& w, bool first, int r,
                                                long long& row) {
     if (w.jend - w.j == w.n) return p.prefix_len > 0 ? 1 : 0;
@@ -290,13 +309,12 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // lengths, and CTA 0 leaves the plan for the merge kernel.
 template <int RB, int TILE, bool PREFIX, int THREADS>
 __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scratch /* shared, THREADS / 32 + 2 */,
-                                            PagedWalk& w) {
+                                            PagedWalk& w, bool& starts) {
   using S = PagedSchedule<RB, TILE, PREFIX>;
   if constexpr (PREFIX) {
     if (static_cast<long long>(blockIdx.x) >= p.prefix_ctas) return false;
     const long long g = cta_start(p.prefix_units, p.prefix_ctas, blockIdx.x);
-    S::begin(p, w, g, cta_start(p.prefix_units, p.prefix_ctas, blockIdx.x + 1ll), 0, 0);
-    return true;
+    return S::begin(p, w, g, cta_start(p.prefix_units, p.prefix_ctas, blockIdx.x + 1ll), 0, 0, starts);
   } else {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kWarps = THREADS / 32;
@@ -320,7 +338,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
         mine = 0;
         if (b < p.B) {
           const SeqKeys s = seq_keys(p, b);
-          mine = per * tiles_of(s.lo, s.hi, TILE);
+          mine = per * S::units(tiles_of(s.lo, s.hi, TILE));
           if (pass == 0 && blockIdx.x == 0 && __ldg(p.lens + b) > p.capacity) atomicOr(p.status, kPagedPage);
         }
         long long incl = mine;
@@ -359,8 +377,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
         if (g >= gend) return false;
       }
     }
-    S::begin(p, w, g, gend, static_cast<int>(scratch[kWarps]), scratch[kWarps + 1]);
-    return true;
+    return S::begin(p, w, g, gend, static_cast<int>(scratch[kWarps]), scratch[kWarps + 1], starts);
   }
 }
 
@@ -393,11 +410,11 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
   }
   paged_begin<PREFIX>(p);
   PagedWalk w;
-  if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(p, scratch, w)) {
+  bool first;  // the segment holds the share's first unit
+  if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(p, scratch, w, first)) {
     paged_end<PREFIX>(p);
     return;
   }
-  const long long first_g = w.g;
   __syncthreads();
 
   // the tiles [j0, j1) of a segment part in which this warp has keys
@@ -517,11 +534,14 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     // ---- the segment's rows ------------------------------------------------
     int lo[2], hi[2];
     uint32_t qf[kKT][4];
-    long long out_row[2];  // row in [B * H * T], -1: none
+    long long out_row[2];  // row in [B * H * T], -1: no such row
+    bool none[2];          // the row sees no key
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       out_row[i] = S::row(p, w, g8 + 8 * i, lo[i], hi[i]);
       const bool there = out_row[i] >= 0;
+      none[i] = hi[i] <= lo[i];  // such a row is not masked either (its warp would mask every tile), but dropped
+      if (none[i]) lo[i] = 0, hi[i] = 0x7fffffff;
       const uint32_t* const src = reinterpret_cast<const uint32_t*>(p.q + (there ? out_row[i] : 0) * D);
 #pragma unroll
       for (int kk = 0; kk < kKT; ++kk) {
@@ -710,10 +730,15 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (out_row[i] < 0) continue;
-      const float inv = l[i] > 0.f ? 1.0f / l[i] : 0.f;
-      const float lb = l[i] > 0.f ? m[i] + __log2f(l[i]) : NEG_INF;
+      const bool some = !none[i] && l[i] > 0.f;
+      const float lb = some ? m[i] + __log2f(l[i]) : NEG_INF;
+      if (!some) {
+#pragma unroll
+        for (int n = 0; n < kNT / 4; ++n) fin[n][2 * i] = fin[n][2 * i + 1] = 0.f;
+      }
+      const float inv = some ? 1.0f / l[i] : 0.f;
       long long row = out_row[i];
-      const int to = S::target(p, w, w.g == first_g, g8 + 8 * i, row);
+      const int to = S::target(p, w, first, g8 + 8 * i, row);
       if (to == 0) {
         uint16_t* const dst = p.out + row * D + col;
 #pragma unroll
@@ -728,6 +753,7 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
         if (col == 0) (to == 1 ? p.whole_l[PREFIX] : p.piece_l[PREFIX])[row] = lb;
       }
     }
+    first = false;
   } while (S::next(p, w));
   if (!ok) {  // let every copy in flight land before the CTA's shared memory goes
     for (int i = consumed; i < issued; ++i)
@@ -753,8 +779,9 @@ struct RowParts {
     ctas = p.plan[1];
     const long long u0 = p.plan[2 + b], u1 = p.plan[3 + b];
     const int blocks = row_blocks(p.rows, p.rb[0]);
-    const long long n = quotient(u1 - u0, static_cast<long long>(p.Hk) * blocks);
-    x0 = u0 + (static_cast<long long>(hk) * blocks + rr / p.rb[0]) * n;
+    const long long each = quotient(u1 - u0, static_cast<long long>(p.Hk) * blocks);
+    const long long n = each - extra_units(p.rb[0]);  // tiles; none: each is 0
+    x0 = u0 + (static_cast<long long>(hk) * blocks + rr / p.rb[0]) * each;
     in_own = rr % p.rb[0];
     n_own = 0;
     c0 = 0;
@@ -769,7 +796,7 @@ struct RowParts {
       const long long pr = static_cast<long long>(b) * p.rows + rr;  // row among the K/V head's prefix rows
       const long long block = quotient(pr, p.rb[1]);
       in_prefix = static_cast<int>(pr - block * p.rb[1]);
-      y0 = (static_cast<long long>(hk) * p.prefix_blocks + block) * p.prefix_tiles;
+      y0 = (static_cast<long long>(hk) * p.prefix_blocks + block) * (p.prefix_tiles + extra_units(p.rb[1]));
       d0 = cta_of(p.prefix_units, p.prefix_ctas, y0);
       n_all += static_cast<int>(cta_of(p.prefix_units, p.prefix_ctas, y0 + p.prefix_tiles - 1) - d0) + 1;
     }
@@ -785,7 +812,7 @@ struct RowParts {
       return;
     }
     const long long c = (pre ? d0 : c0) + k;
-    // a CTA's first segment is its piece 0; the row block is that one unless it starts inside the CTA
+    // piece 0 of a CTA is the row block that holds its first unit, which starts there or before
     const long long first = pre ? cta_start(p.prefix_units, p.prefix_ctas, c) : cta_start(units, ctas, c);
     const long long slot = 2 * c + (first >= (pre ? y0 : x0) ? 0 : 1);
     const long long r = slot * p.rb[pre] + (pre ? in_prefix : in_own);

@@ -146,8 +146,9 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
     return;
   }
   PagedWalk w;
+  bool first;  // the segment holds the share's first unit
   if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(
-          p, reinterpret_cast<long long*>(tile_smem + C::kBarOff + kTileScratchOff), w)) {
+          p, reinterpret_cast<long long*>(tile_smem + C::kBarOff + kTileScratchOff), w, first)) {
     paged_end<PREFIX>(p);
     return;
   }
@@ -399,10 +400,11 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
     };
     put_walk(w);
     int used = 0, item = 0, seg = 0;  // uses of S_t, ring items, segments with tiles
-    bool ok = true, first = true, more = true;
+    bool ok = true, more = true;
     do {
       int n, lo, hi, k0;
-      bool busy, low_edge, high_edge;  // the first or last tile reaches past the segment's keys
+      bool busy, none;            // the warp has rows that see keys; this row sees none
+      bool low_edge, high_edge;  // the first or last tile reaches past the segment's keys
       {
         const PagedWalk v = *walk;
         int jlo, jhi;
@@ -411,7 +413,12 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
         k0 = (v.tile0 + jlo) * C::kTile;
         low_edge = k0 < v.lo;
         high_edge = (v.tile0 + jhi) * C::kTile > v.hi;
-        busy = __any_sync(0xffffffffu, S::row(p, v, PAIR ? t * 128 + r : r, lo, hi) >= 0);  // the warp has rows
+        const bool there = S::row(p, v, PAIR ? t * 128 + r : r, lo, hi) >= 0;
+        // A row that sees no key is not masked (its warp would mask every tile) but dropped at the end, and a warp
+        // of such rows has nothing to do.
+        none = hi <= lo;
+        if (none) lo = 0, hi = 0x7fffffff;
+        busy = __any_sync(0xffffffffu, there && !none);
       }
       float m_bar = NEG_INF, l = 0.f, r_max = NEG_INF;
       if (!PAIR && t) k0 += C::kTile;
@@ -540,6 +547,7 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
       }
       if (!ok) break;
       item += 2 * n;
+      if (none) l = 0.f;
       // O's normaliser counts the row's largest P as rounded for P V, as in fa_fwd_kernel
       float l_o = l;
       if (l > 0.f) {
@@ -571,7 +579,7 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
         ++seg;
       }
       PagedWalk v = *walk;
-      if (busy) {
+      {
         const long long out_row = S::row(p, v, PAIR ? t * 128 + r : r, lo, hi);
         long long row = out_row;
         const int to = S::target(p, v, first, PAIR ? t * 128 + r : r, row);
