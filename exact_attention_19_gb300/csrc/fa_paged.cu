@@ -68,7 +68,7 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 // Rows per row block, by the rows that share each K/V byte: the warp-level
 // kernel's 16, or the tcgen05 kernel's 128 or 256.
 int block_rows(long long rows) { return rows <= 16 ? 16 : (rows <= 128 ? 128 : 256); }
-constexpr int kTileKeys = 128;  // keys of a unit in either kernel
+constexpr int kTileKeys = fa::kPagedTile;
 int grid_of(int block_rows, int sms) { return block_rows == 16 ? 2 * sms : sms; }  // all CTAs resident
 
 constexpr long long kLongOwn = 16;
@@ -169,10 +169,9 @@ int launch_part(const Caches& c, const fa::PagedParams& p, int grid, cudaStream_
 }
 
 template <int D>
-int launch(const Caches& c, const fa::PagedParams& p, const Layout& l, long long rows, int own_grid,
-           cudaStream_t stream) {
+int launch(const Caches& c, const fa::PagedParams& p, const Layout& l, long long rows, cudaStream_t stream) {
   int st = p.prefix_len > 0 ? launch_part<D, true>(c, p, l.grid[1], stream) : FA_OK;
-  if (st == FA_OK) st = launch_part<D, false>(c, p, own_grid, stream);
+  if (st == FA_OK) st = launch_part<D, false>(c, p, p.own_grid, stream);
   return st == FA_OK ? launch_merge<D>(p, rows, stream) : st;
 }
 
@@ -257,14 +256,14 @@ int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
   // Beside a prefix kernel that leaves a quarter of the SMs or more free, the own keys are cut for the free ones
   // alone (64 sequences behind 8192 tokens: 43 us against 55 with shares that wait for the other SMs), unless
   // the table allows more work than kLongOwn units per CTA, for which every SM is wanted.
-  int own_grid = l.grid[0];
+  p.own_grid = l.grid[0];
   if (prefix_len > 0 && l.prefix_ctas * 4 <= 3ll * sms) {
     const long long tiles = (1ll * max_pages * page_size + kTileKeys - 1) / kTileKeys;
-    if (1ll * B * Hk * fa::row_blocks(p.rows, l.rb[0]) * tiles <= kLongOwn * own_grid)
-      own_grid = own_grid / sms * static_cast<int>(sms - l.prefix_ctas);
+    if (1ll * B * Hk * fa::row_blocks(p.rows, l.rb[0]) * tiles <= kLongOwn * p.own_grid)
+      p.own_grid = p.own_grid / sms * static_cast<int>(sms - l.prefix_ctas);
   }
   const Caches c = {k_cache, v_cache, strides, d, page_size, Hk, n_pages};
-  return d == 64 ? launch<64>(c, p, l, rows, own_grid, stream) : launch<128>(c, p, l, rows, own_grid, stream);
+  return d == 64 ? launch<64>(c, p, l, rows, stream) : launch<128>(c, p, l, rows, stream);
 }
 
 }  // namespace

@@ -47,7 +47,8 @@ struct PagedParams {
   int prefix_len;           // 0: no prefix
   int left, right;          // own window, -1 = open
   float scale_log2;         // scale * log2(e)
-  long long* plan;          // own units: [0] units, [1] CTAs with work, [2 + b] first unit of sequence b
+  long long* plan;          // own units, for the merge of a large batch: [0] units, [1 + b] first unit of sequence b
+  int own_grid;             // CTAs of the launch over own keys
   int rb[2];                // rows of a row block: own keys, prefix
   int prefix_blocks;        // row blocks of a K/V head, key tiles, units and CTAs of the prefix
   int prefix_tiles;
@@ -126,6 +127,8 @@ template <bool PREFIX>
 __device__ __forceinline__ void paged_end(const PagedParams& p) {
   if (!PREFIX && p.prefix_len > 0) grid_wait();
 }
+
+constexpr int kPagedTile = 128;  // keys of a unit
 
 // What a row block costs beside its tiles (its rows, its first wait, its
 // output), in tiles: the line of units holds so many empty ones behind each row
@@ -258,7 +261,8 @@ struct PagedSchedule {
 template <int D>
 struct PagedCfg {
   static constexpr int kWarps = 4, kThreads = 128;
-  static constexpr int kRows = 16, kKeys = 32, kTile = kWarps * kKeys;
+  static constexpr int kRows = 16, kKeys = 32, kTile = kPagedTile;
+  static_assert(kTile == kWarps * kKeys, "a warp takes its keys of every tile");
   static constexpr int kBoxes = D / 64;
   static constexpr uint32_t kBoxBytes = kKeys * 128u;
   static constexpr uint32_t kItemBytes = kBoxes * kBoxBytes;  // 32 keys of K or of V
@@ -356,7 +360,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
           all += scratch[i];
         }
         first = before + incl - mine;
-        if (pass == 0 && blockIdx.x == 0 && b < p.B) p.plan[2 + b] = first;
+        if (pass == 0 && blockIdx.x == 0 && b < p.B) p.plan[1 + b] = first;
         if (pass == 1 && mine > 0 && first <= g && g < first + mine) {
           scratch[kWarps] = b;
           scratch[kWarps + 1] = first;
@@ -368,8 +372,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
         const long long ctas = paged_ctas(gridDim.x, run, RB);
         if (blockIdx.x == 0 && threadIdx.x == 0) {
           p.plan[0] = run;
-          p.plan[1] = ctas;
-          p.plan[2 + p.B] = run;
+          p.plan[1 + p.B] = run;
         }
         if (static_cast<long long>(blockIdx.x) >= ctas) return false;
         g = cta_start(run, ctas, blockIdx.x);
@@ -766,18 +769,26 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
 // Joins the parts of every row that more than one CTA (or the prefix and the
 // own keys) contributed to, and writes the rows that saw no key.
 // ---------------------------------------------------------------------------
+// Up to so many sequences a warp of the merge sums their units itself, before it
+// waits for the parts; of larger batches it reads the plan after the wait.
+constexpr int kMergeScan = 256;
+
 // The parts of one row, in order: own keys of CTAs [c0, c1], prefix of [d0, d1].
 struct RowParts {
   long long row, c0, x0, d0, y0, units, ctas;
   int n_own, n_all, in_own, in_prefix;  // row inside its row block
-  __device__ __forceinline__ void find(const PagedParams& p, long long r) {
+  int b, hk, rr;
+  __device__ __forceinline__ void locate(const PagedParams& p, long long r) {
     row = r;
     const long long bh = quotient(row, p.rows);
-    const int rr = static_cast<int>(row - bh * p.rows);
-    const int b = static_cast<int>(quotient(bh, p.Hk)), hk = static_cast<int>(bh - static_cast<long long>(b) * p.Hk);
-    units = p.plan[0];
-    ctas = p.plan[1];
-    const long long u0 = p.plan[2 + b], u1 = p.plan[3 + b];
+    rr = static_cast<int>(row - bh * p.rows);
+    b = static_cast<int>(quotient(bh, p.Hk));
+    hk = static_cast<int>(bh - static_cast<long long>(b) * p.Hk);
+  }
+  // all: units of the launch, u0 and u1: of the sequences before this one, and with it
+  __device__ __forceinline__ void find(const PagedParams& p, long long all, long long u0, long long u1) {
+    units = all;
+    ctas = paged_ctas(p.own_grid, all, p.rb[0]);
     const int blocks = row_blocks(p.rows, p.rb[0]);
     const long long each = quotient(u1 - u0, static_cast<long long>(p.Hk) * blocks);
     const long long n = each - extra_units(p.rb[0]);  // tiles; none: each is 0
@@ -800,6 +811,44 @@ struct RowParts {
       d0 = cta_of(p.prefix_units, p.prefix_ctas, y0);
       n_all += static_cast<int>(cta_of(p.prefix_units, p.prefix_ctas, y0 + p.prefix_tiles - 1) - d0) + 1;
     }
+  }
+  // Whole warp: locate() done, the rest, and the wait for the parts.  In a small batch everything that does
+  // not need them comes before the wait and runs beside the kernel that writes them.
+  __device__ __forceinline__ void wait(const PagedParams& p) {
+    if (p.B <= kMergeScan) {
+      const long long per = static_cast<long long>(p.Hk) * row_blocks(p.rows, p.rb[0]);
+      const int lane = threadIdx.x & 31;
+      long long all = 0, before = 0;
+      int mine = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        unsigned u = 0;  // units of a row block of sequence b0 + lane
+        if (b0 + lane < p.B) {
+          const SeqKeys s = seq_keys(p, b0 + lane);
+          const int n = tiles_of(s.lo, s.hi, kPagedTile);
+          u = n > 0 ? n + extra_units(p.rb[0]) : 0;
+        }
+        unsigned incl = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += up;
+        }
+        // each lane for its own row's sequence
+        const int at = min(max(b - b0, 0), 31);
+        const unsigned upto = __shfl_sync(0xffffffffu, incl, at), of = __shfl_sync(0xffffffffu, u, at);
+        if (b >= b0 && b < b0 + 32) {
+          before = all + upto - of;
+          mine = static_cast<int>(of);
+        }
+        all += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      find(p, all * per, before * per, (before + mine) * per);
+      grid_wait();
+    } else {
+      grid_wait();
+      find(p, p.plan[0], p.plan[1 + b], p.plan[2 + b]);
+    }
+    grid_release();
   }
   // written by the one CTA that held it
   __device__ __forceinline__ bool done(const PagedParams& p) const { return p.prefix_len == 0 && n_own == 1; }
@@ -850,10 +899,9 @@ __global__ void __launch_bounds__(128) fa_paged_merge_row_kernel(const PagedPara
   constexpr int kPer = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float NEG_INF = -__int_as_float(0x7f800000);
-  grid_wait();
-  grid_release();
   RowParts parts;
-  parts.find(p, blockIdx.x);
+  parts.locate(p, blockIdx.x);
+  parts.wait(p);
   if (parts.done(p)) return;
   float mx = NEG_INF, sum = 0.f, acc[kPer];
 #pragma unroll
@@ -934,12 +982,11 @@ __global__ void __launch_bounds__(128) fa_paged_merge_rows_kernel(const PagedPar
   const float NEG_INF = -__int_as_float(0x7f800000);
   const long long all = static_cast<long long>(p.B) * p.Hk * p.rows;
   const long long row0 = (static_cast<long long>(blockIdx.x) * 4 + warp) * kRows;
-  grid_wait();
-  grid_release();
-  if (row0 >= all) return;
   const int group = lane >> 3;
   RowParts parts;
-  parts.find(p, min(row0 + group, all - 1));
+  parts.locate(p, min(row0 + group, all - 1));
+  parts.wait(p);
+  if (row0 >= all) return;
   const int n_mine = (row0 + group < all && !parts.done(p)) ? parts.n_all : 0;
   const bool write = row0 + group < all && !parts.done(p);
   const int most = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(n_mine));

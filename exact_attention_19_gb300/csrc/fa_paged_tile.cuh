@@ -32,7 +32,7 @@ namespace fa {
 
 template <int D, bool PAIR>
 struct TileCfg {
-  static constexpr int kRows = PAIR ? 256 : 128, kTile = 128;
+  static constexpr int kRows = PAIR ? 256 : 128, kTile = kPagedTile;
   static constexpr int kThreads = 384, kWarpProd = 8, kWarpMma = 9;
   static constexpr int kBoxes = D / 64;
   static constexpr uint32_t kBox = 128u * 128u;
