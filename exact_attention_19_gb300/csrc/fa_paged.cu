@@ -110,8 +110,9 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
   return l;
 }
 
-// Rows from which one warp of the merge joins four rows; below, four warps join one.
-constexpr long long kMergeRows = 8192;
+// The merge: from kMergeRows rows, or kMergeFewRows with at most kMergeParts parts to a row, one warp joins
+// four rows; else two warps join one (from kMergeFewRows rows, so that one wave of CTAs holds them) or four.
+constexpr long long kMergeRows = 8192, kMergeFewRows = 1536, kMergeParts = 4;
 
 // Programmatic dependent launch: the kernel may be scheduled while the one ahead
 // of it on the stream still runs, and waits on the device (paged_begin) for what
@@ -134,8 +135,14 @@ int launch_kernel(K kernel, long long grid, int threads, size_t smem, cudaStream
 
 template <int D>
 int launch_merge(const fa::PagedParams& p, long long rows, cudaStream_t stream) {
-  if (rows >= kMergeRows) return launch_kernel(fa::fa_paged_merge_rows_kernel<D>, (rows + 15) / 16, 128, 0, stream, p);
-  return launch_kernel(fa::fa_paged_merge_row_kernel<D>, rows, 128, 0, stream, p);
+  // parts of a row where the shares cut every row block alike
+  long long parts = p.own_grid / (1ll * p.B * p.Hk * fa::row_blocks(p.rows, p.rb[0])) + 1;
+  if (p.prefix_len > 0) parts += p.prefix_ctas / (1ll * p.Hk * p.prefix_blocks) + 1;
+  if (rows >= kMergeRows || (rows >= kMergeFewRows && parts <= kMergeParts))
+    return launch_kernel(fa::fa_paged_merge_rows_kernel<D>, (rows + 15) / 16, 128, 0, stream, p);
+  if (rows >= kMergeFewRows)
+    return launch_kernel(fa::fa_paged_merge_row_kernel<D, 2>, (rows + 1) / 2, 128, 0, stream, p);
+  return launch_kernel(fa::fa_paged_merge_row_kernel<D, 4>, rows, 128, 0, stream, p);
 }
 
 struct Caches {

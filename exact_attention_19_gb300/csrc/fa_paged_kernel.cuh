@@ -892,30 +892,35 @@ __device__ __forceinline__ void merge_store(const PagedParams& p, long long row,
   if (lane == 0) p.lse[row] = sum > 0.f ? (top + __log2f(sum)) * 0.69314718055994530942f : -__int_as_float(0x7f800000);
 }
 
-// Few rows: four warps per row take its parts in turn, each lane finds one part
-// and its L, and the warps meet in shared memory.
-template <int D>
+// Few rows, or many parts to a row: WARPS (4 or 2) warps per row take its parts
+// in turn, each lane finds one part and its L, and the warps meet in shared
+// memory.
+template <int D, int WARPS>
 __global__ void __launch_bounds__(128) fa_paged_merge_row_kernel(const PagedParams p) {
   constexpr int kPer = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) % WARPS, lane = threadIdx.x & 31;  // warp of the row
   const float NEG_INF = -__int_as_float(0x7f800000);
+  const long long all = static_cast<long long>(p.B) * p.Hk * p.rows;
+  const long long row = static_cast<long long>(blockIdx.x) * (4 / WARPS) + (threadIdx.x >> 5) / WARPS;
   RowParts parts;
-  parts.locate(p, blockIdx.x);
+  parts.locate(p, min(row, all - 1));
   parts.wait(p);
-  if (parts.done(p)) return;
+  const bool idle = row >= all || parts.done(p);
+  if (WARPS == 4 && idle) return;
+  const int n_all = idle ? 0 : parts.n_all;
   float mx = NEG_INF, sum = 0.f, acc[kPer];
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  for (int base = warp; base < parts.n_all; base += 128) {
-    const int i = base + lane * 4;
+  for (int base = warp; base < n_all; base += 32 * WARPS) {
+    const int i = base + lane * WARPS;
     const float* po = nullptr;
     float L = NEG_INF;
-    if (i < parts.n_all) {
+    if (i < n_all) {
       const float* pl;
       parts.at(p, D, i, po, pl);
       L = *pl;
     }
-    const int count = min(32, (parts.n_all - base + 3) / 4);
+    const int count = min(32, (n_all - base + WARPS - 1) / WARPS);
     auto src = [&](int k) -> const float* {
       return reinterpret_cast<const float*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), k));
     };
@@ -945,7 +950,8 @@ __global__ void __launch_bounds__(128) fa_paged_merge_row_kernel(const PagedPara
       for (int e = 0; e < kPer; ++e) acc[e] = fmaf(c, v[e], acc[e]);
     }
   }
-  __shared__ float sh[4][D + 2];
+  __shared__ float shared[4][D + 2];
+  float (*const sh)[D + 2] = shared + (threadIdx.x >> 5) / WARPS * WARPS;  // the row's warps
 #pragma unroll
   for (int e = 0; e < kPer; ++e) sh[warp][lane * kPer + e] = acc[e];
   if (lane == 0) {
@@ -953,16 +959,16 @@ __global__ void __launch_bounds__(128) fa_paged_merge_row_kernel(const PagedPara
     sh[warp][D + 1] = sum;
   }
   __syncthreads();
-  if (warp != 0) return;
+  if (warp != 0 || idle) return;
   float top = NEG_INF;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = fmaxf(top, sh[i][D]);
+  for (int i = 0; i < WARPS; ++i) top = fmaxf(top, sh[i][D]);
   sum = 0.f;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
   if (top != NEG_INF) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < WARPS; ++i) {
       const float c = sh[i][D] == NEG_INF ? 0.f : ex2(sh[i][D] - top);
       sum += c * sh[i][D + 1];
 #pragma unroll
