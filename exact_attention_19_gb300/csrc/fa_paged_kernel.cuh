@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (out_row[i] < 0) continue;
-      const bool some = !none[i] && l[i] > 0.f;
+      const bool some = !none[i] && l[i] != 0.f;  // NaN (from NaN or infinite scores) goes through
       const float lb = some ? m[i] + __log2f(l[i]) : NEG_INF;
       if (!some) {
 #pragma unroll
@@ -883,13 +883,13 @@ __device__ __forceinline__ void merge_load(const float* src, int lane, float (&v
 template <int D>
 __device__ __forceinline__ void merge_store(const PagedParams& p, long long row, int lane, const float (&acc)[D / 32],
                                             float top, float sum) {
-  const float inv = sum > 0.f ? 1.0f / sum : 0.f;
+  const float inv = sum != 0.f ? 1.0f / sum : 0.f;  // a NaN among the parts stays one
   uint16_t* const dst = p.out + row * D + lane * (D / 32);
   if constexpr (D == 128)
     *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
   else
     *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-  if (lane == 0) p.lse[row] = sum > 0.f ? (top + __log2f(sum)) * 0.69314718055994530942f : -__int_as_float(0x7f800000);
+  if (lane == 0) p.lse[row] = sum != 0.f ? (top + __log2f(sum)) * 0.69314718055994530942f : -__int_as_float(0x7f800000);
 }
 
 // Few rows, or many parts to a row: WARPS (4 or 2) warps per row take its parts
@@ -930,8 +930,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_row_kernel(const PagedPara
     float top = fmaxf(mx, L);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (top == NEG_INF) continue;
-    const float a = mx == NEG_INF ? 0.f : ex2(mx - top);
+    const float a = mx == NEG_INF ? 0.f : ex2(mx - top);  // no key in any part: every weight is 0
     const float wt = L == NEG_INF ? 0.f : ex2(L - top);
     float ws = wt;
 #pragma unroll
@@ -966,14 +965,13 @@ __global__ void __launch_bounds__(128) fa_paged_merge_row_kernel(const PagedPara
   sum = 0.f;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-  if (top != NEG_INF) {
 #pragma unroll
-    for (int i = 0; i < WARPS; ++i) {
-      const float c = sh[i][D] == NEG_INF ? 0.f : ex2(sh[i][D] - top);
-      sum += c * sh[i][D + 1];
+  for (int i = 0; i < WARPS; ++i) {
+    // a warp whose parts hold no key, or nothing but NaN, has top -inf: its sum counts as it is
+    const float c = sh[i][D] == NEG_INF ? 1.f : ex2(sh[i][D] - top);
+    sum += c * sh[i][D + 1];
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) acc[e] += c * sh[i][lane * kPer + e];
-    }
+    for (int e = 0; e < kPer; ++e) acc[e] += c * sh[i][lane * kPer + e];
   }
   merge_store<D>(p, parts.row, lane, acc, top, sum);
 }

@@ -550,12 +550,12 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
       if (none) l = 0.f;
       // O's normaliser counts the row's largest P as rounded for P V, as in fa_fwd_kernel
       float l_o = l;
-      if (l > 0.f) {
+      if (l != 0.f) {  // NaN (from NaN or infinite scores) goes through, here and below
         const float e_max = ex2(fmaf(r_max, c, -m_bar));
         l_o += __uint_as_float(pack_bf16(e_max, 0.f) << 16) - e_max;
       }
-      float inv = l > 0.f ? 1.0f / l_o : 0.f;
-      float lb = l > 0.f ? m_bar + __log2f(l) : NEG_INF;
+      float inv = l != 0.f ? 1.0f / l_o : 0.f;
+      float lb = l != 0.f ? m_bar + __log2f(l) : NEG_INF;
       float inv_other = 0.f;  // factor of the other warpgroup's O
       if (n > 0) {
         ok = uniform(mbar_wait(bar(kTBarFinal + (PAIR ? t : 0)), seg & 1, abort_flag));
@@ -572,9 +572,9 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
           const float top = fmaxf(lb, st.x);
           const float wm = lb == NEG_INF ? 0.f : ex2(lb - top), wo = st.x == NEG_INF ? 0.f : ex2(st.x - top);
           const float sum = wm + wo;
-          inv = sum > 0.f ? wm * inv / sum : 0.f;
-          inv_other = sum > 0.f ? wo * st.y / sum : 0.f;
-          lb = sum > 0.f ? top + __log2f(sum) : NEG_INF;
+          inv = wm != 0.f ? wm * inv / sum : 0.f;
+          inv_other = wo != 0.f ? wo * st.y / sum : 0.f;
+          lb = sum != 0.f ? top + __log2f(sum) : NEG_INF;
         }
         ++seg;
       }
@@ -597,12 +597,12 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
             tmem_ld_wait(o);
             // a factor of zero drops what may be nothing but stale bits
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = inv > 0.f ? __uint_as_float(o[e]) * inv : 0.f;
+            for (int e = 0; e < 32; ++e) f[e] = inv != 0.f ? __uint_as_float(o[e]) * inv : 0.f;
             if constexpr (!PAIR) {
               tmem_ld32(lane_base + C::kTmO + (t ^ 1) * D + col0 + cc * 32, o);
               tmem_ld_wait(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) f[e] += inv_other > 0.f ? __uint_as_float(o[e]) * inv_other : 0.f;
+              for (int e = 0; e < 32; ++e) f[e] += inv_other != 0.f ? __uint_as_float(o[e]) * inv_other : 0.f;
             }
           } else {
 #pragma unroll

@@ -288,6 +288,10 @@ def paged_case(fa, seed, B, H, Hk, T, d, page, lens, new=None, window=(-1, 0), t
     (250, 20, 1, 1, 16, [i * 7 % 90 for i in range(250)], None),  # several sequences to a CTA
     (3, 4, 1, 300, 64, [300, 640, 1000], [300, 7, 299]),          # blocks of rows that see part of the keys
     (1, 1, 1, 600, 256, [600], None),
+    (300, 2, 1, 1, 16, [i * 11 % 61 for i in range(300)], None),  # more sequences than the merge sums itself
+    (1, 2, 1, 1, 256, [20000], None),                             # one row block in the shares of every CTA
+    (1, 40, 1, 1, 128, [9000], None),
+    (400, 4, 4, 6, 16, [6 + i % 30 for i in range(400)], None),   # 9600 rows to merge
 ])
 def test_paged(fa, B, H, Hk, T, d, page, lens, new):
     paged_case(fa, 1 + B, B, H, Hk, T, d, page, lens, new)
@@ -391,6 +395,110 @@ def test_bad_pages_and_lengths_are_reported(fa):
     assert fa.fa_fwd_status(None, clear=True)[0] == 12
 
 
+def test_nan_reaches_the_rows_that_see_it_and_no_others(fa):
+    """A NaN in a visible key or value makes its sequence's rows NaN, not zero, in every kernel; others stay."""
+    for H, T, lens in ((2, 1, [70, 90]), (2, 1, [3000, 2500]), (2, 20, [200, 333]), (4, 70, [500, 450])):
+        for what in ("k", "v"):
+            c = Cache(57, 2, 1, 64, 16, max(lens))
+            for b in range(2):
+                c.fill(c.table[b], lens[b], b)
+            q = rand(58, 2, H, T, 64)
+            good, good_l = run_paged(fa, c, q, lens, None)
+            getattr(c, what)[int(c.table[0, 0]), 0, 3, 5] = math.nan  # the first tokens: every row sees them
+            o, lse = run_paged(fa, c, q, lens, None)
+            hit = torch.isnan(o[0])
+            assert bool(hit.all() if what == "k" else hit[..., 5].all())
+            if what == "k":
+                assert bool(torch.isnan(lse[0]).all())
+            else:
+                assert torch.equal(lse[0], good_l[0])
+            assert torch.equal(o[1], good[1]) and torch.equal(lse[1], good_l[1])
+
+
+def test_pages_shared_between_sequences(fa):
+    """Tables that name the same pages (a forked sequence) read them alike."""
+    c = Cache(59, 3, 2, 128, 16, 300)
+    c.fill(c.table[0], 300, 1)
+    c.table[1] = c.table[0]
+    c.table[2, :10] = c.table[0, :10]
+    c.fill(c.table[2, 10:], 60, 2)
+    q = rand(60, 1, 8, 1, 128).expand(3, -1, -1, -1).contiguous()
+    lens = [300, 300, 220]
+    o, lse = run_paged(fa, c, q, lens, None)
+    want = ref.paged(f64(q), f64(c.k), f64(c.v), c.table, lens, [1] * 3, -1, 0, 1 / math.sqrt(128))
+    ref.check_attention(f64(o), f64(lse), want)
+    # the parts of a row depend on where its sequence lies in the call, so equal sequences agree to rounding
+    assert float((o[0].float() - o[1].float()).abs().max()) <= 4 * ref.U * float(o.float().abs().max())
+
+
+def test_caches_and_strides_past_32_bits(fa):
+    """A cache of more than 2^31 elements whose last pages are used, and a view with row strides as large."""
+    n_pages, page, d = 140000, 256, 64
+    need = 2 * 2 * n_pages * page * d + (4 << 30)
+    if torch.cuda.mem_get_info()[0] < need:
+        pytest.skip(f"needs {need >> 30} GB")
+    k, v = (torch.empty(n_pages, 1, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert k.numel() > 2 ** 31
+    c = Cache(63, 2, 1, d, page, 600)
+    c.k, c.v = k, v
+    c.table = np.array([[n_pages - 1, 139000, n_pages - 7], [0, n_pages - 3, 138001]], dtype=np.int32)
+    x = [rand(64 + i, 2, 1, 600, d) for i in range(3)]
+    lens = i32([600, 600])
+    tq = fa.kv_append(*x, k, v, c.device_table(), lens)
+    o, lse = fa.fwd_paged(tq, k, v, c.device_table(), lens)
+    want, want_l = fa.fwd(*x, causal=True, n_splits=1)
+    err = (o.float() - want.float()).abs()
+    assert bool((err <= 4 * ref.U * (want.float().abs() + x[2].float().abs().max())).all())
+    assert bool(((lse - want_l).abs() <= 2.0 ** -11 * want_l.abs().clamp(min=1)).all())
+    del c, tq, o, lse
+    flat = k.view(-1)
+    far = torch.as_strided(flat, (2, 3, 2, d), (1024, 64, 2 ** 31 + 64, 1))
+    far.copy_(rand(70, 2, 3, 2, d))
+    w, _ = fa.rope_freqs(d)
+    y, _ = fa.rope(far, None, w, offset=9)
+    check_rope(y, far, np.arange(2) + 9, w, 1.0, False)
+    out = torch.as_strided(v.view(-1), (2, 3, 2, d), (2 ** 31 + 64, 64, 1024, 1))
+    fa.rope(far, None, w, offset=9, q_out=out)
+    assert torch.equal(out, y)
+
+
+def test_many_repeats_agree(fa):
+    """Calls with many row blocks per CTA, again and again: the same bits, and no wait that gives up."""
+    for B, H, Hk, T, d, n in ((6, 32, 2, 8, 128, 2500), (40, 16, 2, 20, 64, 400), (30, 16, 4, 1, 128, 3000)):
+        c = Cache(66, B, Hk, d, 32, n)
+        lens = [n - 61 * i % (n - T) for i in range(B)]
+        for b in range(B):
+            c.fill(c.table[b], lens[b], b)
+        q = rand(67, B, H, T, d)
+        o, lse = run_paged(fa, c, q, lens, None)
+        for _ in range(40):
+            a, b = run_paged(fa, c, q, lens, None)
+            assert torch.equal(a, o) and torch.equal(b, lse)
+
+
+def test_another_stream_takes_the_same_path(fa):
+    """The calls with an explicit stream (checked in Python) against the usual ones (checked in C++)."""
+    B, H, Hk, T, d, page = 2, 4, 2, 3, 64, 16
+    w, mag = fa.rope_freqs(d, scaling="by_parts", factor=2.0)
+    _, (q, k, v) = packed(68, B, T, H, Hk, d)
+    side = torch.cuda.Stream()
+    got = []
+    for stream in (None, side):
+        c = Cache(69, B, Hk, d, page, 40, prefix_len=20)
+        c.fill(c.prefix_pages, 20, 5)
+        lens = i32([3, 3])
+        torch.cuda.synchronize()
+        tq = fa.kv_append(q, k, v, c.k, c.v, c.device_table(), lens, w, offset=20, mag=mag, stream=stream)
+        torch.cuda.synchronize()
+        r = [tq, *fa.rope(q, k, w, mag=mag, stream=stream), *fa.rope_bwd(q, None, w, stream=stream)[:1]]
+        torch.cuda.synchronize()
+        r += [*run_paged(fa, c, tq, [3, 3], None, stream=stream), *run_paged(fa, c, tq, [3, 3], None, prefix_len=20,
+                                                                             stream=stream)]
+        torch.cuda.synchronize()
+        got.append(r + [c.k[int(c.table[0, 0]), :, :3], c.v[int(c.table[1, 0]), :, :3]])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
@@ -490,6 +598,43 @@ def test_captured_steps_follow_growing_lengths(fa):
         step(caches[1])
         assert torch.equal(got[0], o) and torch.equal(got[1], lse), t
     assert torch.equal(caches[0].k.view(torch.int16), caches[1].k.view(torch.int16))
+
+
+def test_captured_rotation_and_prefix_replay(fa):
+    """rope, rope_bwd and fwd_prefix replay on new contents; two graphs of one call share no workspace."""
+    B, H, Hk, T, d, n = 3, 4, 2, 1, 64, 150
+    c = Cache(83, B, Hk, d, 16, 64, prefix_len=n)
+    c.fill(c.prefix_pages, n, 1)
+    for b in range(B):
+        c.fill(c.table[b], 64, 2 + b)
+    w, _ = fa.rope_freqs(d)
+    pages, table, lens = torch.from_numpy(c.prefix_pages).cuda(), c.device_table(), i32([1, 2, 3])
+    q = rand(84, B, H, T, d)
+
+    def step():
+        y, _ = fa.rope(q, None, w, offset=7)
+        o, lse = fa.fwd_prefix(y, c.k, c.v, pages, n, table, lens)
+        g, _ = fa.rope_bwd(o, None, w, offset=7)
+        return o, lse, g
+
+    step()
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in range(2)], []
+    for g in graphs:
+        with torch.cuda.graph(g):
+            outs.append(step())
+    for i in range(3):
+        lens.fill_(5 * i + 1)
+        q.copy_(rand(85 + i, B, H, T, d))
+        streams = [torch.cuda.Stream() for _ in graphs]
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):  # both at once
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        want = step()
+        for out in outs:
+            assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
 def test_two_streams_at_once(fa):
