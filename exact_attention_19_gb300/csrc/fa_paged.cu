@@ -159,12 +159,12 @@ struct Caches {
 // One part of a call: the prefix or the sequences' own keys.
 template <int D, bool PREFIX>
 int launch_part(const Caches& c, const fa::PagedParams& p, int grid, cudaStream_t stream) {
-  const int rb = p.rb[PREFIX];
+  const int rb = p.rb[PREFIX];  // a prefix's is 128 or 256 here
   CUtensorMap mk, mv;
   if (!c.maps(&mk, &mv, rb == 16 ? fa::PagedCfg<D>::kKeys : kTileKeys)) return FA_ERR_LAUNCH;
-  if (rb == 16) {
+  if (!PREFIX && rb == 16) {
     using S = fa::PagedCfg<D>;
-    return launch_kernel(fa::fa_paged_kernel<D, PREFIX>, grid, S::kThreads, S::kSmemBytes, stream, mk, mv, p);
+    return launch_kernel(fa::fa_paged_kernel<D, false>, grid, S::kThreads, S::kSmemBytes, stream, mk, mv, p);
   }
   if (rb == 128) {
     using T = fa::TileCfg<D, false>;
@@ -177,8 +177,17 @@ int launch_part(const Caches& c, const fa::PagedParams& p, int grid, cudaStream_
 
 template <int D>
 int launch(const Caches& c, const fa::PagedParams& p, const Layout& l, long long rows, cudaStream_t stream) {
-  int st = p.prefix_len > 0 ? launch_part<D, true>(c, p, l.grid[1], stream) : FA_OK;
-  if (st == FA_OK) st = launch_part<D, false>(c, p, p.own_grid, stream);
+  int st = FA_OK;
+  if (p.prefix_len > 0 && l.rb[1] == 16) {  // and so l.rb[0] == 16
+    using S = fa::PagedCfg<D>;
+    CUtensorMap mk, mv;
+    if (!c.maps(&mk, &mv, S::kKeys)) return FA_ERR_LAUNCH;
+    st = launch_kernel(fa::fa_paged_kernel<D, true>, p.prefix_ctas + p.own_grid, S::kThreads, S::kSmemBytes, stream,
+                       mk, mv, p);
+  } else {
+    if (p.prefix_len > 0) st = launch_part<D, true>(c, p, l.grid[1], stream);
+    if (st == FA_OK) st = launch_part<D, false>(c, p, p.own_grid, stream);
+  }
   return st == FA_OK ? launch_merge<D>(p, rows, stream) : st;
 }
 

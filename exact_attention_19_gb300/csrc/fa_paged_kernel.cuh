@@ -116,16 +116,15 @@ __host__ __device__ __forceinline__ int row_blocks(long long rows, int rb) { ret
 // a prefix kernel needs nothing of it and runs beside it (all work before the
 // prefix kernel is done, or that kernel would not have let this one start); it
 // waits before it ends, so that the merge, which waits for it, sees both.
+// `beside`: this is such a kernel.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-template <bool PREFIX>
-__device__ __forceinline__ void paged_begin(const PagedParams& p) {
-  if (PREFIX || p.prefix_len == 0) grid_wait();
+__device__ __forceinline__ void paged_begin(bool beside) {
+  if (!beside) grid_wait();
   grid_release();
 }
-template <bool PREFIX>
-__device__ __forceinline__ void paged_end(const PagedParams& p) {
-  if (!PREFIX && p.prefix_len > 0) grid_wait();
+__device__ __forceinline__ void paged_end(bool beside) {
+  if (beside) grid_wait();
 }
 
 constexpr int kPagedTile = 128;  // keys of a unit
@@ -237,10 +236,10 @@ struct PagedSchedule {
   }
   // where a row block's result goes: 0 the output, 1 whole_*, 2 piece_* (row = of the piece); first: the
   // segment holds the CTA's first unit
-  static __device__ __forceinline__ int target(const PagedParams& p, const PagedWalk& w, bool first, int r,
+  static __device__ __forceinline__ int target(const PagedParams& p, const PagedWalk& w, int block, bool first, int r,
                                                long long& row) {
     if (w.jend - w.j == w.n) return p.prefix_len > 0 ? 1 : 0;
-    const long long slot = 2ll * blockIdx.x + (first ? 0 : 1);
+    const long long slot = 2ll * block + (first ? 0 : 1);
     row = slot * RB + r;
     return 2;
   }
@@ -308,17 +307,18 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Block-wide: the CTA's share of the launch's units, as the walk's first
-// segment; false when it has none.  For own keys the units come from the
-// lengths, and CTA 0 leaves the plan for the merge kernel.
+// Block-wide: share `block` of the prefix's or the own keys' units, as the walk's
+// first segment; false when it has none.  For own keys the units come from the
+// lengths, and share 0 leaves the plan for the merge.
 template <int RB, int TILE, bool PREFIX, int THREADS>
-__device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scratch /* shared, THREADS / 32 + 2 */,
-                                            PagedWalk& w, bool& starts) {
+__device__ __forceinline__ bool paged_share(const PagedParams& p, const int block,
+                                            long long* scratch /* shared, THREADS / 32 + 2 */, PagedWalk& w,
+                                            bool& starts) {
   using S = PagedSchedule<RB, TILE, PREFIX>;
   if constexpr (PREFIX) {
-    if (static_cast<long long>(blockIdx.x) >= p.prefix_ctas) return false;
-    const long long g = cta_start(p.prefix_units, p.prefix_ctas, blockIdx.x);
-    return S::begin(p, w, g, cta_start(p.prefix_units, p.prefix_ctas, blockIdx.x + 1ll), 0, 0, starts);
+    if (block >= p.prefix_ctas) return false;
+    const long long g = cta_start(p.prefix_units, p.prefix_ctas, block);
+    return S::begin(p, w, g, cta_start(p.prefix_units, p.prefix_ctas, block + 1ll), 0, 0, starts);
   } else {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kWarps = THREADS / 32;
@@ -343,7 +343,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
         if (b < p.B) {
           const SeqKeys s = seq_keys(p, b);
           mine = per * S::units(tiles_of(s.lo, s.hi, TILE));
-          if (pass == 0 && blockIdx.x == 0 && __ldg(p.lens + b) > p.capacity) atomicOr(p.status, kPagedPage);
+          if (pass == 0 && block == 0 && __ldg(p.lens + b) > p.capacity) atomicOr(p.status, kPagedPage);
         }
         long long incl = mine;
 #pragma unroll
@@ -360,7 +360,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
           all += scratch[i];
         }
         first = before + incl - mine;
-        if (pass == 0 && blockIdx.x == 0 && b < p.B) p.plan[1 + b] = first;
+        if (pass == 0 && block == 0 && b < p.B) p.plan[1 + b] = first;
         if (pass == 1 && mine > 0 && first <= g && g < first + mine) {
           scratch[kWarps] = b;
           scratch[kWarps + 1] = first;
@@ -369,14 +369,14 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
         __syncthreads();
       }
       if (pass == 0) {
-        const long long ctas = paged_ctas(gridDim.x, run, RB);
-        if (blockIdx.x == 0 && threadIdx.x == 0) {
+        const long long ctas = paged_ctas(p.own_grid, run, RB);
+        if (block == 0 && threadIdx.x == 0) {
           p.plan[0] = run;
           p.plan[1 + p.B] = run;
         }
-        if (static_cast<long long>(blockIdx.x) >= ctas) return false;
-        g = cta_start(run, ctas, blockIdx.x);
-        gend = cta_start(run, ctas, blockIdx.x + 1ll);
+        if (block >= ctas) return false;
+        g = cta_start(run, ctas, block);
+        gend = cta_start(run, ctas, block + 1ll);
         if (g >= gend) return false;
       }
     }
@@ -384,16 +384,15 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, long long* scr
   }
 }
 
+// The CTA's share `block` of the prefix or of the own keys.
 template <int D, bool PREFIX>
-__global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
-    fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                    const PagedParams p) {
+__device__ __forceinline__ void paged_rows(const CUtensorMap& tmK, const CUtensorMap& tmV, const PagedParams& p,
+                                           const int block, uint8_t* const smem_raw, long long* const scratch,
+                                           const bool beside) {
   using C = PagedCfg<D>;
   using S = PagedSchedule<C::kRows, C::kTile, PREFIX>;
   constexpr int kNT = D / 8;   // 8-column tiles of O
   constexpr int kKT = D / 16;  // 16-deep steps of Q K^T
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ long long scratch[C::kWarps + 2];
   const uint32_t raw_addr = smem_addr(smem_raw);
   const uint32_t base = (raw_addr + 1023u) & ~1023u;
   uint8_t* const sbase = smem_raw + (base - raw_addr);
@@ -411,11 +410,11 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     tma_prefetch_map(&tmK);
     tma_prefetch_map(&tmV);
   }
-  paged_begin<PREFIX>(p);
+  paged_begin(beside);
   PagedWalk w;
   bool first;  // the segment holds the share's first unit
-  if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(p, scratch, w, first)) {
-    paged_end<PREFIX>(p);
+  if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(p, block, scratch, w, first)) {
+    paged_end(beside);
     return;
   }
   __syncthreads();
@@ -741,7 +740,7 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
       }
       const float inv = some ? 1.0f / l[i] : 0.f;
       long long row = out_row[i];
-      const int to = S::target(p, w, first, g8 + 8 * i, row);
+      const int to = S::target(p, w, block, first, g8 + 8 * i, row);
       if (to == 0) {
         uint16_t* const dst = p.out + row * D + col;
 #pragma unroll
@@ -762,7 +761,27 @@ __global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
     for (int i = consumed; i < issued; ++i)
       mbar_wait(bars + 8 * (i % C::kRing), static_cast<uint32_t>(i / C::kRing) & 1u, nullptr);
   }
-  paged_end<PREFIX>(p);
+  paged_end(beside);
+}
+
+// BOTH: the first prefix_ctas CTAs take the prefix's shares and the others the
+// own keys' (a prefix whose rows of the whole batch fit one block: one launch less,
+// 9.0 -> 8.1 us for 4 sequences behind 1000 tokens, 12 heads of 64).  Else the own keys alone.
+template <int D, bool BOTH>
+__global__ void __launch_bounds__(PagedCfg<D>::kThreads, 2)
+    fa_paged_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                    const PagedParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long scratch[PagedCfg<D>::kWarps + 2];
+  int block = static_cast<int>(blockIdx.x);
+  if constexpr (BOTH) {
+    if (block < static_cast<int>(p.prefix_ctas)) {
+      paged_rows<D, true>(tmK, tmV, p, block, smem_raw, scratch, false);
+      return;
+    }
+    block -= static_cast<int>(p.prefix_ctas);
+  }
+  paged_rows<D, false>(tmK, tmV, p, block, smem_raw, scratch, !BOTH && p.prefix_len > 0);
 }
 
 // ---------------------------------------------------------------------------

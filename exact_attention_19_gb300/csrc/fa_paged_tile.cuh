@@ -121,6 +121,8 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
     atomicOr(p.status, kPagedTimeout | (role << 8));
   };
   auto uniform = [](bool v) -> bool { return __all_sync(0xffffffffu, v); };
+  const bool beside = !PREFIX && p.prefix_len > 0;
+  const int block = static_cast<int>(blockIdx.x);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -139,17 +141,17 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
     tma_prefetch_map(&tmK);
     tma_prefetch_map(&tmV);
   }
-  paged_begin<PREFIX>(p);
+  paged_begin(beside);
   if (base & 1023u) {  // the swizzled layouts need it; the launch places it so
     if (threadIdx.x == 0) atomicOr(p.status, kPagedTimeout | (16u << 8));
-    paged_end<PREFIX>(p);
+    paged_end(beside);
     return;
   }
   PagedWalk w;
   bool first;  // the segment holds the share's first unit
   if (!paged_share<C::kRows, C::kTile, PREFIX, C::kThreads>(
-          p, reinterpret_cast<long long*>(tile_smem + C::kBarOff + kTileScratchOff), w, first)) {
-    paged_end<PREFIX>(p);
+          p, block, reinterpret_cast<long long*>(tile_smem + C::kBarOff + kTileScratchOff), w, first)) {
+    paged_end(beside);
     return;
   }
   if (warp == C::kWarpMma) {
@@ -582,7 +584,7 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
       {
         const long long out_row = S::row(p, v, PAIR ? t * 128 + r : r, lo, hi);
         long long row = out_row;
-        const int to = S::target(p, v, first, PAIR ? t * 128 + r : r, row);
+        const int to = S::target(p, v, block, first, PAIR ? t * 128 + r : r, row);
         // PAIR: the whole row; else warpgroup t's half of the columns
         constexpr int kCols = PAIR ? D : D / 2;
         const int col0 = PAIR ? 0 : t * kCols;
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
-  paged_end<PREFIX>(p);
+  paged_end(beside);
 }
 
 }  // namespace fa
