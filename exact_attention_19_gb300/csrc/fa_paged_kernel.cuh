@@ -216,23 +216,32 @@ struct PagedSchedule {
   static __device__ __forceinline__ const int* pages(const PagedParams& p, const PagedWalk& w) {
     return PREFIX ? p.prefix_pages : p.table + static_cast<long long>(w.b) * p.max_pages;
   }
-  // The row of [B * H * T] that row r of the segment's block is (-1: none) and the keys [lo, hi) it sees; a row
-  // that does not exist needs no mask, as nothing of it is stored.
-  static __device__ __forceinline__ long long row(const PagedParams& p, const PagedWalk& w, int r, int& lo, int& hi) {
-    int b = w.b, rr = w.rb * RB + r;
+  // The row of [B * H * T] that row r of the segment's block is (-1: none): row rr of sequence b and the
+  // segment's K/V head.
+  static __device__ __forceinline__ long long row(const PagedParams& p, const PagedWalk& w, int r, int& b, int& rr) {
+    b = w.b;
+    rr = w.rb * RB + r;
     bool there = rr < p.rows;
     if constexpr (PREFIX) {
       b = rr / p.rows;
       rr -= b * p.rows;
       there = b < p.B;
     }
+    return there ? (static_cast<long long>(b) * p.Hk + w.hk) * p.rows + rr : -1;
+  }
+  // The same with the keys [lo, hi) that the row sees; a row that does not exist needs no mask, as nothing of it
+  // is stored.
+  static __device__ __forceinline__ long long row_keys(const PagedParams& p, const PagedWalk& w, int r, int& lo,
+                                                       int& hi) {
+    int b, rr;
+    const long long at = row(p, w, r, b, rr);
     lo = 0;
     hi = 0x7fffffff;
-    if (!there) return -1;
+    if (at < 0) return at;
     const SeqKeys s = seq_keys(p, b);
     if constexpr (PREFIX) hi = row_prefix_keys(p, s, rr % p.T);
     else row_own_keys(p, s, rr % p.T, lo, hi);
-    return (static_cast<long long>(b) * p.Hk + w.hk) * p.rows + rr;
+    return at;
   }
   // where a row block's result goes: 0 the output, 1 whole_*, 2 piece_* (row = of the piece); first: the
   // segment holds the CTA's first unit
@@ -540,7 +549,7 @@ __device__ __forceinline__ void paged_rows(const CUtensorMap& tmK, const CUtenso
     bool none[2];          // the row sees no key
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      out_row[i] = S::row(p, w, g8 + 8 * i, lo[i], hi[i]);
+      out_row[i] = S::row_keys(p, w, g8 + 8 * i, lo[i], hi[i]);
       const bool there = out_row[i] >= 0;
       none[i] = hi[i] <= lo[i];  // such a row is not masked either (its warp would mask every tile), but dropped
       if (none[i]) lo[i] = 0, hi[i] = 0x7fffffff;

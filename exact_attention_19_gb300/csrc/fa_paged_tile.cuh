@@ -358,8 +358,8 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
         long long row[C::kRows / 64];
 #pragma unroll
         for (int i = 0; i < C::kRows / 64; ++i) {
-          int lo, hi;
-          row[i] = S::row(p, w, 64 * i + tid, lo, hi);
+          int b, rr;
+          row[i] = S::row(p, w, 64 * i + tid, b, rr);
         }
 #pragma unroll
         for (int i = 0; i < C::kRows / 64; ++i) {
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
         k0 = (v.tile0 + jlo) * C::kTile;
         low_edge = k0 < v.lo;
         high_edge = (v.tile0 + jhi) * C::kTile > v.hi;
-        const bool there = S::row(p, v, PAIR ? t * 128 + r : r, lo, hi) >= 0;
+        const bool there = S::row_keys(p, v, PAIR ? t * 128 + r : r, lo, hi) >= 0;
         // A row that sees no key is not masked (its warp would mask every tile) but dropped at the end, and a warp
         // of such rows has nothing to do.
         none = hi <= lo;
@@ -582,7 +582,8 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
       }
       PagedWalk v = *walk;
       {
-        const long long out_row = S::row(p, v, PAIR ? t * 128 + r : r, lo, hi);
+        int b, rr;
+        const long long out_row = S::row(p, v, PAIR ? t * 128 + r : r, b, rr);
         long long row = out_row;
         const int to = S::target(p, v, block, first, PAIR ? t * 128 + r : r, row);
         // PAIR: the whole row; else warpgroup t's half of the columns
