@@ -66,11 +66,17 @@ bool make_cache_map(CUtensorMap* map, const void* ptr, int d, int page, int Hk, 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
 // Rows per row block, by the rows that share each K/V byte: the warp-level
-// kernel's 16, or the tcgen05 kernel's 128 or 256.
+// kernel's 16, or the tcgen05 kernel's 128 (one query tile) or 256 (a pair).
+// d = 128, 16 sequences x 8192 keys, 2 K/V heads, us: 16 rows 29.5 on the
+// warp-level kernel, 35.9 on the tile kernel (1000 keys: 11.1, 14.9); 32 rows as
+// two row blocks of 16 read K and V twice, 33.2 against 36.6 while they stay in
+// L2, but 319 against 169 for 32 x 8192 keys of 8 heads; 128 rows 41.9 on one
+// query tile, 44.8 as half of a pair; 256 rows 47.8 on a pair, 52.6 on two tiles.
 int block_rows(long long rows) { return rows <= 16 ? 16 : (rows <= 128 ? 128 : 256); }
 constexpr int kTileKeys = fa::kPagedTile;
 int grid_of(int block_rows, int sms) { return block_rows == 16 ? 2 * sms : sms; }  // all CTAs resident
 
+// Tiles of 128 keys per CTA up to which own keys leave the prefix its SMs.
 constexpr long long kLongOwn = 16;
 
 // The row blocks, tiles and CTAs of a call, and the parts of its workspace, in
@@ -98,7 +104,7 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
       l.prefix_blocks = fa::row_blocks(rows * B, l.rb[1]);
       l.prefix_tiles = (prefix_len + kTileKeys - 1) / kTileKeys;
       l.prefix_units = 1ll * Hk * l.prefix_blocks * (l.prefix_tiles + fa::extra_units(l.rb[1]));
-      l.prefix_ctas = fa::paged_ctas(l.grid[1], l.prefix_units, l.rb[1]);
+      l.prefix_ctas = fa::paged_ctas(l.grid[1], l.prefix_units, fa::least_units(l.rb[1], true));
       l.grid[1] = static_cast<int>(l.prefix_ctas);
     }
     const size_t pieces = 2 * static_cast<size_t>(l.grid[i]) * l.rb[i];
@@ -112,6 +118,9 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
 
 // The merge: from kMergeRows rows, or kMergeFewRows with at most kMergeParts parts to a row, one warp joins
 // four rows; else two warps join one (from kMergeFewRows rows, so that one wave of CTAs holds them) or four.
+// Whole calls, us: 16384 rows 71 with a warp for four rows, 85 with four warps to each; 2048 rows of 3 parts 37.1
+// with a warp for four, 38.6 with four to one; 2048 rows of 11 parts 36.3 with two to one, 40.2 with four; 1152
+// rows of 12 parts 64.3 with four to one, 70.4 with a warp for four.
 constexpr long long kMergeRows = 8192, kMergeFewRows = 1536, kMergeParts = 4;
 
 // Programmatic dependent launch: the kernel may be scheduled while the one ahead

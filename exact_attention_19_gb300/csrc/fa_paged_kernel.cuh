@@ -17,7 +17,7 @@
 // there, so the host needs none of them and a captured launch stays right as
 // the sequences grow.  A CTA that holds all units of a row block writes its
 // output; else it writes its part (O normalised by its own sum, and L, the
-// base-2 log of that sum) and fa_paged_merge_kernel joins the parts:
+// base-2 log of that sum) and a merge kernel joins the parts:
 //   L = log2 sum 2^L_i,  O = sum 2^(L_i - L) O_i.
 #pragma once
 
@@ -89,11 +89,16 @@ __device__ __forceinline__ int row_prefix_keys(const PagedParams& p, const SeqKe
   return (t < s.fresh && s.len - s.fresh + t >= 0) ? p.prefix_len : 0;
 }
 
-// CTAs that `units` units of a row block of rb rows are shared among: at least so
-// many units each that the parts' O (rb * D * 4 bytes, written and read again)
-// stays small beside the keys they read (512 D bytes a tile of 128).
-__host__ __device__ __forceinline__ long long paged_ctas(long long grid, long long units, int rb) {
-  const long long most = units / (rb == 16 ? 1 : rb == 128 ? 4 : 8);
+// Units that a CTA takes at least: with fewer, the parts' O (rb * D * 4 bytes,
+// written and read again) outweighs the keys they read (512 D bytes a tile), with
+// more, short calls leave SMs idle.  Row blocks of 256: 8 for a prefix (64
+// sequences behind 8192 tokens: 36 us, with 4 it takes 58), 3 for own keys (16 x
+// 1000 keys, 2 K/V heads: 21 us, with 8 it takes 27).
+__host__ __device__ constexpr int least_units(int rb, bool prefix) {
+  return rb == 16 ? 1 : rb == 128 ? 4 : prefix ? 8 : 3;
+}
+__host__ __device__ __forceinline__ long long paged_ctas(long long grid, long long units, int least) {
+  const long long most = units / least;
   return most < 1 ? 1 : (most < grid ? most : grid);
 }
 // a / b for a >= 0, b > 0: a 32-bit division where both fit (a 64-bit one is a long instruction sequence)
@@ -378,7 +383,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, const int bloc
         __syncthreads();
       }
       if (pass == 0) {
-        const long long ctas = paged_ctas(p.own_grid, run, RB);
+        const long long ctas = paged_ctas(p.own_grid, run, least_units(RB, false));
         if (block == 0 && threadIdx.x == 0) {
           p.plan[0] = run;
           p.plan[1 + p.B] = run;
@@ -816,7 +821,7 @@ struct RowParts {
   // all: units of the launch, u0 and u1: of the sequences before this one, and with it
   __device__ __forceinline__ void find(const PagedParams& p, long long all, long long u0, long long u1) {
     units = all;
-    ctas = paged_ctas(p.own_grid, all, p.rb[0]);
+    ctas = paged_ctas(p.own_grid, all, least_units(p.rb[0], false));
     const int blocks = row_blocks(p.rows, p.rb[0]);
     const long long each = quotient(u1 - u0, static_cast<long long>(p.Hk) * blocks);
     const long long n = each - extra_units(p.rb[0]);  // tiles; none: each is 0

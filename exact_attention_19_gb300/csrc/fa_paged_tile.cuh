@@ -24,6 +24,14 @@
 // Keys outside the segment's range (the end of a page, pages given back below a
 // window) are masked in S; their V rows, which may hold anything, are zeroed in
 // shared memory by the softmax warps before they hand over P (0 * NaN is NaN).
+//
+// Bound: with few rows DRAM (a tile's K and V, 64 KB at D = 128, take 1.5 us of an
+// SM's share of 6.8 TB/s; loop alone about 7 TB/s on 32 rows), with a pair the
+// tensor pipe (1.5 us a tile against 1.35 at the measured bf16 rate; 2 x 256
+// tokens of 32/8 heads over 65536 keys: 1270-1360 TFLOP/s).  Short calls are bound
+// by what the loop does not cover: 6 us to the first scores (the lengths, then
+// 224 KB of Q, K and V per SM at once), 3 us for the last row block's output, the
+// merge.
 #pragma once
 
 #include "fa_paged_kernel.cuh"
@@ -393,7 +401,7 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
     const float NEG_INF = -__int_as_float(0x7f800000);
     float2* const stats = reinterpret_cast<float2*>(tile_smem + C::kStatOff);
     // The walk lies in shared memory while the tile loop runs: the S row takes 128 registers, and a walk kept
-    // beside it was spilled and reloaded for every tile (94 us against 71 for 2 x 256 tokens over 8192, 32/8 heads).
+    // beside it was spilled and reloaded for every tile (2 x 256 tokens over 8192, 32/8 heads: 94 us, not 90).
     PagedWalk* const walk = reinterpret_cast<PagedWalk*>(tile_smem + C::kBarOff + kTileWalkOff) + warp;
     auto put_walk = [&](const PagedWalk& v) {
       __syncwarp();
