@@ -17,6 +17,11 @@
 // elements (two 16-byte chunks, 8 pairs) of one token and walks over heads with
 // its 8 cosines and sines in registers, so the angles are computed once per
 // token and chunk, not per head.
+// 4 x 8192 tokens, 32 + 8 heads of 128 (671 MB): 103 us, 6.5 TB/s, 96% of the
+// copy rate; 3 x 4099 tokens, 16 + 16 heads (201 MB), 34.5 us, 86% (one and a
+// half waves of CTAs); a call of 256 tokens 3.4 us, its launch.  Appending 4 x up
+// to 2048 tokens, 32 + 2 x 8 heads (115 MB): 22.9 us, 74% (the page's index comes
+// before the first store).
 #pragma once
 
 #include <cstdint>
@@ -120,22 +125,16 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
   const int h_lo = blockIdx.y * p.heads_per_cta, h_hi = h_lo + p.heads_per_cta;
 
   long long pos;
-  long long page = 0, slot = 0;
-  bool cached = true;  // the token has a slot in the cache
+  long long page = -1, slot = 0;  // the token's place in the cache; page: checked where it is used, so that the
+                                  // first heads' loads need not wait for it
   if constexpr (PAGED) {
-    const int fresh = p.new_lens ? min(p.new_lens[b], p.N) : p.N;
-    if (n >= fresh) return;
-    const long long own = static_cast<long long>(p.seq_lens[b]) - fresh + n;
-    if (own < 0) return;  // no token: a padded entry of the batch
+    const int len = p.seq_lens[b], fresh = p.new_lens ? min(p.new_lens[b], p.N) : p.N;
+    const long long own = static_cast<long long>(len) - fresh + n;
+    if (n >= fresh || own < 0) return;  // padding, or a padded entry of the batch
     pos = p.offset + own;
     if (h_hi > p.heads[0]) {
       const long long pi = own >> p.page_shift;
-      cached = pi < p.max_pages;
-      if (cached) {
-        page = p.block_table[static_cast<long long>(b) * p.max_pages + pi];
-        cached = page >= 0 && page < p.n_pages;
-      }
-      if (!cached && u == 0) atomicOr(p.status, kStatusPage);
+      if (pi < p.max_pages) page = p.block_table[static_cast<long long>(b) * p.max_pages + pi];
       slot = own & ((1ll << p.page_shift) - 1);
     }
   } else {
@@ -167,15 +166,10 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
     const int lo = max(h_lo - first, 0), hi = min(h_hi - first, p.heads[t]);
     first += p.heads[t];
     if (lo >= hi) continue;
-    const uint16_t* src = p.src[t] + b * p.src_s[t].b + n * p.src_s[t].n;
-    uint16_t* dst;
-    if (PAGED && t > 0) {
-      if (!cached) continue;
-      dst = p.dst[t] + page * p.dst_s[t].b + slot * p.dst_s[t].n;
-    } else {
-      dst = p.dst[t] + b * p.dst_s[t].b + n * p.dst_s[t].n;
-    }
-    constexpr int kU = 4;  // heads in flight: 8 loads of 16 bytes per thread
+    const uint16_t* const src = p.src[t] + b * p.src_s[t].b + n * p.src_s[t].n;
+    // heads in flight, two loads of 16 bytes each (4 x 2048 appended: 22.9 us with 2, 23.7 with 4; 4 x 8192
+    // rotated: 104.7 with 2, 103.1 with 4)
+    constexpr int kU = PAGED ? 2 : 4;
     for (int h = lo; h < hi; h += kU) {
       uint4 a[kU], e[kU];
 #pragma unroll
@@ -184,6 +178,16 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
           a[i] = *reinterpret_cast<const uint4*>(src + (h + i) * p.src_s[t].h + c0);
           e[i] = *reinterpret_cast<const uint4*>(src + (h + i) * p.src_s[t].h + c1);
         }
+      uint16_t* dst = p.dst[t];
+      if (PAGED && t > 0) {
+        if (page < 0 || page >= p.n_pages) {  // the token has no slot
+          if (u == 0) atomicOr(p.status, kStatusPage);
+          break;
+        }
+        dst += page * p.dst_s[t].b + slot * p.dst_s[t].n;
+      } else {
+        dst += b * p.dst_s[t].b + n * p.dst_s[t].n;
+      }
 #pragma unroll
       for (int i = 0; i < kU; ++i)
         if (h + i < hi) {
