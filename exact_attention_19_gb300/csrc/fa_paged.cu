@@ -220,8 +220,8 @@ int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
     return FA_ERR_SHAPE;
   if (left < -1 || right < -1 || prefix_len < 0 || prefix_len > kMaxKeys) return FA_ERR_SHAPE;
   const long long rows = static_cast<long long>(B) * H * T;
-  if (static_cast<long long>(max_pages) * page_size > kMaxKeys || rows >= (1ll << 31) ||
-      static_cast<long long>(B) * H >= (1ll << 31))
+  if (static_cast<long long>(max_pages) * page_size > kMaxKeys || static_cast<long long>(B) * H >= (1ll << 31) ||
+      rows >= (1ll << 31) - 256)  // a row block's last row still has an int's index
     return FA_ERR_SHAPE;
   if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_SCALE;
   for (int i = 0; i < 6; ++i)  // page, head and token strides of K, then of V; a tensor map's limit is 2^40 bytes

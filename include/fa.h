@@ -256,8 +256,9 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const double
  *           of q_out, then page, head and token strides of k_cache and v_cache.
  * rot       0 (nothing turns; inv_freq may be NULL) or as in fa_rope; position =
  *           offset + own position (a shared prefix's length goes in offset).
- * Two tokens of one call must not share a slot.  Cache slots of other tokens
- * stay as they are.  Errors as fa_rope; T == 0 is a successful no-op.
+ * q_out may be q itself (same pointer, same strides); no other output may overlap
+ * an input.  Two tokens of one call must not share a slot.  Cache slots of other
+ * tokens stay as they are.  Errors as fa_rope; T == 0 is a successful no-op.
  * The first call on a device looks up the status word's address there: make
  * that first call before any stream capture.
  */
@@ -271,7 +272,8 @@ int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, void*
  * sequences' cached keys, grouped heads included: query head h reads K/V head
  * h / (H / Hk).
  *
- * q, o  bf16 [B, H, T, d] contiguous;  lse fp32 [B, H, T].
+ * q, o  bf16 [B, H, T, d] contiguous;  lse fp32 [B, H, T].  The outputs must not
+ *       overlap each other or any input.
  * The token at own position pos sees own keys j with
  *     pos - window_left <= j <= pos + window_right,   0 <= j < seq_lens[b],
  * -1 leaving a side open: (-1, 0) is causal, (-1, -1) every cached key (an

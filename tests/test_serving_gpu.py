@@ -637,6 +637,39 @@ def test_captured_rotation_and_prefix_replay(fa):
             assert all(torch.equal(a, b) for a, b in zip(out, want))
 
 
+def test_capture_behind_copies_and_joined_streams(fa):
+    """The calls inside a larger graph: behind a copy and a fill, and behind two streams that join."""
+    B, H, Hk, T, d = 2, 4, 2, 1, 64
+    c = Cache(87, B, Hk, d, 16, 200)
+    for b in range(B):
+        c.fill(c.table[b], 200, b)
+    table, lens, q = c.device_table(), i32([200, 150]), rand(88, B, H, T, d)
+    q_in, lens_in = rand(89, B, H, T, d), i32([31, 180])
+    x = torch.zeros(1 << 20, device="cuda")
+    fa.fwd_paged(q, c.k, c.v, table, lens)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        q.copy_(q_in)
+        lens.copy_(lens_in)
+        first = fa.fwd_paged(q, c.k, c.v, table, lens)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            x.add_(1.0)
+            q.copy_(q_in.flip(0))
+        x[:7].zero_()
+        torch.cuda.current_stream().wait_stream(side)
+        second = fa.fwd_paged(q, c.k, c.v, table, lens)
+        x.mul_(2.0)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for got, qq in ((first, q_in), (second, q_in.flip(0).contiguous())):
+        want = fa.fwd_paged(qq, c.k, c.v, table, lens_in)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_two_streams_at_once(fa):
     """Calls on two streams, each with its own workspace, give what they give alone."""
     B, H, Hk, T, d = 4, 8, 2, 1, 128
