@@ -292,6 +292,7 @@ def paged_case(fa, seed, B, H, Hk, T, d, page, lens, new=None, window=(-1, 0), t
     (1, 2, 1, 1, 256, [20000], None),                             # one row block in the shares of every CTA
     (1, 40, 1, 1, 128, [9000], None),
     (400, 4, 4, 6, 16, [6 + i % 30 for i in range(400)], None),   # 9600 rows to merge
+    (2500, 1, 1, 1, 16, [i * 13 % 47 for i in range(2500)], None),
 ])
 def test_paged(fa, B, H, Hk, T, d, page, lens, new):
     paged_case(fa, 1 + B, B, H, Hk, T, d, page, lens, new)
@@ -365,9 +366,10 @@ def test_paged_repeats_bit_for_bit_and_takes_buffers(fa):
     assert e.value.status == 11
 
 
-def test_bad_pages_and_lengths_are_reported(fa):
+@pytest.mark.parametrize("T", [1, 40])
+def test_bad_pages_and_lengths_are_reported(fa, T):
     """A page index outside the cache, or a length past the table: no access outside, FA_ERR_PAGE."""
-    B, H, Hk, T, d, page = 2, 2, 1, 1, 64, 16
+    B, H, Hk, d, page = 2, 2, 1, 64, 16
     c = Cache(51, B, Hk, d, page, 64)
     lens = [40, 64]
     for b in range(B):
@@ -383,7 +385,7 @@ def test_bad_pages_and_lengths_are_reported(fa):
         assert (st, word) == (12, 2)
         assert torch.equal(o[1], good[1]) and bool(torch.isfinite(o).all())
         k0 = c.k.clone()
-        fa.kv_append(None, rand(1, B, Hk, T, d), rand(2, B, Hk, T, d), c.k, c.v, c.device_table(), i32([17, 0]))
+        fa.kv_append(None, rand(1, B, Hk, 1, d), rand(2, B, Hk, 1, d), c.k, c.v, c.device_table(), i32([17, 0]))
         st, word = fa.fa_fwd_status(None, clear=True)
         assert (st, word) == (12, 2)
         assert torch.equal(c.k, k0)
@@ -391,8 +393,12 @@ def test_bad_pages_and_lengths_are_reported(fa):
     o, _ = run_paged(fa, c, q, [65, 64], None)
     assert fa.fa_fwd_status(None, clear=True)[0] == 12
     assert torch.equal(o[1], good[1])
-    fa.kv_append(None, rand(1, B, Hk, T, d), rand(2, B, Hk, T, d), c.k, c.v, c.device_table(), i32([65, 0]))
+    fa.kv_append(None, rand(1, B, Hk, 1, d), rand(2, B, Hk, 1, d), c.k, c.v, c.device_table(), i32([65, 0]))
     assert fa.fa_fwd_status(None, clear=True)[0] == 12
+    for bad in (-1, c.k.shape[0]):
+        c.prefix_pages = np.array([0, bad], dtype=np.int32)
+        o, _ = run_paged(fa, c, q, lens, None, prefix_len=20)
+        assert fa.fa_fwd_status(None, clear=True)[0] == 12 and bool(torch.isfinite(o).all())
 
 
 def test_nan_reaches_the_rows_that_see_it_and_no_others(fa):
