@@ -138,8 +138,7 @@ int launch_kernel(K kernel, long long grid, int threads, size_t smem, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  return (e == cudaSuccess && cudaGetLastError() == cudaSuccess) ? FA_OK : FA_ERR_LAUNCH;
+  return fa_host::launched(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 template <int D>

@@ -43,12 +43,12 @@ int launch(fa::RopeParams& p, int interleaved, int sms, cudaStream_t stream) {
   if (groups > 65535) groups = 65535;  // grid y
   p.heads_per_cta = static_cast<int>((heads + groups - 1) / groups);
   groups = (heads + p.heads_per_cta - 1) / p.heads_per_cta;
-  const dim3 grid(static_cast<unsigned>(tiles), static_cast<unsigned>(groups));
-  if (interleaved)
-    fa::fa_rope_kernel<D, true, PAGED><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-  else
-    fa::fa_rope_kernel<D, false, PAGED><<<grid, fa::kRopeThreads, 0, stream>>>(p);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles), static_cast<unsigned>(groups));
+  cfg.blockDim = dim3(fa::kRopeThreads);
+  cfg.stream = stream;
+  return fa_host::launched(interleaved ? cudaLaunchKernelEx(&cfg, fa::fa_rope_kernel<D, true, PAGED>, p)
+                                       : cudaLaunchKernelEx(&cfg, fa::fa_rope_kernel<D, false, PAGED>, p));
 }
 
 bool misaligned(const void* p) { return reinterpret_cast<uintptr_t>(p) & 15u; }

@@ -318,8 +318,8 @@ def fwd_paged(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = 
     q: [B, H, T, d] contiguous CUDA bf16 (as ``kv_append`` returns it), T from 1 (decoding) to a prompt's chunk;
     H a multiple of the cache's heads (query head h reads K/V head h // (H / Hk)).  The cache, block_table,
     seq_lens (with the new tokens) and new_lens as in ``kv_append``.  ``window=(left, right)`` as in ``fwd``,
-    around the token's own position: (-1, 0) is causal, (-1, -1) every cached key.  Padding rows and rows
-    that see no key get O = 0 and LSE = -inf.  The lengths are read on the GPU, so a captured call stays
+    around the token's own position: (-1, 0) is causal, (-1, -1) every cached key (an encoder's states: from
+    rows at negative positions too).  Rows past new_lens and rows that see no key get O = 0 and LSE = -inf.  The lengths are read on the GPU, so a captured call stays
     right as they grow.  ``workspace`` (``fa_paged_workspace_bytes(B, H, Hk, T, d, 0)`` bytes) may be given; calls
     that may overlap need one each.  Runs on ``stream`` (default: the current torch stream), asynchronously.
     """

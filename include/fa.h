@@ -277,8 +277,10 @@ int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, void*
  * The token at own position pos sees own keys j with
  *     pos - window_left <= j <= pos + window_right,   0 <= j < seq_lens[b],
  * -1 leaving a side open: (-1, 0) is causal, (-1, -1) every cached key (an
- * encoder's states of a length per sequence).  Padding rows and rows that see
- * no key get O = 0, LSE = -inf.  Slots outside every row's window or past the
+ * encoder's states of a length per sequence; with more new rows than keys the
+ * first rows' positions are negative, and a window open or wide enough to the
+ * right still reaches keys from there).  Rows from new_lens[b] on and rows that
+ * see no key get O = 0, LSE = -inf.  Slots outside every row's window or past the
  * length may hold anything, NaN included; a key that some rows of a sequence
  * see and others do not must be finite.
  * strides    host array of 6: page, head and token strides of k_cache, v_cache.

@@ -121,6 +121,38 @@ def test_rope_in_place_and_strided_outputs(fa):
     assert torch.equal(v, v0)  # the packed neighbour is untouched
 
 
+def test_an_error_left_behind_is_not_this_calls(fa):
+    """A runtime call that failed earlier in the process leaves its error to be read: the calls here go by their own
+    launches, so nothing is reported, run again or, in place, turned twice."""
+    import ctypes
+
+    runtime = ctypes.CDLL("libcudart.so.13")
+    q = rand(64, 1, 2, 40, 64)
+    w, _ = fa.rope_freqs(64)
+    want, _ = fa.rope(q, None, w)
+    c = Cache(65, 1, 2, 64, 16, 64)
+    table, lens, k = c.device_table(), i32([40]), rand(66, 1, 2, 40, 64)
+    fa.kv_append(None, k, k, c.k, c.v, table, lens, w)
+    want_o, _ = fa.fwd_paged(want, c.k, c.v, table, lens)
+    a, b = q.clone(), q.clone()
+    torch.cuda.synchronize()
+    try:
+        def left():
+            runtime.cudaSetDevice(1 << 20)  # no such device
+            assert runtime.cudaPeekAtLastError() != 0
+
+        left()
+        fa.rope(a, None, w, q_out=a)
+        left()
+        fa.kv_append(b, k, k, c.k, c.v, table, lens, w, q_out=b)
+        o, lse = torch.empty_like(q), torch.empty(1, 2, 40, dtype=torch.float32, device="cuda")
+        left()
+        fa.fwd_paged(want, c.k, c.v, table, lens, out=o, lse=lse)
+    finally:
+        runtime.cudaGetLastError()
+    assert torch.equal(a, want) and torch.equal(b, want) and torch.equal(o, want_o)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 @pytest.mark.parametrize("d,rot", [(64, 64), (128, 48)])
 def test_rope_backward(fa, d, rot, interleaved):
