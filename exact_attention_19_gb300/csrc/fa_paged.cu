@@ -70,7 +70,10 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 // d = 128, 16 sequences x 8192 keys, 2 K/V heads, us: 16 rows 29.5 on the
 // warp-level kernel, 35.9 on the tile kernel (1000 keys: 11.1, 14.9); 32 rows as
 // two row blocks of 16 read K and V twice, 33.2 against 36.6 while they stay in
-// L2, but 319 against 169 for 32 x 8192 keys of 8 heads; 128 rows 41.9 on one
+// L2, but 319 against 169 for 32 x 8192 keys of 8 heads; blocks of 32 rows on
+// warp-level MMAs run at 158 TFLOP/s, that path's rate: 16 x up to 1000 keys 12.8
+// against 15.6, but 32 x up to 8192 of 8 heads 113.8 against 103.2, and the host
+// does not know the lengths; 128 rows 41.9 on one
 // query tile, 44.8 as half of a pair; 256 rows 47.8 on a pair, 52.6 on two tiles.
 int block_rows(long long rows) { return rows <= 16 ? 16 : (rows <= 128 ? 128 : 256); }
 constexpr int kTileKeys = fa::kPagedTile;
