@@ -469,6 +469,58 @@ def test_pages_shared_between_sequences(fa):
     assert float((o[0].float() - o[1].float()).abs().max()) <= 4 * ref.U * float(o.float().abs().max())
 
 
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_keys_and_values_in_one_tensor(fa, T):
+    """K and V as views of one allocation, [n_pages, 2, page, Hk, d] and heads outermost: other page, head and
+    token strides for the same calls, to the bit."""
+    B, H, Hk, d, page, lens = 2, 4, 2, 64, 32, [300, 411]
+    q, k, v = rand(71, B, H, T, d), rand(72, B, Hk, T, d), rand(73, B, Hk, T, d)
+    w, _ = fa.rope_freqs(d)
+    base = Cache(70, B, Hk, d, page, max(lens))
+    for b in range(B):
+        base.fill(base.table[b], lens[b] - T, 74 + b)
+    n = base.k.shape[0]
+    one = torch.full((n, 2, page, Hk, d), math.nan, dtype=torch.bfloat16, device="cuda")
+    heads = torch.full((2, Hk, n, page, d), math.nan, dtype=torch.bfloat16, device="cuda")
+    views = [(base.k, base.v), tuple(one[:, i].transpose(1, 2) for i in range(2)),
+             tuple(heads[i].transpose(0, 1) for i in range(2))]
+    results = []
+    keep = base.k.clone(), base.v.clone()
+    for kc, vc in views:
+        kc.copy_(keep[0])
+        vc.copy_(keep[1])
+        turned = fa.kv_append(q, k, v, kc, vc, base.device_table(), i32(lens), w)
+        results.append(fa.fwd_paged(turned, kc, vc, base.device_table(), i32(lens)) + (kc.clone(), vc.clone()))
+    want = ref.paged(f64(turned), f64(results[0][2]), f64(results[0][3]), base.table, lens, [T] * B, -1, 0, d ** -0.5)
+    ref.check_attention(f64(results[0][0]), f64(results[0][1]), want)
+    for r in results[1:]:
+        assert torch.equal(r[0], results[0][0]) and torch.equal(r[1], results[0][1])
+        for a, b in zip(r[2:], results[0][2:]):
+            assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+def test_a_long_prompt_at_once(fa):
+    """A prompt of 5000 tokens appended and attended in one call, beside a sequence that has one token more."""
+    H, Hk, d, page, T, lens, new = 4, 2, 128, 64, 5000, [5000, 700], [5000, 1]
+    c = Cache(75, 2, Hk, d, page, max(lens))
+    c.fill(c.table[1], lens[1] - 1, 76)
+    q, k, v = rand(77, 2, H, T, d), rand(78, 2, Hk, T, d), rand(79, 2, Hk, T, d)
+    w, _ = fa.rope_freqs(d, base=500000.0)
+    turned = fa.kv_append(q, k, v, c.k, c.v, c.device_table(), i32(lens), w, new_lens=i32(new))
+    o, lse = fa.fwd_paged(turned, c.k, c.v, c.device_table(), i32(lens), new_lens=i32(new))
+    rows = [0, 1, 127, 128, 255, 256, 2500, 4735, 4998, 4999]  # of the first sequence, and the second's one
+    for b, at in ((0, rows), (1, [0])):
+        n = lens[b]
+        keys, values = ([ref.gather(f64(x), c.table[b], n, hk) for hk in range(Hk)] for x in (c.k, c.v))
+        for h in range(H):
+            kk, vv = keys[h // (H // Hk)], values[h // (H // Hk)]
+            pos = np.array([n - new[b] + t for t in at])
+            got_q = f64(turned[b, h])[at]
+            want = ref.attend(got_q, kk, vv, np.zeros(len(at), int), pos + 1, d ** -0.5)
+            ref.check_attention(f64(o[b, h])[at], f64(lse[b, h])[at], (want[0], want[1], want[2]))
+    assert float(o[1, :, 1:].abs().max()) == 0 and bool(torch.isneginf(lse[1, :, 1:]).all())
+
+
 def test_caches_and_strides_past_32_bits(fa):
     """A cache of more than 2^31 elements whose last pages are used, and a view with row strides as large."""
     n_pages, page, d = 140000, 256, 64
