@@ -203,8 +203,12 @@ size_t fa_bwd_workspace_bytes(int B, int H, int Nq);
  *             An output may be its own input (same pointer, same strides);
  *             otherwise it must not overlap an input.
  * inv_freq    fp64 [rot / 2], radians per position (any scaling of long
- *             contexts is in these values and in mag).  The angle is exact for
- *             every position: positions multiply a 64-bit fraction of a turn.
+ *             contexts is in these values and in mag).  A position p multiplies
+ *             a 64-bit fraction of a turn: the angle is off by at most
+ *             |p| (2^-65 + |inv_freq| 2^-72) turns, then fp32's relative error
+ *             (sine and cosine too, near their zeros as elsewhere).  Any 32-bit
+ *             position is far below a bf16 rounding, and so are offsets up to
+ *             2^48 in size; past that the angle fades out.
  * positions   int32 [B, N] (position_stride, >= N, int32s from one sequence to the
  *             next) or one row for all (position_stride 0); NULL: position
  *             = offset + row.  offset is added in both cases.

@@ -1,0 +1,54 @@
+"""The serving operators at their edges: angles near zero, frequencies and values that are not finite, new lengths
+under a window, calls whose input is the call before's output, and prefixes long enough for every way the work of
+prefix and own keys is shared out.
+"""
+import math
+
+import numpy as np
+import pytest
+
+import serving_ref as ref
+
+torch = pytest.importorskip("torch")
+
+from test_serving_gpu import Cache, _status, f64, fa, i32, paged_case, rand, run_paged  # noqa: E402,F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("zero", [0, 1])
+def test_rope_keeps_the_relative_accuracy_of_sine_and_cosine(fa, zero, interleaved):
+    """Pairs one element of which is zero: the results are the other one times a sine or a cosine alone, so an error
+    that is small only beside one shows.  Slow pairs at small positions have sines down to 1e-8.
+
+    Roundings, each relative: the reduced angle to fp32 2^-23 (its fixed-point error is below 2^-50 turns), its
+    multiplication by 2 pi 2^-23, sine and cosine of it 2^-22.5, mag and the product 2^-23: below 2^-20
+    together, then one to bf16."""
+    d, mag = 128, 1.375
+    w, _ = fa.rope_freqs(d, base=500000.0, scaling="linear", factor=8.0)
+    p = np.array([0, 1, -1, 2, 7, 100, -3000, 12345], dtype=np.int32)
+    q = rand(101, 1, 2, len(p), d)
+    first = q[..., 0::2] if interleaved else q[..., :d // 2]
+    second = q[..., 1::2] if interleaved else q[..., d // 2:]
+    (second if zero else first).zero_()
+    for back in (False, True):
+        turn = fa.rope_bwd if back else fa.rope
+        y, _ = turn(q, None, w, positions=torch.from_numpy(p).cuda(), interleaved=interleaved, mag=mag)
+        want, _ = ref.rotate(f64(q)[0], p, f64(w), mag, interleaved, -1.0 if back else 1.0)
+        err = np.abs(f64(y)[0] - want)
+        assert np.all(err <= (ref.U + 2.0 ** -20) * np.abs(want)), float((err / np.maximum(np.abs(want), 1e-30)).max())
+
+
+def test_rope_angle_of_far_positions(fa):
+    """The angle is off by at most |p| (2^-65 + |w| 2^-72) turns, beside fp32's roundings: offsets of 64 bits."""
+    N, d = 6, 64
+    w = torch.tensor([1.0, 0.37, 5e-3, 1e-6, 800.0, 0.0, -2.5, 3e-9], dtype=torch.float64).cuda()
+    q = rand(103, 1, 1, N, d)
+    for offset in (0, 2 ** 31, 10 ** 12, -10 ** 12, 2 ** 48, -2 ** 48):
+        y, _ = fa.rope(q, None, w, offset=offset)
+        want, size = ref.rotate(f64(q)[0], offset + np.arange(N), f64(w), 1.0, False)
+        turns = (abs(offset) + N) * (2.0 ** -65 + np.abs(f64(w)) * 2.0 ** -72)
+        slack = np.zeros(d)
+        slack[:8] = slack[8:16] = 2 * math.pi * turns
+        assert np.all(np.abs(f64(y)[0] - want) <= ref.U * np.abs(want) + (2.0 ** -20 + slack) * size), offset
