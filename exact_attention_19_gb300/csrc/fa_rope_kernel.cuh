@@ -22,7 +22,7 @@
 // token and chunk, not per head.
 // 4 x 8192 tokens, 32 + 8 heads of 128 (671 MB): 102.4 us, 6.6 TB/s, 97% of the
 // copy rate; 3 x 4099 tokens, 16 + 16 heads (201 MB), 33.3 us, 89% (one and a
-// half waves of CTAs); a call of 256 tokens 2.8 us, its launch.  Appending 4 x up
+// half waves of CTAs); a call of 256 tokens 2.9 us, its launch.  Appending 4 x up
 // to 2048 tokens, 32 + 2 x 8 heads (115 MB): 22.0 us, 77% (the page's index comes
 // before the first store).
 #pragma once
@@ -69,7 +69,7 @@ __device__ __forceinline__ unsigned long long turns_per_position(double w) {
   const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(w));
   const int expo = static_cast<int>((bits >> 52) & 0x7ffu);
   const unsigned long long frac = bits & 0xfffffffffffffull;
-  if (expo == 0 || expo == 0x7ff) return 0ull;  // zero, subnormal (below 2^-64 turns) or not finite
+  if (expo == 0 || expo == 0x7ff) return 0ull;  // zero, subnormal (below 2^-64 turns); not finite: see finite()
   const unsigned long long m = frac | (1ull << 52);
   // |w| = m 2^(expo - 1075); turns 2^64 = (m * kInv2Pi66) >> (1077 - expo)
   const unsigned long long lo = m * kInv2Pi66, hi = __umul64hi(m, kInv2Pi66);
@@ -83,6 +83,9 @@ __device__ __forceinline__ unsigned long long turns_per_position(double w) {
   else f = s > -64 ? lo << (-s) : 0ull;
   return (bits >> 63) ? 0ull - f : f;
 }
+
+// integer tests: fp64 comparisons run at a small fraction of the rate here
+__device__ __forceinline__ bool finite(double w) { return (__double2hiint(w) & 0x7ff00000) != 0x7ff00000; }
 
 // Cosine and sine of a 64-bit fraction of a turn, each with fp32's relative
 // accuracy: a slow pair's sine at a small position is all that one element of the
@@ -157,8 +160,13 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
   __shared__ unsigned long long freq[D / 2];
   static_assert(D / 2 <= kRopeThreads, "a thread converts one frequency");
   const bool angles = h_lo < p.heads[0] + p.heads[1];
-  if (angles && threadIdx.x < p.rot / 2) freq[threadIdx.x] = turns_per_position(__ldg(p.inv_freq + threadIdx.x));
-  __syncthreads();
+  bool broken = false;
+  if (angles && threadIdx.x < p.rot / 2) {
+    const double w = __ldg(p.inv_freq + threadIdx.x);
+    freq[threadIdx.x] = turns_per_position(w);
+    broken = !finite(w);
+  }
+  broken = __syncthreads_or(broken) != 0;  // some frequency is NaN or infinite: its pairs become NaN
   const long long tok = static_cast<long long>(blockIdx.x) * (kRopeThreads / kUnits) + threadIdx.x / kUnits;
   const int u = threadIdx.x % kUnits;
   if (tok >= p.tokens) return;
@@ -191,6 +199,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
     for (int i = 0; i < 8; ++i) {
       float sn, cs;
       cos_sin_turns(pos * freq[8 * u + i], cs, sn);
+      if (broken && !finite(__ldg(p.inv_freq + 8 * u + i))) cs = sn = __int_as_float(0x7fffffff);
       c[i] = cs * p.mag;
       s[i] = sn * (p.mag * p.sin_sign);
     }

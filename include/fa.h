@@ -208,7 +208,8 @@ size_t fa_bwd_workspace_bytes(int B, int H, int Nq);
  *             |p| (2^-65 + |inv_freq| 2^-72) turns, then fp32's relative error
  *             (sine and cosine too, near their zeros as elsewhere).  Any 32-bit
  *             position is far below a bf16 rounding, and so are offsets up to
- *             2^48 in size; past that the angle fades out.
+ *             2^48 in size; past that the angle fades out.  A value of NaN or
+ *             infinity makes its pair NaN.
  * positions   int32 [B, N] (position_stride, >= N, int32s from one sequence to the
  *             next) or one row for all (position_stride 0); NULL: position
  *             = offset + row.  offset is added in both cases.

@@ -52,3 +52,25 @@ def test_rope_angle_of_far_positions(fa):
         slack = np.zeros(d)
         slack[:8] = slack[8:16] = 2 * math.pi * turns
         assert np.all(np.abs(f64(y)[0] - want) <= ref.U * np.abs(want) + (2.0 ** -20 + slack) * size), offset
+
+
+def test_frequencies_that_are_not_finite(fa):
+    """A frequency of NaN or infinity makes its pairs NaN, in the rotation and in the cache; others stay."""
+    d, page, T = 64, 16, 3
+    w, _ = fa.rope_freqs(d)
+    bad = w.clone()
+    bad[3], bad[17], bad[30] = math.nan, math.inf, -math.inf
+    q, k = rand(105, 1, 2, T, d), rand(106, 1, 1, T, d)
+    hit = torch.zeros(d, dtype=torch.bool, device="cuda")
+    for i in (3, 17, 30):
+        hit[i] = hit[i + d // 2] = True
+    good, _ = fa.rope(q, None, w)
+    for turn, want in ((fa.rope, good), (fa.rope_bwd, fa.rope_bwd(q, None, w)[0])):
+        y, _ = turn(q, None, bad)
+        assert bool(torch.isnan(y[..., hit]).all()) and torch.equal(y[..., ~hit], want[..., ~hit])
+    c = Cache(107, 1, 1, d, page, T)
+    tq = fa.kv_append(q, k, k, c.k, c.v, c.device_table(), i32([T]), bad)
+    at = int(c.table[0, 0])
+    assert bool(torch.isnan(tq[..., hit]).all()) and torch.equal(tq[..., ~hit], good[..., ~hit])
+    assert bool(torch.isnan(c.k[at, :, :T][..., hit]).all()) and bool(torch.isfinite(c.k[at, :, :T][..., ~hit]).all())
+    assert torch.equal(c.v[at, :, :T], k[0])
