@@ -1042,12 +1042,13 @@ __global__ void __launch_bounds__(128) fa_paged_merge_rows_kernel(const PagedPar
     for (int e = 0; e < kPer; ++e) acc[r][e] = 0.f;
   for (int base = 0; base < most; base += 8) {
     const int i = base + (lane & 7);
-    const float* po = p.whole_o[0];  // never read through for a missing part
+    const float* po = nullptr;  // no part, or one without a key that the row sees
     float L = NEG_INF;
     if (i < n_mine) {
       const float* pl;
       parts.at(p, D, i, po, pl);
       L = *pl;
+      if (L == NEG_INF) po = nullptr;
     }
     float top = fmaxf(mx, L);
 #pragma unroll
@@ -1075,7 +1076,7 @@ __global__ void __launch_bounds__(128) fa_paged_merge_rows_kernel(const PagedPar
         const float c = __shfl_sync(0xffffffffu, wt, r * 8 + k);
         const float* const src = reinterpret_cast<const float*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), r * 8 + k));
-        if (c > 0.f) {
+        if (src != nullptr) {  // a weight of zero multiplies all the same: 0 * NaN is NaN
           float v[kPer];
           merge_load<D>(src, lane, v);
 #pragma unroll

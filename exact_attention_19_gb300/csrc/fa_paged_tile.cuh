@@ -567,6 +567,9 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
       float inv = l != 0.f ? 1.0f / l_o : 0.f;
       float lb = l != 0.f ? m_bar + __log2f(l) : NEG_INF;
       float inv_other = 0.f;  // factor of the other warpgroup's O
+      // which O holds keys of this row: the other is nothing but stale bits.  A factor that is zero because its keys
+      // weigh nothing beside the other's still multiplies (0 * NaN is NaN).
+      bool some = lb != NEG_INF, some_other = false;
       if (n > 0) {
         ok = uniform(mbar_wait(bar(kTBarFinal + (PAIR ? t : 0)), seg & 1, abort_flag));
         if (!ok) break;
@@ -581,9 +584,10 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
           const float2 st = stats[(t ^ 1) * 128 + r];
           const float top = fmaxf(lb, st.x);
           const float wm = lb == NEG_INF ? 0.f : ex2(lb - top), wo = st.x == NEG_INF ? 0.f : ex2(st.x - top);
-          const float sum = wm + wo;
-          inv = wm != 0.f ? wm * inv / sum : 0.f;
-          inv_other = wo != 0.f ? wo * st.y / sum : 0.f;
+          const float sum = wm + wo;  // 0: neither has keys of this row
+          some_other = st.x != NEG_INF;
+          inv = wm * inv / sum;
+          inv_other = wo * st.y / sum;
           lb = sum != 0.f ? top + __log2f(sum) : NEG_INF;
         }
         ++seg;
@@ -606,14 +610,13 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
             uint32_t o[32];
             tmem_ld32(tO + col0 + cc * 32, o);
             tmem_ld_wait(o);
-            // a factor of zero drops what may be nothing but stale bits
 #pragma unroll
-            for (int e = 0; e < 32; ++e) f[e] = inv != 0.f ? __uint_as_float(o[e]) * inv : 0.f;
+            for (int e = 0; e < 32; ++e) f[e] = some ? __uint_as_float(o[e]) * inv : 0.f;
             if constexpr (!PAIR) {
               tmem_ld32(lane_base + C::kTmO + (t ^ 1) * D + col0 + cc * 32, o);
               tmem_ld_wait(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) f[e] += inv_other != 0.f ? __uint_as_float(o[e]) * inv_other : 0.f;
+              for (int e = 0; e < 32; ++e) f[e] += some_other ? __uint_as_float(o[e]) * inv_other : 0.f;
             }
           } else {
 #pragma unroll

@@ -74,3 +74,51 @@ def test_frequencies_that_are_not_finite(fa):
     assert bool(torch.isnan(tq[..., hit]).all()) and torch.equal(tq[..., ~hit], good[..., ~hit])
     assert bool(torch.isnan(c.k[at, :, :T][..., hit]).all()) and bool(torch.isfinite(c.k[at, :, :T][..., ~hit]).all())
     assert torch.equal(c.v[at, :, :T], k[0])
+
+
+@pytest.mark.parametrize("B,H,Hk,T,n,at,prefix_len", [
+    (1, 2, 1, 1, 3000, 5, 0),        # row blocks of 16, parts joined by several warps to a row
+    (1, 32, 1, 1, 384, 200, 0),      # one CTA's query tile: key tiles of the other warpgroup
+    (1, 32, 1, 1, 384, 300, 0),
+    (2, 40, 1, 1, 6000, 700, 0),     # a query tile in the shares of many CTAs
+    (2, 16, 4, 32, 1500, 40, 0),     # 1024 rows, several warps to a row
+    (4, 32, 2, 80, 900, 3, 0),       # 10240 rows, four to a warp
+    (2, 64, 4, 96, 1300, 700, 0),    # a pair of query tiles
+    (40, 8, 2, 2, 30, 1500, 4000),   # the shared prefix's part
+    (40, 8, 2, 2, 30, 4000, 4000),   # the own keys' part
+])
+def test_nan_in_a_value_of_vanishing_weight(fa, B, H, Hk, T, n, at, prefix_len):
+    """Keys whose weight is zero in fp32 (a score 300 below the others'), one of their values NaN: 0 * NaN is NaN,
+    whichever part of the row holds it, and whoever joins the parts."""
+    d, page = 64, 16
+    c = Cache(109, B, Hk, d, page, n, prefix_len=prefix_len)
+    for b in range(B):
+        c.fill(c.table[b], n, b)
+    c.fill(c.prefix_pages, prefix_len, 99)
+    low = (at // 128) * 128  # its key tile scores low, all others high
+    for b in range(B):
+        for pages, first, length in ((c.prefix_pages, 0, prefix_len), (c.table[b], prefix_len, n)):
+            j = np.arange(length)
+            slots = torch.from_numpy(np.asarray(pages)[j // page]).cuda().long()
+            tile = (low if at < prefix_len or not prefix_len else prefix_len)
+            high = (first + j < tile) | (first + j >= (tile + 128 if at < prefix_len or not prefix_len else 1 << 30))
+            x = torch.from_numpy(np.where(high, 20.0, -20.0)).to(torch.bfloat16).cuda()
+            c.k[slots, :, torch.from_numpy(j % page).cuda()] = x[:, None, None].expand(-1, Hk, d)
+    q = torch.ones(B, H, T, d, dtype=torch.bfloat16, device="cuda")
+    good, good_l = run_paged(fa, c, q, [n] * B, None, prefix_len=prefix_len)
+    assert bool(torch.isfinite(good).all())
+    own = at - prefix_len if prefix_len and at >= prefix_len else at
+    hits = range(B) if prefix_len and at < prefix_len else [0]
+    pages = c.prefix_pages if prefix_len and at < prefix_len else c.table[0]
+    c.v[int(pages[own // page]), :, own % page, 5] = math.nan
+    o, lse = run_paged(fa, c, q, [n] * B, None, prefix_len=prefix_len)
+    assert torch.equal(lse, good_l)
+    sees = torch.ones(T, dtype=torch.bool, device="cuda")
+    if not (prefix_len and at < prefix_len):  # tokens before it do not see it
+        sees = torch.arange(T, device="cuda") + n - T >= own
+    for b in range(B):
+        if b in hits:
+            assert bool(torch.isnan(o[b][:, sees, 5]).all())
+            assert torch.equal(o[b][..., :5], good[b][..., :5]) and torch.equal(o[b][..., 6:], good[b][..., 6:])
+        else:
+            assert torch.equal(o[b], good[b])
