@@ -62,18 +62,30 @@ struct PagedParams {
   unsigned int* status;
 };
 
+// An index or length that an earlier kernel of the stream may have written: a coherent load that stays behind the
+// wait for that kernel (paged_begin).  ld.global.nc wants memory that nothing writes while the kernel is resident,
+// and as plain loads the compiler left 16 x 4 tokens over 31999 keys 2 us slower than either.
+__device__ __forceinline__ int coherent(const int* at) {
+  int v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(at));
+  return v;
+}
+
 // The own keys [lo, hi) of a sequence that any of its new tokens sees.
 struct SeqKeys {
   int len, fresh, lo, hi;
 };
-__device__ __forceinline__ SeqKeys seq_keys(const PagedParams& p, int b) {
+__device__ __forceinline__ SeqKeys seq_keys(const PagedParams& p, int len, int fresh) {
   SeqKeys s;
-  s.len = max(0, min(__ldg(p.lens + b), p.capacity));
-  s.fresh = p.new_lens ? max(0, min(__ldg(p.new_lens + b), p.T)) : p.T;
+  s.len = max(0, min(len, p.capacity));
+  s.fresh = max(0, min(fresh, p.T));
   s.hi = s.fresh > 0 ? s.len : 0;
   s.lo = p.left < 0 ? 0 : static_cast<int>(max(0ll, static_cast<long long>(s.len) - s.fresh - p.left));
   s.lo = min(s.lo, s.hi);
   return s;
+}
+__device__ __forceinline__ SeqKeys seq_keys(const PagedParams& p, int b) {
+  return seq_keys(p, coherent(p.lens + b), p.new_lens ? coherent(p.new_lens + b) : p.T);
 }
 __device__ __forceinline__ int tiles_of(int lo, int hi, int tile) { return hi > lo ? (hi + tile - 1) / tile - lo / tile : 0; }
 
@@ -122,6 +134,8 @@ __host__ __device__ __forceinline__ int row_blocks(long long rows, int rb) { ret
 // prefix kernel is done, or that kernel would not have let this one start); it
 // waits before it ends, so that the merge, which waits for it, sees both.
 // `beside`: this is such a kernel.
+// Everything that an earlier kernel of the stream may write (queries, lengths, page indices, parts) is read by
+// coherent loads behind the wait.  (The merge's lengths: RowParts::wait.)
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void paged_begin(bool beside) {
@@ -243,9 +257,8 @@ struct PagedSchedule {
     lo = 0;
     hi = 0x7fffffff;
     if (at < 0) return at;
-    const SeqKeys s = seq_keys(p, b);
-    if constexpr (PREFIX) hi = row_prefix_keys(p, s, rr % p.T);
-    else row_own_keys(p, s, rr % p.T, lo, hi);
+    if constexpr (PREFIX) hi = row_prefix_keys(p, seq_keys(p, b), rr % p.T);
+    else row_own_keys(p, seq_keys(p, b), rr % p.T, lo, hi);
     return at;
   }
   // where a row block's result goes: 0 the output, 1 whole_*, 2 piece_* (row = of the piece); first: the
@@ -364,7 +377,7 @@ __device__ __forceinline__ bool paged_share(const PagedParams& p, const int bloc
         if (b < p.B) {
           const SeqKeys s = seq_keys(p, b);
           mine = per * S::units(tiles_of(s.lo, s.hi, TILE));
-          if (pass == 0 && block == 0 && __ldg(p.lens + b) > p.capacity) atomicOr(p.status, kPagedPage);
+          if (pass == 0 && block == 0 && coherent(p.lens + b) > p.capacity) atomicOr(p.status, kPagedPage);
         }
         long long incl = mine;
 #pragma unroll
@@ -483,8 +496,8 @@ __device__ __forceinline__ void paged_rows(const CUtensorMap& tmK, const CUtenso
         const int* const pages = S::pages(p, f);
         n_page = n_page2 = -1;
         if (lane < n_n) {
-          if (k + chunk > f.lo) n_page = __ldg(pages + (k >> p.page_shift));
-          if (chunk < C::kKeys && k + chunk < f.hi) n_page2 = __ldg(pages + (k >> p.page_shift) + 1);
+          if (k + chunk > f.lo) n_page = coherent(pages + (k >> p.page_shift));
+          if (chunk < C::kKeys && k + chunk < f.hi) n_page2 = coherent(pages + (k >> p.page_shift) + 1);
         }
         return;
       }
@@ -568,8 +581,8 @@ __device__ __forceinline__ void paged_rows(const CUtensorMap& tmK, const CUtenso
       const uint32_t* const src = reinterpret_cast<const uint32_t*>(p.q + (there ? out_row[i] : 0) * D);
 #pragma unroll
       for (int kk = 0; kk < kKT; ++kk) {
-        qf[kk][i] = there ? __ldg(src + kk * 8 + q4) : 0u;
-        qf[kk][2 + i] = there ? __ldg(src + kk * 8 + 4 + q4) : 0u;
+        qf[kk][i] = there ? src[kk * 8 + q4] : 0u;
+        qf[kk][2 + i] = there ? src[kk * 8 + 4 + q4] : 0u;
       }
     }
     float o[kNT][4];
@@ -853,7 +866,9 @@ struct RowParts {
     }
   }
   // Whole warp: locate() done, the rest, and the wait for the parts.  In a small batch everything that does
-  // not need them comes before the wait and runs beside the kernel that writes them.
+  // not need them comes before the wait and runs beside the kernel that writes them.  That is the lengths alone,
+  // complete before that kernel's CTAs let this one start (each waited first); read from L2, as no wait of this
+  // kernel stands between an earlier kernel's lines in this SM's L1 and the load.
   __device__ __forceinline__ void wait(const PagedParams& p) {
     if (p.B <= kMergeScan) {
       const long long per = static_cast<long long>(p.Hk) * row_blocks(p.rows, p.rb[0]);
@@ -863,7 +878,8 @@ struct RowParts {
       for (int b0 = 0; b0 < p.B; b0 += 32) {
         unsigned u = 0;  // units of a row block of sequence b0 + lane
         if (b0 + lane < p.B) {
-          const SeqKeys s = seq_keys(p, b0 + lane);
+          const SeqKeys s =
+              seq_keys(p, __ldcg(p.lens + b0 + lane), p.new_lens ? __ldcg(p.new_lens + b0 + lane) : p.T);
           const int n = tiles_of(s.lo, s.hi, kPagedTile);
           u = n > 0 ? n + extra_units(p.rb[0]) : 0;
         }

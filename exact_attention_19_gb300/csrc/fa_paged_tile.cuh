@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
         auto wanted = [&](int k) -> bool { return mine && k < w.hi && k + chunk_rows > w.lo; };
         auto page_of = [&](int j) -> int {
           const int k = key_of(j);
-          return (j < jhi && wanted(k)) ? __ldg(pages + (k >> p.page_shift)) : -1;
+          return (j < jhi && wanted(k)) ? coherent(pages + (k >> p.page_shift)) : -1;
         };
         auto put = [&](const CUtensorMap* map, int j, int page) -> bool {
           const int s = item % C::kRing;

@@ -122,3 +122,42 @@ def test_nan_in_a_value_of_vanishing_weight(fa, B, H, Hk, T, n, at, prefix_len):
             assert torch.equal(o[b][..., :5], good[b][..., :5]) and torch.equal(o[b][..., 6:], good[b][..., 6:])
         else:
             assert torch.equal(o[b], good[b])
+
+
+@pytest.mark.parametrize("B,H,Hk,T,n,prefix_len", [
+    (4, 8, 2, 1, 700, 0), (2, 8, 2, 20, 400, 0), (2, 16, 1, 40, 500, 0), (6, 8, 2, 1, 90, 1500), (40, 8, 1, 1, 40, 900),
+])
+def test_an_output_is_the_next_calls_query(fa, B, H, Hk, T, n, prefix_len):
+    """Calls one after another without a pause, each reading what the one before wrote into two buffers in turn,
+    and lengths that a kernel between them changes: what they give with a wait between them."""
+    d, page, rounds = 64, 16, 24
+    c = Cache(111, B, Hk, d, page, n, prefix_len=prefix_len)
+    for b in range(B):
+        c.fill(c.table[b], n, b)
+    c.fill(c.prefix_pages, prefix_len, 99)
+    table, pages = c.device_table(), torch.from_numpy(c.prefix_pages).cuda()
+    ws = torch.empty(fa.fa_paged_workspace_bytes(B, H, Hk, T, d, prefix_len), dtype=torch.uint8, device="cuda")
+    q0 = rand(112, B, H, T, d)
+
+    def chain(wait):
+        bufs, lses = [q0.clone(), torch.zeros_like(q0)], []
+        lens, new = i32([n - rounds - 9 * b % 20 for b in range(B)]), i32([T] * B)
+        for i in range(rounds):
+            lens.add_(1)
+            a, out = bufs[i % 2], bufs[1 - i % 2]
+            lse = torch.empty(B, H, T, device="cuda")
+            args = dict(new_lens=new, out=out, lse=lse, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+            if prefix_len:
+                fa.fwd_prefix(a, c.k, c.v, pages, prefix_len, table, lens, **args)
+            else:
+                fa.fwd_paged(a, c.k, c.v, table, lens, **args)
+            if wait:
+                torch.cuda.synchronize()
+            lses.append(lse)
+        return bufs + lses
+
+    want = chain(True)
+    for _ in range(6):
+        assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
