@@ -84,6 +84,18 @@ def rope_freqs(rot: int, base: float = 10000.0, scaling: str | None = None, fact
     return w.to(device), mag
 
 
+def _c_int(name, value, bits):
+    """``value`` for a C integer of ``bits`` bits, which ctypes would cut to them without a word."""
+    if not -(1 << (bits - 1)) <= value < 1 << (bits - 1):
+        raise ValueError(f"{name} = {value} does not fit {bits} bits")
+    return value
+
+
+def _reach(name, value):
+    """One side of a window: past 2^31 - 1 it is open whatever its size, as no cache holds so many keys."""
+    return _c_int(name, min(value, (1 << 31) - 1), 32)
+
+
 def _need(name, t, dtype, dim):
     if not (isinstance(t, _Tensor) and t.dtype is dtype and t.is_cuda):
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
@@ -134,6 +146,7 @@ def _rope(backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, 
         done = _native_rope(backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out)
         if done is not None:
             return done
+    offset = _c_int("offset", offset, 64)
     _need("q", q, _BF16, 4)
     q_shape = q.shape
     B, H, N, d = q_shape
@@ -239,6 +252,7 @@ def kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq=None, n
                               interleaved, mag, q_out)
         if done is not None:
             return done
+    offset = _c_int("offset", offset, 64)
     _need("k", k, _BF16, 4)
     _need("v", v, _BF16, 4)
     k_shape = k.shape
@@ -328,10 +342,11 @@ def fwd_paged(q, k_cache, v_cache, block_table, seq_lens, scale: float | None = 
                              out, lse, workspace)
         if done is not None:
             return done
+    left, right = _reach("window[0]", window[0]), _reach("window[1]", window[1])
     out, lse, workspace, ws_bytes, new, rest = _paged_args(
         q, k_cache, v_cache, block_table, seq_lens, new_lens, scale, out, lse, workspace, stream, 0)
     st = load().fa_fwd_paged(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                             block_table.data_ptr(), seq_lens.data_ptr(), new, *rest, window[0], window[1],
+                             block_table.data_ptr(), seq_lens.data_ptr(), new, *rest, left, right,
                              workspace.data_ptr(), ws_bytes, _handle(stream, q))
     if st != 0:
         raise FaError(st, "fa_fwd_paged")
@@ -353,7 +368,7 @@ def fwd_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_table, 
         if done is not None:
             return done
     _need("prefix_pages", prefix_pages, _I32, 1)
-    if prefix_len <= 0:
+    if _c_int("prefix_len", prefix_len, 32) <= 0:
         raise ValueError("prefix_len must be > 0 (without a prefix: fwd_paged)")
     out, lse, workspace, ws_bytes, new, rest = _paged_args(
         q, k_cache, v_cache, block_table, seq_lens, new_lens, scale, out, lse, workspace, stream, prefix_len)

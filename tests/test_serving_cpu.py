@@ -168,3 +168,28 @@ def test_reference_pins():
     p = np.exp(q[0] @ k.T * 0.5)
     assert np.allclose(o[0], p @ v / p.sum()) and np.isclose(lse[0], np.log(p.sum()))
     assert np.allclose(o[1], v[2]) and np.all(o[2] == 0) and np.isneginf(lse[2])
+
+
+def test_python_entry_points_refuse_integers_past_the_c_types():
+    """An offset, length or window reach that ctypes would cut to its low bits; a reach past 2^31 - 1 is an open side."""
+    x = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+    w = torch.zeros(32, dtype=torch.float64)
+    t = torch.zeros(1, 1, dtype=torch.int32)
+    n = torch.zeros(1, dtype=torch.int32)
+    for bad in (2 ** 63, -2 ** 63 - 1, 2 ** 64):
+        for f in (lambda: fa.rope(x, x, w, offset=bad), lambda: fa.rope_bwd(x, None, w, offset=bad),
+                  lambda: fa.kv_append(x, x, x, x, x, t, n, w, offset=bad)):
+            with pytest.raises(ValueError):
+                f()
+    for bad in ((-2 ** 31 - 1, 0), (0, -2 ** 32)):
+        with pytest.raises(ValueError):
+            fa.fwd_paged(x, x, x, t, n, window=bad)
+    for wide in ((2 ** 31, 0), (2 ** 64, 2 ** 40)):  # no refusal of these: the host tensors are what stops the call
+        with pytest.raises(TypeError):
+            fa.fwd_paged(x, x, x, t, n, window=wide)
+    from exact_attention_19_gb300 import serving
+
+    assert [serving._reach("", v) for v in (-1, 0, 7, 2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5)] == [-1, 0, 7] + [2 ** 31 - 1] * 3
+    for bad in (2 ** 31, 2 ** 32 + 8):
+        with pytest.raises(ValueError):
+            serving._c_int("prefix_len", bad, 32)

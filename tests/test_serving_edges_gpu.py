@@ -161,3 +161,29 @@ def test_an_output_is_the_next_calls_query(fa, B, H, Hk, T, n, prefix_len):
     want = chain(True)
     for _ in range(6):
         assert all(torch.equal(a, b) for a, b in zip(chain(False), want))
+
+
+def test_windows_and_offsets_past_the_c_types(fa):
+    """A window reach past 32 bits is an open one, not its low 32 bits; an offset past 64 bits is refused."""
+    B, H, Hk, T, d, n = 2, 4, 2, 2, 64, 100
+    c = Cache(141, B, Hk, d, 16, n)
+    for b in range(B):
+        c.fill(c.table[b], n, b)
+    q, lens, table = rand(142, B, H, T, d), i32([n, 60]), c.device_table()
+    want = fa.fwd_paged(q, c.k, c.v, table, lens)
+    side = torch.cuda.current_stream()
+    for left in (2 ** 31, 2 ** 32, 2 ** 32 + 3, 2 ** 63, 2 ** 64 + 1):
+        for stream in (None, side):
+            got = fa.fwd_paged(q, c.k, c.v, table, lens, window=(left, 0), stream=stream)
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), left
+    every = fa.fwd_paged(q, c.k, c.v, table, lens, window=(-1, -1))
+    got = fa.fwd_paged(q, c.k, c.v, table, lens, window=(2 ** 33, 2 ** 32 + 1))
+    assert all(torch.equal(a, b) for a, b in zip(got, every))
+    w, _ = fa.rope_freqs(d)
+    for bad in (2 ** 63, -2 ** 63 - 1, 2 ** 64 + 5):
+        with pytest.raises(ValueError):
+            fa.rope(q, None, w, offset=bad)
+        with pytest.raises(ValueError):
+            fa.kv_append(q, q[:, :Hk], q[:, :Hk], c.k, c.v, table, lens, w, offset=bad)
+    with pytest.raises(ValueError):
+        fa.fwd_paged(q, c.k, c.v, table, lens, window=(-2 ** 32, 0))
