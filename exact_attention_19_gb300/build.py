@@ -73,28 +73,50 @@ def needs_build() -> bool:
     return _stale(LIB_PATH, DEPS) or _stale(TORCH_LIB_PATH, TORCH_DEPS)
 
 
-def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile what is out of date (both libraries at once); the path of libfa_gb300.so."""
-    jobs = []
-    for out, deps, make in ((LIB_PATH, DEPS, lambda o: command(o, verbose_ptxas)),
-                            (TORCH_LIB_PATH, TORCH_DEPS, torch_command)):
-        if force or _stale(out, deps):
-            os.makedirs(LIB_DIR, exist_ok=True)
-            tmp = out + f".tmp{os.getpid()}"
-            cmd = make(tmp)
-            jobs.append((out, tmp, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE,
-                                                         text=True)))
-    failed = []
-    for out, tmp, cmd, job in jobs:
-        stdout, stderr = job.communicate()
-        if job.returncode != 0:
-            failed.append(f"{cmd[0]} failed:\n{stdout}\n{stderr}")
-            continue
-        if verbose_ptxas:
-            sys.stderr.write(stderr)
-        os.replace(tmp, out)
-    if failed:
-        raise RuntimeError("\n".join(failed))
+def _start(out: str, cmd: list[str]):
+    return out, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.PIPE, text=True)
+
+
+def _finish(job, tmp: str, echo: bool) -> str:
+    """Wait for a compiler and put its output in place; what went wrong, or an empty text."""
+    out, cmd, proc = job
+    stdout, stderr = proc.communicate()
+    if proc.returncode != 0:
+        return f"{cmd[0]} failed:\n{stdout}\n{stderr}"
+    if echo:
+        sys.stderr.write(stderr)
+    os.replace(tmp, out)
+    return ""
+
+
+def build(force: bool = False, verbose_ptxas: bool = False, strict: bool = False) -> str:
+    """Compile what is out of date (both libraries at once); the path of libfa_gb300.so.
+
+    The C ABI needs no torch: where torch is missing, or fa_torch.so does not compile against it,
+    libfa_gb300.so is built all the same, with a note on stderr (the torch entry points raise at their
+    first use); ``strict`` raises instead, once libfa_gb300.so is in place.
+    """
+    os.makedirs(LIB_DIR, exist_ok=True)
+    suffix = f".tmp{os.getpid()}"
+    lib_job = torch_job = None
+    if force or _stale(LIB_PATH, DEPS):
+        lib_job = _start(LIB_PATH, command(LIB_PATH + suffix, verbose_ptxas))
+    torch_failure = ""
+    try:
+        if force or _stale(TORCH_LIB_PATH, TORCH_DEPS):
+            torch_job = _start(TORCH_LIB_PATH, torch_command(TORCH_LIB_PATH + suffix))
+    except Exception as e:  # no torch, a torch that does not load, no host compiler
+        torch_failure = f"{type(e).__name__}: {e}"
+    failure = _finish(lib_job, LIB_PATH + suffix, verbose_ptxas) if lib_job else ""
+    if torch_job:
+        torch_failure = _finish(torch_job, TORCH_LIB_PATH + suffix, verbose_ptxas)
+    if failure:
+        raise RuntimeError("\n".join(x for x in (failure, torch_failure) if x))
+    if torch_failure:
+        if strict:
+            raise RuntimeError(f"fa_torch.so was not built: {torch_failure}")
+        sys.stderr.write(f"fa_torch.so (the torch entry points rope, kv_append, fwd_paged, fwd_prefix) was not built: "
+                         f"{torch_failure}\n")
     return LIB_PATH
 
 

@@ -193,3 +193,56 @@ def test_python_entry_points_refuse_integers_past_the_c_types():
     for bad in (2 ** 31, 2 ** 32 + 8):
         with pytest.raises(ValueError):
             serving._c_int("prefix_len", bad, 32)
+
+
+@pytest.fixture
+def toy_build(tmp_path, monkeypatch):
+    """build() on compilers that write a word, into a folder of its own."""
+    source = tmp_path / "source"
+    source.write_text("x")
+
+    def toy(word):
+        return lambda out, *_: ["sh", "-c", f"echo {word} > {out}"]
+
+    monkeypatch.setattr(fa_build, "LIB_DIR", str(tmp_path))
+    monkeypatch.setattr(fa_build, "LIB_PATH", str(tmp_path / "lib.so"))
+    monkeypatch.setattr(fa_build, "TORCH_LIB_PATH", str(tmp_path / "torch.so"))
+    monkeypatch.setattr(fa_build, "DEPS", [str(source)])
+    monkeypatch.setattr(fa_build, "TORCH_DEPS", [str(source)])
+    monkeypatch.setattr(fa_build, "command", toy("lib"))
+    monkeypatch.setattr(fa_build, "torch_command", toy("torch"))
+    return tmp_path
+
+
+def test_build_puts_both_libraries_in_place(toy_build):
+    fa_build.build(strict=True)
+    assert sorted(f.name for f in toy_build.iterdir()) == ["lib.so", "source", "torch.so"]
+    assert not fa_build.needs_build()
+
+
+def test_build_of_the_c_library_needs_no_torch(toy_build, monkeypatch, capfd):
+    """Without torch, with a torch that does not load, without a host compiler and with one that fails:
+    libfa_gb300.so is built, a note or (strict) an error says what is missing."""
+    def missing(out):
+        raise ImportError("No module named 'torch'")
+
+    def broken(out):
+        raise OSError("libtorch.so: cannot open shared object file")
+
+    for torch_command, word in ((missing, "torch"), (broken, "libtorch"), (lambda out: ["/no/such/compiler"], "compiler"),
+                                (lambda out: ["sh", "-c", "echo no header >&2; exit 1"], "no header")):
+        monkeypatch.setattr(fa_build, "torch_command", torch_command)
+        fa_build.build(force=True)
+        assert word in capfd.readouterr().err
+        assert sorted(f.name for f in toy_build.iterdir()) == ["lib.so", "source"]
+        (toy_build / "lib.so").unlink()
+        with pytest.raises(RuntimeError, match=word):
+            fa_build.build(strict=True)
+        assert (toy_build / "lib.so").read_text() == "lib\n"
+
+
+def test_build_reports_a_failing_c_library(toy_build, monkeypatch):
+    monkeypatch.setattr(fa_build, "command", lambda out, *_: ["sh", "-c", "echo bad kernel >&2; exit 2"])
+    with pytest.raises(RuntimeError, match="bad kernel"):
+        fa_build.build()
+    assert not (toy_build / "lib.so").exists() and (toy_build / "torch.so").exists()
