@@ -5,8 +5,9 @@ forward, split-KV merge and backward kernel instantiation), fa_rope.cu (rotary
 positions and the paged cache's append), fa_paged.cu (attention over the paged
 cache), fa_probe.cu (the exp2-throughput probe) and fa_selftest.cu (the
 bounded-wait self-test), compiled in parallel by one nvcc call; beside them
-fa_torch.so, the host-side fast path of the torch entry points (fa_torch.cpp,
-the host compiler against torch's headers).
+fa_torch, the host-side fast path of the torch entry points (fa_torch.cpp, the
+host compiler against torch's headers; its file is named after the torch and
+Python it was compiled for).
 """
 from __future__ import annotations
 
@@ -27,7 +28,6 @@ DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_ptx.cuh", "fa_host.h", "fa
                                                        "fa_paged_kernel.cuh", "fa_paged_tile.cuh")] + [
     os.path.join(INCLUDE, "fa.h")]
 
-TORCH_LIB_PATH = os.path.join(LIB_DIR, "fa_torch.so")
 TORCH_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
 TORCH_DEPS = [TORCH_SOURCE, os.path.join(INCLUDE, "fa.h")]
 
@@ -49,7 +49,18 @@ def command(out: str = LIB_PATH, verbose_ptxas: bool = False) -> list[str]:
     return cmd
 
 
-def torch_command(out: str = TORCH_LIB_PATH) -> list[str]:
+def torch_lib_path() -> str:
+    """Where the torch module for the running interpreter and torch lies.  It is compiled against torch's
+    C++ classes, so each version of either has a file of its own and never loads another's."""
+    import sysconfig
+
+    import torch
+
+    return os.path.join(LIB_DIR, f"fa_torch.{torch.__version__}.cxx11abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+                                 f"{sysconfig.get_config_var('EXT_SUFFIX') or '.so'}")
+
+
+def torch_command(out: str) -> list[str]:
     import sysconfig
 
     import torch
@@ -70,7 +81,7 @@ def _stale(out: str, deps: list[str]) -> bool:
 
 
 def needs_build() -> bool:
-    return _stale(LIB_PATH, DEPS) or _stale(TORCH_LIB_PATH, TORCH_DEPS)
+    return _stale(LIB_PATH, DEPS) or _stale(torch_lib_path(), TORCH_DEPS)
 
 
 def _start(out: str, cmd: list[str]):
@@ -92,7 +103,7 @@ def _finish(job, tmp: str, echo: bool) -> str:
 def build(force: bool = False, verbose_ptxas: bool = False, strict: bool = False) -> str:
     """Compile what is out of date (both libraries at once); the path of libfa_gb300.so.
 
-    The C ABI needs no torch: where torch is missing, or fa_torch.so does not compile against it,
+    The C ABI needs no torch: where torch is missing, or fa_torch does not compile against it,
     libfa_gb300.so is built all the same, with a note on stderr (the torch entry points raise at their
     first use); ``strict`` raises instead, once libfa_gb300.so is in place.
     """
@@ -103,19 +114,20 @@ def build(force: bool = False, verbose_ptxas: bool = False, strict: bool = False
         lib_job = _start(LIB_PATH, command(LIB_PATH + suffix, verbose_ptxas))
     torch_failure = ""
     try:
-        if force or _stale(TORCH_LIB_PATH, TORCH_DEPS):
-            torch_job = _start(TORCH_LIB_PATH, torch_command(TORCH_LIB_PATH + suffix))
+        torch_path = torch_lib_path()
+        if force or _stale(torch_path, TORCH_DEPS):
+            torch_job = _start(torch_path, torch_command(torch_path + suffix))
     except Exception as e:  # no torch, a torch that does not load, no host compiler
         torch_failure = f"{type(e).__name__}: {e}"
     failure = _finish(lib_job, LIB_PATH + suffix, verbose_ptxas) if lib_job else ""
     if torch_job:
-        torch_failure = _finish(torch_job, TORCH_LIB_PATH + suffix, verbose_ptxas)
+        torch_failure = _finish(torch_job, torch_path + suffix, verbose_ptxas)
     if failure:
         raise RuntimeError("\n".join(x for x in (failure, torch_failure) if x))
     if torch_failure:
         if strict:
-            raise RuntimeError(f"fa_torch.so was not built: {torch_failure}")
-        sys.stderr.write(f"fa_torch.so (the torch entry points rope, kv_append, fwd_paged, fwd_prefix) was not built: "
+            raise RuntimeError(f"fa_torch was not built: {torch_failure}")
+        sys.stderr.write(f"fa_torch (the torch entry points rope, kv_append, fwd_paged, fwd_prefix) was not built: "
                          f"{torch_failure}\n")
     return LIB_PATH
 

@@ -21,6 +21,7 @@ import struct
 import torch
 
 from . import FaError, load
+from .build import torch_lib_path
 
 _BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
 _Tensor = torch.Tensor
@@ -30,7 +31,7 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 
 def _load_native():
     """The fa_torch module, bound to the loaded library's functions."""
-    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "fa_torch.so")
+    path = torch_lib_path()
     if not os.path.exists(path):
         raise ImportError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
     loader = importlib.machinery.ExtensionFileLoader("fa_torch", path)

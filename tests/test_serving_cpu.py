@@ -206,7 +206,7 @@ def toy_build(tmp_path, monkeypatch):
 
     monkeypatch.setattr(fa_build, "LIB_DIR", str(tmp_path))
     monkeypatch.setattr(fa_build, "LIB_PATH", str(tmp_path / "lib.so"))
-    monkeypatch.setattr(fa_build, "TORCH_LIB_PATH", str(tmp_path / "torch.so"))
+    monkeypatch.setattr(fa_build, "torch_lib_path", lambda: str(tmp_path / "torch.so"))
     monkeypatch.setattr(fa_build, "DEPS", [str(source)])
     monkeypatch.setattr(fa_build, "TORCH_DEPS", [str(source)])
     monkeypatch.setattr(fa_build, "command", toy("lib"))
@@ -246,3 +246,18 @@ def test_build_reports_a_failing_c_library(toy_build, monkeypatch):
     with pytest.raises(RuntimeError, match="bad kernel"):
         fa_build.build()
     assert not (toy_build / "lib.so").exists() and (toy_build / "torch.so").exists()
+
+
+def test_the_torch_module_belongs_to_one_torch(monkeypatch):
+    """Another torch, ABI or Python has another file, so a module compiled for an earlier one counts as missing."""
+    import sysconfig
+
+    fa_build.build()
+    here = fa_build.torch_lib_path()
+    assert not fa_build.needs_build() and torch.__version__ in here and sysconfig.get_config_var("SOABI") in here
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    assert fa_build.torch_lib_path() != here and fa_build.needs_build()
+    from exact_attention_19_gb300 import serving
+
+    with pytest.raises(ImportError, match="build it"):
+        serving._load_native()
