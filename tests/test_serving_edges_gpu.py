@@ -187,3 +187,128 @@ def test_windows_and_offsets_past_the_c_types(fa):
             fa.kv_append(q, q[:, :Hk], q[:, :Hk], c.k, c.v, table, lens, w, offset=bad)
     with pytest.raises(ValueError):
         fa.fwd_paged(q, c.k, c.v, table, lens, window=(-2 ** 32, 0))
+
+
+@pytest.mark.parametrize("B,H,Hk,T,d,page,lens,new,window", [
+    (3, 4, 2, 5, 64, 16, [300, 40, 77], [5, 1, 0], (20, 0)),
+    (3, 4, 4, 3, 128, 32, [129, 7, 64], [1, 3, 2], (0, 0)),
+    (3, 4, 2, 20, 64, 16, [500, 90, 31], [20, 3, 0], (64, 0)),        # blocks of 128 rows
+    (2, 8, 2, 30, 128, 64, [700, 260], [11, 30], (127, 5)),
+    (3, 4, 1, 100, 64, 32, [900, 300, 130], [100, 1, 57], (30, 0)),   # blocks of 256 rows
+    (3, 4, 1, 300, 128, 64, [300, 640, 1000], [300, 7, 299], (100, 0)),
+    (3, 2, 1, 200, 64, 16, [400, 200, 333], [200, 64, 1], (0, 130)),
+    (2, 4, 2, 40, 64, 16, [200, 64], [13, 40], (-1, 3)),
+    (2, 4, 2, 40, 64, 16, [200, 20], [13, 40], (16, -1)),
+])
+def test_new_lens_under_a_window(fa, B, H, Hk, T, d, page, lens, new, window):
+    paged_case(fa, 121, B, H, Hk, T, d, page, lens, new, window)
+
+
+@pytest.mark.parametrize("T", [1, 30, 200])
+def test_negative_lengths_are_empty_entries(fa, T):
+    """seq_lens and new_lens below zero, as padded entries of a batch may hold."""
+    paged_case(fa, 123, 4, 4, 2, T, 64, 16, [-3, 240, 0, -2 ** 31], None, (-1, 0))
+    paged_case(fa, 124, 4, 4, 2, T, 64, 16, [-3, 240, 70, 230], [1, -5, -2 ** 31, T], (-1, -1))
+    paged_case(fa, 125, 4, 4, 2, T, 64, 16, [-3, 240, 70, 230], [T, 1, -1, T], prefix_len=150)
+
+
+@pytest.mark.parametrize("H,T,n", [(1, 1, 40), (2, 1, 3000), (32, 1, 300), (32, 1, 5000), (32, 20, 700)])
+@pytest.mark.parametrize("low", [-math.inf, torch.finfo(torch.bfloat16).min / 64])
+def test_keys_of_minus_infinity_weigh_nothing(fa, H, T, n, low):
+    """Scores of -inf beside finite ones, and scores near the lowest finite value, in every kernel."""
+    d, page = 64, 16
+    c = Cache(127, 1, 1, d, page, n)
+    c.fill(c.table[0], n, 5)
+    q = rand(128, 1, H, T, d).abs().clamp(min=0.01)
+    for j in (0, 17, n // 2):  # every row sees them
+        c.k[int(c.table[0, j // page]), :, j % page] = low
+    o, lse = run_paged(fa, c, q, [n], None)
+    want = ref.paged(f64(q), f64(c.k), f64(c.v), c.table, [n], [T], -1, 0, 0.125)
+    ref.check_attention(f64(o), f64(lse), want)
+
+
+def prefix64(q, c, lens, prefix_len, T):
+    """fwd_prefix in 64 bits on the GPU: (O, LSE, sum_j p_j |v_j|)."""
+    B, H, _, d = q.shape
+    Hk, page = c.Hk, c.page
+    G = H // Hk
+
+    def keys(cache, pages, n, h):
+        j = torch.arange(n, device="cuda")
+        at = torch.from_numpy(np.asarray(pages).copy()).cuda().long()[j // page]
+        return cache[at, h, j % page].double()
+
+    o, size = (torch.zeros(B, H, T, d, dtype=torch.float64, device="cuda") for _ in range(2))
+    lse = torch.full((B, H, T), -math.inf, dtype=torch.float64, device="cuda")
+    for h in range(Hk):
+        shared = [keys(x, c.prefix_pages, prefix_len, h) for x in (c.k, c.v)]
+        for b in range(B):
+            n = lens[b]
+            k, v = (torch.cat([s, keys(x, c.table[b], n, h)]) for s, x in zip(shared, (c.k, c.v)))
+            s = q[b, h * G:(h + 1) * G].double() @ k.T / math.sqrt(d)
+            pos = prefix_len + n - T + torch.arange(T, device="cuda")
+            s = s.masked_fill(torch.arange(prefix_len + n, device="cuda") > pos[:, None], -math.inf)
+            p = s.softmax(-1)
+            o[b, h * G:(h + 1) * G], size[b, h * G:(h + 1) * G] = p @ v, p @ v.abs()
+            lse[b, h * G:(h + 1) * G] = s.logsumexp(-1)
+    return o.cpu().numpy(), lse.cpu().numpy(), size.cpu().numpy()
+
+
+@pytest.mark.parametrize("B,H,Hk,T,d,page,prefix_len,most,wide,captured", [
+    # rows of the whole batch in one block of 16: prefix and own keys in one launch
+    (4, 8, 8, 3, 64, 16, 8000, 700, 0, False),     # the prefix on more CTAs than there are SMs
+    (4, 8, 8, 3, 128, 32, 8001, 700, 0, True),
+    (3, 4, 2, 2, 128, 16, 5000, 400, 0, False),    # on about half of them
+    (5, 6, 2, 1, 128, 64, 900, 130, 100000, False),  # a table for contexts far longer than these
+    (2, 16, 16, 8, 128, 128, 32000, 2000, 0, False),
+    # a query tile of 128 rows
+    (12, 16, 8, 3, 64, 16, 20000, 500, 0, True),
+    (12, 16, 8, 3, 128, 64, 20001, 500, 0, False),
+    (24, 8, 4, 2, 128, 32, 3000, 300, 60000, True),
+    # pairs of query tiles
+    (40, 32, 8, 1, 128, 64, 20000, 300, 0, True),
+    (100, 16, 4, 1, 64, 16, 12001, 90, 0, False),
+    (30, 32, 8, 2, 128, 128, 2500, 200, 30000, False),
+    (6, 16, 2, 40, 128, 64, 9000, 400, 0, False),   # own keys on pairs of query tiles too
+])
+def test_long_prefixes(fa, B, H, Hk, T, d, page, prefix_len, most, wide, captured):
+    """Prefixes that fill most SMs, a few of them, or all twice over, with own keys beside and behind them."""
+    lens = [T + (most - T) * (7 * b % B) // max(1, B - 1) for b in range(B)]
+    c = Cache(131, B, Hk, d, page, max(lens), prefix_len=prefix_len)
+    for b in range(B):
+        c.fill(c.table[b], lens[b], b)
+    c.fill(c.prefix_pages, prefix_len, 99)
+    q = rand(132, B, H, T, d)
+    want = prefix64(q, c, lens, prefix_len, T)
+    if wide:
+        table = np.full((B, wide // page), -1, dtype=np.int32)
+        table[:, :c.max_pages] = c.table
+        c.table = table
+    o, lse = run_paged(fa, c, q, lens, None, prefix_len=prefix_len)
+    ref.check_attention(f64(o), f64(lse), want, f"{B}x{H}/{Hk} T={T} d={d} behind {prefix_len}")
+    if not captured:
+        return
+    pages, table, device_lens, q_in = torch.from_numpy(c.prefix_pages).cuda(), c.device_table(), i32(lens), q.clone()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = fa.fwd_prefix(q_in, c.k, c.v, pages, prefix_len, table, device_lens)
+    for _ in range(3):
+        graph.replay()
+        assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+    q_in.copy_(rand(133, B, H, T, d))
+    graph.replay()
+    again, again_l = fa.fwd_prefix(q_in, c.k, c.v, pages, prefix_len, table, device_lens)
+    assert torch.equal(got[0], again) and torch.equal(got[1], again_l)
+
+
+@pytest.mark.parametrize("H,T,prefix_len", [(2, 3, 0), (4, 40, 0), (4, 150, 0), (2, 3, 300), (8, 20, 300)])
+def test_padding_rows_may_hold_anything(fa, H, T, prefix_len):
+    """NaN queries in the rows past new_lens and in an empty entry of the batch: O = 0, LSE = -inf there, and nothing
+    of it reaches the rows beside them."""
+    c, q, o, lse = paged_case(fa, 135, 3, H, 2, T, 64, 16, [T, 2 * T, 0], [T, 1, T], prefix_len=prefix_len)
+    q = q.clone()
+    q[1, :, 1:] = math.nan
+    q[2] = math.inf
+    got, got_l = run_paged(fa, c, q, [T, 2 * T, 0], [T, 1, T], prefix_len=prefix_len)
+    assert torch.equal(got, o) and torch.equal(got_l, lse)
