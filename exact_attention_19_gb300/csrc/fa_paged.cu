@@ -77,10 +77,9 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 // query tile, 44.8 as half of a pair; 256 rows 47.8 on a pair, 52.6 on two tiles.
 int block_rows(long long rows) { return rows <= 16 ? 16 : (rows <= 128 ? 128 : 256); }
 constexpr int kTileKeys = fa::kPagedTile;
-int grid_of(int block_rows, int sms) { return block_rows == 16 ? 2 * sms : sms; }  // all CTAs resident
-
-// Tiles of 128 keys per CTA up to which own keys leave the prefix its SMs.
-constexpr long long kLongOwn = 16;
+// A wave of one kind's CTAs.  (With a prefix that takes most SMs, own keys run in a second wave; no CTA waits for
+// another but at its end, for a grid that has started whole.)
+int grid_of(int block_rows, int sms) { return block_rows == 16 ? 2 * sms : sms; }
 
 // The row blocks, tiles and CTAs of a call, and the parts of its workspace, in
 // order; every part begins on a 256-byte boundary.
@@ -119,12 +118,17 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
   return l;
 }
 
-// The merge: from kMergeRows rows, or kMergeFewRows with at most kMergeParts parts to a row, one warp joins
-// four rows; else two warps join one (from kMergeFewRows rows, so that one wave of CTAs holds them) or four.
-// Whole calls, us: 16384 rows 71 with a warp for four rows, 85 with four warps to each; 2048 rows of 3 parts 37.1
-// with a warp for four, 38.6 with four to one; 2048 rows of 11 parts 36.3 with two to one, 40.2 with four; 1152
-// rows of 12 parts 64.3 with four to one, 70.4 with a warp for four.
-constexpr long long kMergeRows = 8192, kMergeFewRows = 1536, kMergeParts = 4;
+// The merge: one warp joins four rows where rows are many for their parts (it takes the parts of its rows one
+// after another: from kMergeRows rows and kMergeRowsPerPart times the parts of a row), else two warps join one row
+// (from kMergeTwo rows: the four-warp form's CTAs come in waves then) or four do.  Whole calls, us, with a warp for
+// four rows / two to one / four to one:
+//   rows of parts: 16000 of 3: 45.7 / 65.2 / 83.8;  7680 of 6: 32.8 / 38.0 / 46.6;  6144 of 7 (d = 64): 24.6 / 26.1 /
+//   33.8;  5120 of 4: 25.6 / 28.2 / 33.4;  4096 of 5: 23.6 / 24.8 / 28.9;  2560 of 2: 20.4 / 21.5 / 23.2
+//   the other side: 5120 of 8: 33.5 / 32.4 / 37.8;  4096 of 10: 30.6 / 28.0 / 32.3;  2560 of 8: 22.3 / 21.0 / 22.9;
+//   2048 of 20: 31.1 / 22.7 / 27.6;  1920 of 2: 26.4 / 25.5 / 28.3;  1600 of 4: 25.4 / 22.4 / 26.2
+//   few rows: 1280 of 4: 19.9 / 17.1 / 18.2;  1024 of 5: 21.6 / 17.8 / 18.6;  1024 of 39: 26.3 / 21.4 / 21.2;  768 of 26:
+//   19.8 / 17.1 / 16.8;  512 of 3: 25.9 / 23.7 / 23.6;  160 of 31: 21.6 / 11.4 / 10.6;  16 of 77: 23.2 / 9.9 / 9.3
+constexpr long long kMergeRows = 2400, kMergeRowsPerPart = 700, kMergeTwo = 1024;
 
 // Programmatic dependent launch: the kernel may be scheduled while the one ahead
 // of it on the stream still runs, and waits on the device (paged_begin) for what
@@ -149,9 +153,9 @@ int launch_merge(const fa::PagedParams& p, long long rows, cudaStream_t stream) 
   // parts of a row where the shares cut every row block alike
   long long parts = p.own_grid / (1ll * p.B * p.Hk * fa::row_blocks(p.rows, p.rb[0])) + 1;
   if (p.prefix_len > 0) parts += p.prefix_ctas / (1ll * p.Hk * p.prefix_blocks) + 1;
-  if (rows >= kMergeRows || (rows >= kMergeFewRows && parts <= kMergeParts))
+  if (rows >= kMergeRows && rows >= kMergeRowsPerPart * parts)
     return launch_kernel(fa::fa_paged_merge_rows_kernel<D>, (rows + 15) / 16, 128, 0, stream, p);
-  if (rows >= kMergeFewRows)
+  if (rows >= kMergeTwo)
     return launch_kernel(fa::fa_paged_merge_row_kernel<D, 2>, (rows + 1) / 2, 128, 0, stream, p);
   return launch_kernel(fa::fa_paged_merge_row_kernel<D, 4>, rows, 128, 0, stream, p);
 }
@@ -280,15 +284,18 @@ int paged_impl(const void* q, const void* k_cache, const void* v_cache, void* o,
   }
   p.status = fa_host::status_word(dev);
   if (!p.status) return FA_ERR_LAUNCH;
-  // Beside a prefix kernel that leaves a quarter of the SMs or more free, the own keys are cut for the free ones
-  // alone (64 sequences behind 8192 tokens: 43 us against 55 with shares that wait for the other SMs), unless
-  // the table allows more work than kLongOwn units per CTA, for which every SM is wanted.
+  // Beside a prefix that leaves a quarter of the SMs or more free, the own keys are cut for the free ones alone: a
+  // share that has to wait for a prefix CTA's SM ends last, whatever the lengths.  us, cut for the free SMs / for
+  // all: 16 sequences behind 2000 tokens (prefix on 40 of 152 SMs), up to 100 own keys 19.0 / 20.2, 1000 23.0 / 26.6,
+  // 4000 34.9 / 45.4, 30000 159 / 167;  64 behind 500 (8), 4000 own 94.9 / 118;  100 behind 6000 (51), 60 own
+  // 31.0 / 33.1;  12 x 2 tokens behind 5800 (100), 300 own 18.5 / 22.0;  behind 6300 (108), 3000 own 37.2 / 36.4;  the
+  // worst: 40 x 2 behind 12000 (49), 200 own 29.7 / 28.3.  Past three quarters: behind 7200 (122), 300 own
+  // 19.7 / 22.9, 3000 own 46.1 / 37.7;  30 x 20 tokens behind 3000 (133), 900 own 62.2 / 48.3.
+  // (Prefix rows in one block of 16: two CTAs of that launch fit an SM, but own keys cut for all free places are
+  // slower, 9.3 for 8.1 with 4 sequences behind 1000 tokens, 12 heads of 64.)
   p.own_grid = l.grid[0];
-  if (prefix_len > 0 && l.prefix_ctas * 4 <= 3ll * sms) {
-    const long long tiles = (1ll * max_pages * page_size + kTileKeys - 1) / kTileKeys;
-    if (1ll * B * Hk * fa::row_blocks(p.rows, l.rb[0]) * tiles <= kLongOwn * p.own_grid)
-      p.own_grid = p.own_grid / sms * static_cast<int>(sms - l.prefix_ctas);
-  }
+  if (prefix_len > 0 && l.prefix_ctas * 4 <= 3ll * sms)
+    p.own_grid = p.own_grid / sms * static_cast<int>(sms - l.prefix_ctas);
   const Caches c = {k_cache, v_cache, strides, d, page_size, Hk, n_pages};
   return d == 64 ? launch<64>(c, p, l, rows, stream) : launch<128>(c, p, l, rows, stream);
 }

@@ -103,9 +103,12 @@ __device__ __forceinline__ int row_prefix_keys(const PagedParams& p, const SeqKe
 
 // Units that a CTA takes at least: with fewer, the parts' O (rb * D * 4 bytes,
 // written and read again) outweighs the keys they read (512 D bytes a tile), with
-// more, short calls leave SMs idle.  Row blocks of 256: 8 for a prefix (64
-// sequences behind 8192 tokens: 36 us, with 4 it takes 58), 3 for own keys (16 x
-// 1000 keys, 2 K/V heads: 21 us, with 8 it takes 27).
+// more, short calls leave SMs idle.  Row blocks of 256: 3 for own keys (16 x 1000
+// keys, 2 K/V heads: 21 us, with 8 it takes 27), 8 for a prefix, a middle: us with
+// 4 / 6 / 8 / 12, 32/8 heads unless noted: 64 sequences behind 3000 tokens 28 / 30 / 34 /
+// 41, behind 6000 43 / 31 / 35 / 43, behind 20000 58 / 58 / 58 / 49; 40 x 2 of 16/4 heads
+// behind 12000 34 / 36 / 34 / 39; 128 x 2 of 16/16 behind 2000 65 / 52 / 43 / 43; 128 of 64/8
+// (d = 64) behind 1500 33 / 33 / 28 / 36; 100 of 8/2 (d = 64) behind 8000 23 / 25 / 28 / 33.
 __host__ __device__ constexpr int least_units(int rb, bool prefix) {
   return rb == 16 ? 1 : rb == 128 ? 4 : prefix ? 8 : 3;
 }

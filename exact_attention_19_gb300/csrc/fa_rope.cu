@@ -24,7 +24,8 @@ fa::RopeView contiguous(int heads, int n, int d) {
 
 // Heads per CTA: the angles are computed once per token and CTA, so a CTA takes
 // several heads; but enough CTAs are wanted that the last wave of them is short
-// (3 x 4099 tokens, 32 heads: 34.5 us with 4 heads, 35.6 with 8, 39.6 with 16).  Few
+// (3 x 4099 tokens, 32 heads: 33.5 us with 4 heads, 34.0 with 8, 41.2 with 16;
+// 2 x 2000 of 40: 13.9, 13.2, 12.8, with 2 it takes 16.4).  Few
 // tokens are spread over the SMs whatever the angles cost.
 constexpr long long kCtasPerSm = 24;
 constexpr long long kLeastHeads = 4;

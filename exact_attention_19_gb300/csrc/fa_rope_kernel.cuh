@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
     first += p.heads[t];
     if (lo >= hi) continue;
     const uint16_t* const src = p.src[t] + b * p.src_s[t].b + n * p.src_s[t].n;
-    // heads in flight, two loads of 16 bytes each (4 x 2048 appended: 22.9 us with 2, 23.7 with 4; 4 x 8192
-    // rotated: 104.7 with 2, 103.1 with 4)
+    // heads in flight, two loads of 16 bytes each (4 x 2048 appended: 22.0 us with 2, 24.1 with 4; 4 x 8192
+    // rotated: 103.6 with 2, 102.5 with 4)
     constexpr int kU = PAGED ? 2 : 4;
     for (int h = lo; h < hi; h += kU) {
       uint4 a[kU], e[kU];

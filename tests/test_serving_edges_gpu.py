@@ -312,3 +312,23 @@ def test_padding_rows_may_hold_anything(fa, H, T, prefix_len):
     q[2] = math.inf
     got, got_l = run_paged(fa, c, q, [T, 2 * T, 0], [T, 1, T], prefix_len=prefix_len)
     assert torch.equal(got, o) and torch.equal(got_l, lse)
+
+
+@pytest.mark.parametrize("B,H,Hk,T,n,prefix_len", [(16, 32, 8, 1, 300, 2000), (40, 8, 2, 2, 100, 3000), (6, 16, 4, 1, 400, 2500),
+                                                  (12, 8, 2, 1, 700, 0), (3, 16, 2, 20, 500, 0)])
+def test_a_wider_table_changes_nothing(fa, B, H, Hk, T, n, prefix_len):
+    """A table as wide as a server's longest context, for sequences far shorter: the same shares of the work, so the
+    same bits."""
+    d, page = 64, 64
+    c = Cache(137, B, Hk, d, page, n, prefix_len=prefix_len)
+    lens = [n - 5 * b for b in range(B)]
+    for b in range(B):
+        c.fill(c.table[b], lens[b], b)
+    c.fill(c.prefix_pages, prefix_len, 99)
+    q = rand(138, B, H, T, d)
+    want = run_paged(fa, c, q, lens, None, prefix_len=prefix_len)
+    table = np.full((B, 2000), -1, dtype=np.int32)
+    table[:, :c.max_pages] = c.table
+    c.table = table
+    got = run_paged(fa, c, q, lens, None, prefix_len=prefix_len)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
