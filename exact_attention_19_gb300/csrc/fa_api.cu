@@ -180,8 +180,8 @@ constexpr int kSingleTileMaxKeys = 2048;
 constexpr int kPersistD64MaxKeys = 2048;
 // Causal d = 64 beyond kSingleTileMaxKeys keys: the persistent kernel under
 // cluster launch control once there are this many query-tile pairs per SM
-// (fewer, and single tiles balance better: causal 4 x 16 x 3072, 5 pairs per
-// SM, 6% faster on single tiles; 4 x 16 x 4096, 6.7 per SM, 2.5% slower).
+// (fewer, and single tiles balance better: causal 4 x 16 x 2560, 4.2 pairs per
+// SM, 5% faster on single tiles; 4 x 16 x 4096, 6.7 per SM, 2.5% slower).
 constexpr int kClcMinUnitsPerSm = 6;
 // Causal d = 128: the same dynamic schedule from this many pairs per SM
 // (4 x 32 x 8192, 27 per SM: +1%; 1 x 16 x 32000, 13 per SM with units of up

@@ -230,3 +230,9 @@ def test_timed_steps_without_flush_on_cpu_events():
 
     total, per = bench.timed_steps(FakeTorch, lambda: None, 4, None, None)
     assert per == [1.0, 1.0, 1.0, 1.0] and total == 4.0
+
+
+def test_the_default_workloads_traffic_was_taken_on_this_source():
+    """The line's roofline.traffic is null for any other source of the forward kernels than the captured one: a change
+    to it, its host code included, brings its own capture."""
+    assert bench.read_traffic(bench.DEFAULT_WORKLOAD, bench.kernel_source_hash())
