@@ -504,6 +504,7 @@ __global__ void __launch_bounds__(TileCfg<D, PAIR>::kThreads, 1)
           }
           const float neg_ref = m_bar == NEG_INF ? 0.f : -m_bar;
           float ls0 = 0.f, ls1 = 0.f, ls2 = 0.f, ls3 = 0.f;
+          // P in bf16, the type of the product's operands (fa_paged_kernel says what that costs); l sums in fp32
           auto emit = [&](const float* f, uint32_t col) {
             uint32_t pk[16];
 #pragma unroll

@@ -198,7 +198,8 @@ def rope(q, k, inv_freq, positions=None, offset: int = 0, interleaved: bool = Fa
     be the inputs themselves.  ``inv_freq``: fp64 [rot / 2] on the GPU (``rope_freqs``); the first rot elements
     of a head turn, the others are copied.  ``positions``: int32 [B, N] or [N]; None: 0, 1, 2, ...;
     ``offset`` is added.  ``interleaved``: pairs (2i, 2i + 1) instead of (i, i + rot / 2).  ``mag`` multiplies
-    the turned part.  Runs on ``stream`` (default: the current torch stream), asynchronously.
+    the turned part.  Runs on ``stream`` (default: the current torch stream), asynchronously.  Records no
+    autograd graph: ``rope_bwd`` turns the gradients back.
     """
     return _rope(False, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream)
 

@@ -367,12 +367,14 @@ int fa_version(void);
 
 /*
  * fa_fwd_status -- synchronise `stream`, then report whether any kernel of
- * this library (forward, split-KV, backward) on the current device gave up on
- * a wait (FA_ERR_TIMEOUT) since the last clear.  Every wait inside the kernels
- * is bounded (about 2 s); a wait that runs out records the failing role in the
- * device status word (bit 0, and bits 8.. = 1 softmax/compute, 2 producer,
- * 4 MMA issuer, 8 epilogue), the CTA drains its in-flight copies and MMAs,
- * frees its tensor memory and exits.  *detail (optional) receives the raw
+ * this library (forward, split-KV, backward, paged and shared-prefix attention)
+ * on the current device gave up on a wait (FA_ERR_TIMEOUT) since the last
+ * clear.  Every wait inside the kernels is bounded (about 2 s); a wait that
+ * runs out records the failing role in the device status word (bit 0, and bits
+ * 8.. = 1 softmax/compute, 2 producer, 4 MMA issuer, 8 epilogue, 32 loader of Q;
+ * 16: the CTA's shared memory did not begin on a 1024-byte boundary, and it
+ * computed nothing), the CTA drains its in-flight copies and MMAs, frees its
+ * tensor memory and exits.  *detail (optional) receives the raw
  * status word.  clear != 0 resets the word.  Returns FA_OK, FA_ERR_TIMEOUT,
  * FA_ERR_PAGE (bit 1 alone: a page index or sequence length that the paged
  * calls met lies outside the cache or its table), or FA_ERR_LAUNCH if
