@@ -332,3 +332,49 @@ def test_a_wider_table_changes_nothing(fa, B, H, Hk, T, n, prefix_len):
     c.table = table
     got = run_paged(fa, c, q, lens, None, prefix_len=prefix_len)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_threads_that_share_a_stream(fa):
+    """Host threads whose calls interleave on one stream (prefix, own-key and merge kernels of several calls in any
+    order), each with a workspace of its own, give what they give alone."""
+    import threading
+
+    d, page = 64, 16
+    work = []
+    for i, (B, H, Hk, T, n, prefix_len) in enumerate([(6, 8, 2, 1, 90, 1500), (40, 8, 1, 1, 40, 2500), (3, 4, 2, 2, 800, 0),
+                                                      (2, 16, 1, 30, 300, 700)]):
+        c = Cache(145 + i, B, Hk, d, page, n, prefix_len=prefix_len)
+        for b in range(B):
+            c.fill(c.table[b], n, b)
+        c.fill(c.prefix_pages, prefix_len, 99)
+        q = rand(150 + i, B, H, T, d)
+        work.append((c, q, [n - b % 7 for b in range(B)], prefix_len))
+    want = [run_paged(fa, c, q, lens, None, prefix_len=p) for c, q, lens, p in work]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got, failed, go = [[] for _ in work], [], threading.Barrier(len(work))
+
+    def call(i):
+        try:
+            c, q, lens, p = work[i]
+            table, pages, n = c.device_table(), torch.from_numpy(c.prefix_pages).cuda(), i32(lens)
+            torch.cuda.synchronize()
+            go.wait()
+            for _ in range(30):
+                if p:
+                    got[i].append(fa.fwd_prefix(q, c.k, c.v, pages, p, table, n, stream=side))
+                else:
+                    got[i].append(fa.fwd_paged(q, c.k, c.v, table, n, stream=side))
+            torch.cuda.synchronize()
+        except Exception as e:
+            failed.append(e)
+            go.abort()
+
+    threads = [threading.Thread(target=call, args=(i,)) for i in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for i, (o, lse) in enumerate(want):
+        assert all(torch.equal(a, o) and torch.equal(b, lse) for a, b in got[i])
