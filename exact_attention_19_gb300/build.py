@@ -81,7 +81,12 @@ def _stale(out: str, deps: list[str]) -> bool:
 
 
 def needs_build() -> bool:
-    return _stale(LIB_PATH, DEPS) or _stale(torch_lib_path(), TORCH_DEPS)
+    if _stale(LIB_PATH, DEPS):
+        return True
+    try:
+        return _stale(torch_lib_path(), TORCH_DEPS)
+    except Exception:  # without torch there is no module to build
+        return False
 
 
 def _start(out: str, cmd: list[str]):

@@ -261,3 +261,13 @@ def test_the_torch_module_belongs_to_one_torch(monkeypatch):
 
     with pytest.raises(ImportError, match="build it"):
         serving._load_native()
+
+
+def test_needs_build_without_torch(toy_build, monkeypatch):
+    def missing():
+        raise ImportError("No module named 'torch'")
+
+    monkeypatch.setattr(fa_build, "torch_lib_path", missing)
+    assert fa_build.needs_build()
+    fa_build.build()
+    assert not fa_build.needs_build()
