@@ -1,6 +1,7 @@
 """GB300-native fused exact attention (sm_103a): forward, split-KV, sliding
-window and backward; rotary positions; a paged K/V cache with its append,
-attention over it, and attention of a batch that shares a prefix.
+window and backward; rotary positions, with the norm of each head or without; a
+paged K/V cache with its append, attention over it, and attention of a batch
+that shares a prefix.
 
 Thin ctypes binding over ``libfa_gb300.so`` (C ABI in ``include/fa.h``):
 argument marshalling only, every step of the computation runs in the CUDA
@@ -9,6 +10,7 @@ kernels.  PyTorch supplies device memory and streams.
     o, lse = fwd(q, k, v, causal=False)          # torch bf16 [B, H, N, d]
     dq, dk, dv = bwd(q, k, v, o, lse, do, causal=False)
     q, k = rope(q, k, inv_freq)                  # rope_bwd turns the gradients back
+    q, k = norm_rope(q, k, inv_freq, q_weight, k_weight)     # norm_rope_bwd: its gradients
     q = kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq)
     o, lse = fwd_paged(q, k_cache, v_cache, block_table, seq_lens)
     o, lse = fwd_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens)
@@ -25,10 +27,12 @@ import struct
 
 __all__ = [
     "FaError", "STATUS", "NOALLOC_SCRATCH_BYTES", "library_path", "load",
-    "fwd", "bwd", "rope_freqs", "rope", "rope_bwd", "kv_append", "fwd_paged", "fwd_prefix",
+    "fwd", "bwd", "rope_freqs", "rope", "rope_bwd", "norm_rope", "norm_rope_bwd", "kv_append", "fwd_paged",
+    "fwd_prefix",
     "fa_fwd", "fa_fwd_window", "fa_fwd_splitkv", "fa_fwd_splitkv_noalloc", "fa_splitkv_workspace_bytes",
     "fa_splitkv_heuristic", "fa_bwd", "fa_bwd_window", "fa_bwd_workspace_bytes", "fa_probe_exp2", "fa_selftest_wait",
-    "fa_rope", "fa_kv_append", "fa_fwd_paged", "fa_fwd_prefix", "fa_paged_workspace_bytes",
+    "fa_rope", "fa_norm_rope", "fa_norm_rope_bwd", "fa_norm_bwd_workspace_bytes", "fa_kv_append", "fa_kv_append_norm",
+    "fa_fwd_paged", "fa_fwd_prefix", "fa_paged_workspace_bytes",
     "fa_fwd_status",
     "fa_strerror", "fa_version",
 ]
@@ -105,6 +109,17 @@ def load():
         lib.fa_rope.restype = i32
         lib.fa_kv_append.argtypes = [vp] * 11 + [i32] * 9 + [i64, ctypes.c_float, i32, vp]
         lib.fa_kv_append.restype = i32
+        lib.fa_norm_rope.argtypes = [vp] * 8 + [i64, i64, vp] + [i32] * 6 + [ctypes.c_float, i32, ctypes.c_float, i32,
+                                                                             vp]
+        lib.fa_norm_rope.restype = i32
+        lib.fa_norm_rope_bwd.argtypes = [vp] * 12 + [i64, i64, vp] + [i32] * 6 + [ctypes.c_float, i32, ctypes.c_float,
+                                                                                  i32, vp, ctypes.c_size_t, vp]
+        lib.fa_norm_rope_bwd.restype = i32
+        lib.fa_norm_bwd_workspace_bytes.argtypes = [i32]
+        lib.fa_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+        lib.fa_kv_append_norm.argtypes = [vp] * 14 + [i32] * 9 + [i64, ctypes.c_float, i32, i32, ctypes.c_float, i32,
+                                                                  vp]
+        lib.fa_kv_append_norm.restype = i32
         lib.fa_fwd_paged.argtypes = [vp] * 9 + [i32] * 8 + [ctypes.c_float, i32, i32, vp, ctypes.c_size_t, vp]
         lib.fa_fwd_paged.restype = i32
         lib.fa_fwd_prefix.argtypes = [vp] * 6 + [i32] + [vp] * 4 + [i32] * 8 + [ctypes.c_float, vp, ctypes.c_size_t,
@@ -202,6 +217,35 @@ def fa_kv_append(q, k, v, q_out, k_cache, v_cache, inv_freq, block_table, seq_le
     return load().fa_kv_append(q, k, v, q_out, k_cache, v_cache, inv_freq, block_table, seq_lens, new_lens,
                                _longs(strides), B, H, Hk, T, d, rot, n_pages, page_size, max_pages, offset, mag,
                                interleaved, stream)
+
+
+def fa_norm_rope(q, k, q_out, k_out, inv_freq, q_weight, k_weight, positions, position_stride, offset, strides, B, H,
+                 Hk, N, d, rot, mag, interleaved, eps, weights_f32, stream) -> int:
+    """Raw C-ABI norm-and-rotary call (``strides``: 12 integers or None); returns the status code."""
+    return load().fa_norm_rope(q, k, q_out, k_out, inv_freq, q_weight, k_weight, positions, position_stride, offset,
+                               _longs(strides), B, H, Hk, N, d, rot, mag, interleaved, eps, weights_f32, stream)
+
+
+def fa_norm_rope_bwd(dq, dk, q, k, dq_out, dk_out, dq_weight, dk_weight, inv_freq, q_weight, k_weight, positions,
+                     position_stride, offset, strides, B, H, Hk, N, d, rot, mag, interleaved, eps, weights_f32,
+                     workspace, workspace_bytes, stream) -> int:
+    """Raw C-ABI gradients of fa_norm_rope (``strides``: 18 integers or None); returns the status code."""
+    return load().fa_norm_rope_bwd(dq, dk, q, k, dq_out, dk_out, dq_weight, dk_weight, inv_freq, q_weight, k_weight,
+                                   positions, position_stride, offset, _longs(strides), B, H, Hk, N, d, rot, mag,
+                                   interleaved, eps, weights_f32, workspace, workspace_bytes, stream)
+
+
+def fa_norm_bwd_workspace_bytes(d) -> int:
+    return int(load().fa_norm_bwd_workspace_bytes(int(d)))
+
+
+def fa_kv_append_norm(q, k, v, q_out, k_cache, v_cache, inv_freq, q_weight, k_weight, block_table, seq_lens, new_lens,
+                      shift, strides, B, H, Hk, T, d, rot, n_pages, page_size, max_pages, offset, mag, interleaved,
+                      norm, eps, weights_f32, stream) -> int:
+    """Raw C-ABI append with the norm (``strides``: 18 integers); returns the status code."""
+    return load().fa_kv_append_norm(q, k, v, q_out, k_cache, v_cache, inv_freq, q_weight, k_weight, block_table,
+                                    seq_lens, new_lens, shift, _longs(strides), B, H, Hk, T, d, rot, n_pages, page_size,
+                                    max_pages, offset, mag, interleaved, norm, eps, weights_f32, stream)
 
 
 def fa_fwd_paged(q, k_cache, v_cache, o, lse, block_table, seq_lens, new_lens, strides, B, H, Hk, T, d, n_pages,
@@ -373,7 +417,7 @@ def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
     return dq, dk, dv
 
 
-_SERVING = ("rope_freqs", "rope", "rope_bwd", "kv_append", "fwd_paged", "fwd_prefix")
+_SERVING = ("rope_freqs", "rope", "rope_bwd", "norm_rope", "norm_rope_bwd", "kv_append", "fwd_paged", "fwd_prefix")
 
 
 def __getattr__(name):

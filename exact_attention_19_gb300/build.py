@@ -24,7 +24,7 @@ LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa_gb300.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_rope.cu", "fa_paged.cu", "fa_probe.cu", "fa_selftest.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_ptx.cuh", "fa_host.h", "fa_fwd_kernel.cuh", "fa_fwd_persist.cuh",
-                                                       "fa_bwd_kernel.cuh", "fa_rope_kernel.cuh",
+                                                       "fa_bwd_kernel.cuh", "fa_rope_kernel.cuh", "fa_norm_kernel.cuh",
                                                        "fa_paged_kernel.cuh", "fa_paged_tile.cuh")] + [
     os.path.join(INCLUDE, "fa.h")]
 

@@ -1,5 +1,6 @@
 // fa_rope_kernel.cuh -- rotary positions over [B, H, N, d] tensors, and the
-// same rotation on the way into a paged K/V cache.
+// same rotation on the way into a paged K/V cache; with NORM each head is
+// divided by its root mean square and weighed first.
 //
 // Pair i of a head's rotated part at position p turns by the angle p * w_i:
 //   y0 = mag (x0 cos - x1 sin),  y1 = mag (x1 cos + x0 sin)
@@ -59,8 +60,13 @@ struct RopeParams {
   const int* block_table;  // [B, max_pages]
   const int* seq_lens;     // [B], with the new tokens
   const int* new_lens;     // [B] or nullptr (N each)
+  const int* shift;        // [B] or nullptr: added to a sequence's positions
   int n_pages, max_pages, page_shift;
   unsigned int* status;
+  // norm only
+  const void* weight[2];   // [d] of q and k, or nullptr (ones)
+  int weight_f32;          // their type: fp32, else bf16
+  float eps;
 };
 
 // radians per position -> turns per position modulo 1, 64 fraction bits
@@ -144,13 +150,82 @@ __device__ __forceinline__ void rotate16(uint4& a, uint4& b, const float (&c)[8]
   }
 }
 
+// The same on 16 floats (x[0..7]: first chunk).
+template <bool INTERLEAVED>
+__device__ __forceinline__ void rotate16(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int i0 = INTERLEAVED ? 2 * i : i, i1 = INTERLEAVED ? 2 * i + 1 : 8 + i;
+    const float x0 = x[i0], x1 = x[i1];
+    x[i0] = fmaf(x0, c[i], -(x1 * s[i]));
+    x[i1] = fmaf(x1, c[i], x0 * s[i]);
+  }
+}
+__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float (&x)[16]) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = bf16_lo(w[i]);
+    x[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+__device__ __forceinline__ void pack16(const float (&x)[16], uint4& a, uint4& b) {
+  a = make_uint4(rope_pack(x[0], x[1]), rope_pack(x[2], x[3]), rope_pack(x[4], x[5]), rope_pack(x[6], x[7]));
+  b = make_uint4(rope_pack(x[8], x[9]), rope_pack(x[10], x[11]), rope_pack(x[12], x[13]), rope_pack(x[14], x[15]));
+}
+
+// The weights of elements c0 .. c0 + 7 and c1 .. c1 + 7 of a head.
+__device__ __forceinline__ void load_weight16(const void* weight, int f32, int c0, int c1, float (&w)[16]) {
+  if (!weight) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = 1.f;
+  } else if (f32) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(weight) + (i < 8 ? c0 + i : c1 + i - 8));
+      w[i] = v.x;
+      w[i + 1] = v.y;
+      w[i + 2] = v.z;
+      w[i + 3] = v.w;
+    }
+  } else {
+    const uint16_t* const at = static_cast<const uint16_t*>(weight);
+    unpack16(*reinterpret_cast<const uint4*>(at + c0), *reinterpret_cast<const uint4*>(at + c1), w);
+  }
+}
+
+// The sum over the UNITS lanes that hold one head of one token; they enter and leave together, whatever the
+// rest of their warp does.
+template <int UNITS>
+__device__ __forceinline__ float head_sum(float v) {
+  const unsigned mask = ((1u << UNITS) - 1u) << (threadIdx.x & 31u & ~(UNITS - 1u));
+#pragma unroll
+  for (int o = UNITS / 2; o > 0; o >>= 1) v += __shfl_xor_sync(mask, v, o);
+  return v;
+}
+
+// One head of one token: 1 / sqrt(mean x^2 + eps), the squares summed in fp32 (two sums a thread, then lanes).
+template <int D>
+__device__ __forceinline__ float inverse_rms(const float (&x)[16], float eps) {
+  float a = 0.f, b = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a = fmaf(x[i], x[i], a);
+    b = fmaf(x[8 + i], x[8 + i], b);
+  }
+  return rsqrtf(fmaf(head_sum<D / 16>(a + b), 1.f / D, eps));
+}
+
 constexpr int kRopeThreads = 128;
 
 // grid: x = tiles of kRopeThreads / (D / 16) tokens, y = groups of heads.
 // PAGED: k and v go to the cache slots of their sequence's pages, q to dst[0];
 // a token past its sequence's new tokens, or whose slot lies outside the
 // cache, is not written.
-template <int D, bool INTERLEAVED, bool PAGED>
+// NORM: the 16 elements stay in fp32 from the load through norm, weight and
+// rotation to one rounding at the end (a rounding between norm and rotation, as
+// two calls have it, would be as large as the result's own).
+template <int D, bool INTERLEAVED, bool PAGED, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
   constexpr int kUnits = D / 16;  // threads per token
   // head range of this CTA over q, then k, then v
@@ -180,6 +255,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
     const long long own = static_cast<long long>(len) - fresh + n;
     if (n >= fresh || own < 0) return;  // padding, or a padded entry of the batch
     pos = static_cast<unsigned long long>(p.offset) + own;
+    if (p.shift) pos += static_cast<long long>(p.shift[b]);
     if (h_hi > p.heads[0]) {
       const long long pi = own >> p.page_shift;
       if (pi < p.max_pages) page = p.block_table[static_cast<long long>(b) * p.max_pages + pi];
@@ -212,6 +288,9 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
     first += p.heads[t];
     if (lo >= hi) continue;
     const uint16_t* const src = p.src[t] + b * p.src_s[t].b + n * p.src_s[t].n;
+    float weight[16];
+    if constexpr (NORM)
+      if (t < 2) load_weight16(p.weight[t], p.weight_f32, c0, c1, weight);
     // heads in flight, two loads of 16 bytes each (4 x 2048 appended: 22.0 us with 2, 24.1 with 4; 4 x 8192
     // rotated: 103.6 with 2, 102.5 with 4)
     constexpr int kU = PAGED ? 2 : 4;
@@ -236,7 +315,19 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
 #pragma unroll
       for (int i = 0; i < kU; ++i)
         if (h + i < hi) {
-          if (t < 2 && turns) rotate16<INTERLEAVED>(a[i], e[i], c, s);
+          if constexpr (NORM) {
+            if (t < 2) {
+              float x[16];
+              unpack16(a[i], e[i], x);
+              const float r = inverse_rms<D>(x, p.eps);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) x[j] *= r * weight[j];
+              if (turns) rotate16<INTERLEAVED>(x, c, s);
+              pack16(x, a[i], e[i]);
+            }
+          } else if (t < 2 && turns) {
+            rotate16<INTERLEAVED>(a[i], e[i], c, s);
+          }
           *reinterpret_cast<uint4*>(dst + (h + i) * p.dst_s[t].h + c0) = a[i];
           *reinterpret_cast<uint4*>(dst + (h + i) * p.dst_s[t].h + c1) = e[i];
         }

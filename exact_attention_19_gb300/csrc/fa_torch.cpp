@@ -28,6 +28,10 @@ decltype(&fa_kv_append) g_append = nullptr;
 decltype(&fa_fwd_paged) g_paged = nullptr;
 decltype(&fa_fwd_prefix) g_prefix = nullptr;
 decltype(&fa_paged_workspace_bytes) g_bytes = nullptr;
+decltype(&fa_norm_rope) g_norm = nullptr;
+decltype(&fa_norm_rope_bwd) g_norm_bwd = nullptr;
+decltype(&fa_norm_bwd_workspace_bytes) g_norm_bytes = nullptr;
+decltype(&fa_kv_append_norm) g_append_norm = nullptr;
 
 // A CUDA tensor of the given type and number of dimensions, or nullptr.
 const at::Tensor* tensor(PyObject* o, at::ScalarType type, int64_t dim) {
@@ -84,9 +88,10 @@ cudaStream_t stream_of(const at::Tensor& t) { return c10::cuda::getCurrentCUDASt
 PyObject* none() { Py_RETURN_NONE; }
 
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  void* p[5];
-  if (n != 5) return none();
-  for (int i = 0; i < 5; ++i) {
+  constexpr int kFunctions = 9;
+  void* p[kFunctions];
+  if (n != kFunctions) return none();
+  for (int i = 0; i < kFunctions; ++i) {
     p[i] = PyLong_AsVoidPtr(a[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -95,41 +100,107 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_paged = reinterpret_cast<decltype(g_paged)>(p[2]);
   g_prefix = reinterpret_cast<decltype(g_prefix)>(p[3]);
   g_bytes = reinterpret_cast<decltype(g_bytes)>(p[4]);
+  g_norm = reinterpret_cast<decltype(g_norm)>(p[5]);
+  g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(p[6]);
+  g_norm_bytes = reinterpret_cast<decltype(g_norm_bytes)>(p[7]);
+  g_append_norm = reinterpret_cast<decltype(g_append_norm)>(p[8]);
   return none();
 }
 
+// Positions [B, N] or [N], or None: their pointer and the stride from one sequence to the next.
+bool positions_of(PyObject* o, int64_t B, int64_t N, const int** pos, long long* stride) {
+  *pos = nullptr;
+  *stride = 0;
+  if (o == Py_None) return true;
+  if (!THPVariable_Check(o)) return false;
+  const at::Tensor& t = THPVariable_Unpack(o);
+  const int64_t dim = t.dim();
+  if (t.scalar_type() != at::kInt || !t.is_cuda() || dim < 1 || dim > 2 || t.size(dim - 1) != N ||
+      (dim == 2 && t.size(0) != B) || (N > 1 && t.stride(dim - 1) != 1))
+    return false;
+  if (dim == 2 && B > 1) *stride = t.stride(0);
+  *pos = t.const_data_ptr<int>();
+  return true;
+}
+
+// Frequencies [rot / 2], or None where that is allowed.
+bool frequencies(PyObject* o, bool optional, const double** w, int* rot) {
+  *w = nullptr;
+  *rot = 0;
+  if (optional && o == Py_None) return true;
+  const at::Tensor* t = tensor(o, at::kDouble, 1);
+  if (!t || !t->is_contiguous() || !fits_int(2 * t->size(0))) return false;
+  *w = t->const_data_ptr<double>();
+  *rot = static_cast<int>(2 * t->size(0));
+  return true;
+}
+
+// The weights of a norm, [d] in bf16 or fp32 alike, or None each.
+struct Norm {
+  const void* w[2] = {nullptr, nullptr};
+  int f32 = 0;
+  double eps = 0;
+  bool take(PyObject* q, PyObject* k, PyObject* e, int64_t d) {
+    int known = -1;
+    PyObject* const o[2] = {q, k};
+    for (int i = 0; i < 2; ++i) {
+      if (o[i] == Py_None) continue;
+      if (!THPVariable_Check(o[i])) return false;
+      const at::Tensor& t = THPVariable_Unpack(o[i]);
+      const int type = t.scalar_type() == at::kFloat ? 1 : (t.scalar_type() == at::kBFloat16 ? 0 : -1);
+      if (type < 0 || (known >= 0 && known != type) || !t.is_cuda() || t.dim() != 1 || t.size(0) != d ||
+          !t.is_contiguous())
+        return false;
+      f32 = known = type;
+      w[i] = t.const_data_ptr();
+    }
+    return number(e, &eps);
+  }
+};
+
+// What a call returns: the tensor that the caller gave, or the new one; None for none.
+PyObject* given_or(PyObject* o, const at::Tensor& t) {
+  return o != Py_None ? Py_NewRef(o) : t.defined() ? THPVariable_Wrap(t) : Py_NewRef(Py_None);
+}
+template <int N>
+PyObject* tuple(PyObject* const (&o)[N]) {
+  PyObject* r = PyTuple_New(N);
+  for (int i = 0; i < N; ++i)
+    if (!o[i]) Py_CLEAR(r);
+  for (int i = 0; i < N; ++i) {
+    if (r) PyTuple_SET_ITEM(r, i, o[i]);
+    else Py_XDECREF(o[i]);
+  }
+  return r;
+}
+
 // rope(backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out)
-PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  const at::Tensor* q = n == 10 ? bf16_4d(a[1]) : nullptr;
-  const at::Tensor* w = q ? tensor(a[3], at::kDouble, 1) : nullptr;
+// norm_rope(q, k, inv_freq, q_weight, k_weight, eps, positions, offset, interleaved, mag, q_out, k_out)
+PyObject* rope_call(PyObject* oq, PyObject* ok, PyObject* ow, PyObject* const* a, bool backward, PyObject* const* nw) {
+  const at::Tensor* q = bf16_4d(oq);
+  const double* w = nullptr;
+  int rot = 0;
   long long offset = 0;
   double mag = 0;
-  if (!w || !w->is_contiguous() || !ints(*q) || !integer(a[5], &offset) || !number(a[7], &mag)) return none();
-  const int interleaved = PyObject_IsTrue(a[6]);
+  if (!q || !frequencies(ow, nw != nullptr, &w, &rot) || !ints(*q) || !integer(a[1], &offset) || !number(a[3], &mag))
+    return none();
+  const int interleaved = PyObject_IsTrue(a[2]);
   if (interleaved < 0) return nullptr;
   const int64_t B = q->size(0), H = q->size(1), N = q->size(2), d = q->size(3);
   const at::Tensor* k = nullptr;
-  if (a[2] != Py_None) {
-    k = bf16_4d(a[2]);
+  if (ok != Py_None) {
+    k = bf16_4d(ok);
     if (!k || !ints(*k) || k->size(1) == 0 || !same(*k, B, k->size(1), N, d)) return none();
-  } else if (a[9] != Py_None) {
+  } else if (a[5] != Py_None) {
     return none();
   }
+  Norm norm;
+  if (nw && !norm.take(nw[0], nw[1], nw[2], d)) return none();
   const int* pos = nullptr;
   long long pos_stride = 0;
-  if (a[4] != Py_None) {
-    if (!THPVariable_Check(a[4])) return none();
-    const at::Tensor& t = THPVariable_Unpack(a[4]);
-    const int64_t dim = t.dim();
-    if (t.scalar_type() != at::kInt || !t.is_cuda() || dim < 1 || dim > 2 || t.size(dim - 1) != N ||
-        (dim == 2 && t.size(0) != B) || (N > 1 && t.stride(dim - 1) != 1))
-      return none();
-    if (dim == 2 && B > 1) pos_stride = t.stride(0);
-    pos = t.const_data_ptr<int>();
-  }
-  const at::Tensor qo = output(a[8], *q);
-  const at::Tensor ko = k ? output(a[9], *k) : at::Tensor();
+  if (!positions_of(a[0], B, N, &pos, &pos_stride)) return none();
+  const at::Tensor qo = output(a[4], *q);
+  const at::Tensor ko = k ? output(a[5], *k) : at::Tensor();
   if (!qo.defined() || (k && !ko.defined())) return none();
   long long s[12];
   for (long long& x : s) x = d;
@@ -139,18 +210,96 @@ PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     strides3(*k, s + 3);
     strides3(ko, s + 9);
   }
-  const int st = g_rope(q->const_data_ptr(), k ? k->const_data_ptr() : nullptr, qo.data_ptr(),
-                        k ? ko.data_ptr() : nullptr, w->const_data_ptr<double>(), pos, pos_stride, offset, s,
-                        static_cast<int>(B), static_cast<int>(H), k ? static_cast<int>(k->size(1)) : 0,
-                        static_cast<int>(N), static_cast<int>(d), static_cast<int>(2 * w->size(0)),
-                        static_cast<float>(mag), interleaved, a[0] == Py_True ? 1 : 0, stream_of(*q));
+  const void *qp = q->const_data_ptr(), *kp = k ? k->const_data_ptr() : nullptr;
+  void *qop = qo.data_ptr(), *kop = k ? ko.data_ptr() : nullptr;
+  const int b = static_cast<int>(B), h = static_cast<int>(H), hk = k ? static_cast<int>(k->size(1)) : 0,
+            rows = static_cast<int>(N), dd = static_cast<int>(d);
+  const float m = static_cast<float>(mag);
+  const cudaStream_t stream = stream_of(*q);
+  const int st = nw ? g_norm(qp, kp, qop, kop, w, norm.w[0], norm.w[1], pos, pos_stride, offset, s, b, h, hk, rows, dd,
+                             rot, m, interleaved, static_cast<float>(norm.eps), norm.f32, stream)
+                    : g_rope(qp, kp, qop, kop, w, pos, pos_stride, offset, s, b, h, hk, rows, dd, rot, m, interleaved,
+                             backward ? 1 : 0, stream);
   if (st != FA_OK) return none();
-  PyObject* const first = a[8] != Py_None ? Py_NewRef(a[8]) : THPVariable_Wrap(qo);
-  PyObject* const second = !k ? Py_NewRef(Py_None) : a[9] != Py_None ? Py_NewRef(a[9]) : THPVariable_Wrap(ko);
-  PyObject* const r = first && second ? PyTuple_Pack(2, first, second) : nullptr;
-  Py_XDECREF(first);
-  Py_XDECREF(second);
-  return r;
+  return tuple<2>({given_or(a[4], qo), given_or(a[5], ko)});
+}
+PyObject* py_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return n == 10 ? rope_call(a[1], a[2], a[3], a + 4, a[0] == Py_True, nullptr) : none();
+  END_HANDLE_TH_ERRORS
+}
+PyObject* py_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return n == 12 ? rope_call(a[0], a[1], a[2], a + 6, false, a + 3) : none();
+  END_HANDLE_TH_ERRORS
+}
+
+// norm_rope_bwd(dq, dk, q, k, inv_freq, q_weight, k_weight, eps, positions, offset, interleaved, mag, q_out, k_out,
+//               workspace)
+PyObject* py_norm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const at::Tensor* dq = n == 15 ? bf16_4d(a[0]) : nullptr;
+  const at::Tensor* q = dq ? bf16_4d(a[2]) : nullptr;
+  const double* w = nullptr;
+  int rot = 0;
+  long long offset = 0;
+  double mag = 0;
+  if (!q || !ints(*q) || dq->sizes() != q->sizes() || !frequencies(a[4], true, &w, &rot) || !integer(a[9], &offset) ||
+      !number(a[11], &mag))
+    return none();
+  const int interleaved = PyObject_IsTrue(a[10]);
+  if (interleaved < 0) return nullptr;
+  const int64_t B = q->size(0), H = q->size(1), N = q->size(2), d = q->size(3);
+  const at::Tensor *k = nullptr, *dk = nullptr;
+  if (a[3] != Py_None) {
+    k = bf16_4d(a[3]);
+    dk = bf16_4d(a[1]);
+    if (!k || !dk || !ints(*k) || k->size(1) == 0 || !same(*k, B, k->size(1), N, d) || dk->sizes() != k->sizes())
+      return none();
+  } else if (a[1] != Py_None || a[13] != Py_None || a[6] != Py_None) {
+    return none();
+  }
+  Norm norm;
+  const int* pos = nullptr;
+  long long pos_stride = 0;
+  if (!norm.take(a[5], a[6], a[7], d) || !positions_of(a[8], B, N, &pos, &pos_stride)) return none();
+  const at::Tensor qo = output(a[12], *q);
+  const at::Tensor ko = k ? output(a[13], *k) : at::Tensor();
+  if (!qo.defined() || (k && !ko.defined())) return none();
+  at::Tensor dw[2], ws;
+  for (int i = 0; i < 2; ++i)
+    if (norm.w[i]) dw[i] = at::empty({d}, q->options().dtype(at::kFloat));
+  size_t bytes = 0;
+  if (norm.w[0] || norm.w[1]) {
+    if (a[14] == Py_None) {
+      bytes = g_norm_bytes(static_cast<int>(d));
+      ws = at::empty({static_cast<int64_t>(bytes)}, q->options().dtype(at::kByte));
+    } else {
+      if (!THPVariable_Check(a[14])) return none();
+      ws = THPVariable_Unpack(a[14]);
+      if (!ws.is_cuda() || !ws.is_contiguous()) return none();
+      bytes = ws.nbytes();
+    }
+  }
+  long long s[18];
+  for (long long& x : s) x = d;
+  strides3(*dq, s);
+  strides3(*q, s + 6);
+  strides3(qo, s + 12);
+  if (k) {
+    strides3(*dk, s + 3);
+    strides3(*k, s + 9);
+    strides3(ko, s + 15);
+  }
+  const int st = g_norm_bwd(
+      dq->const_data_ptr(), k ? dk->const_data_ptr() : nullptr, q->const_data_ptr(), k ? k->const_data_ptr() : nullptr,
+      qo.data_ptr(), k ? ko.data_ptr() : nullptr, norm.w[0] ? dw[0].data_ptr<float>() : nullptr,
+      norm.w[1] ? dw[1].data_ptr<float>() : nullptr, w, norm.w[0], norm.w[1], pos, pos_stride, offset, s,
+      static_cast<int>(B), static_cast<int>(H), k ? static_cast<int>(k->size(1)) : 0, static_cast<int>(N),
+      static_cast<int>(d), rot, static_cast<float>(mag), interleaved, static_cast<float>(norm.eps), norm.f32,
+      ws.defined() ? ws.data_ptr() : nullptr, bytes, stream_of(*q));
+  if (st != FA_OK) return none();
+  return tuple<4>({given_or(a[12], qo), given_or(a[13], ko), given_or(Py_None, dw[0]), given_or(Py_None, dw[1])});
   END_HANDLE_TH_ERRORS
 }
 
@@ -178,9 +327,9 @@ struct Cache {
 };
 
 // kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq, new_lens, offset, interleaved, mag, q_out)
-PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  const at::Tensor* q = n == 13 ? bf16_4d(a[0]) : nullptr;
+// kv_append_norm(the same, eps, q_weight, k_weight, shift)
+PyObject* append_call(PyObject* const* a, PyObject* const* nw) {
+  const at::Tensor* q = bf16_4d(a[0]);
   const at::Tensor* k = q ? bf16_4d(a[1]) : nullptr;
   const at::Tensor* v = k ? bf16_4d(a[2]) : nullptr;
   long long offset = 0;
@@ -196,11 +345,15 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     return none();
   const double* w = nullptr;
   int rot = 0;
-  if (a[7] != Py_None) {
-    const at::Tensor* t = tensor(a[7], at::kDouble, 1);
-    if (!t || !t->is_contiguous()) return none();
-    w = t->const_data_ptr<double>();
-    rot = static_cast<int>(2 * t->size(0));
+  if (!frequencies(a[7], true, &w, &rot)) return none();
+  Norm norm;
+  const int* shift = nullptr;
+  if (nw && nw[0] != Py_None && !norm.take(nw[1], nw[2], nw[0], d)) return none();
+  if (nw && nw[0] == Py_None && (nw[1] != Py_None || nw[2] != Py_None)) return none();
+  if (nw && nw[3] != Py_None) {
+    const at::Tensor* t = tensor(nw[3], at::kInt, 1);
+    if (!t || t->size(0) != B || !t->is_contiguous()) return none();
+    shift = t->const_data_ptr<int>();
   }
   const at::Tensor qo = output(a[12], *q);
   if (!qo.defined()) return none();
@@ -208,15 +361,29 @@ PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   strides3(*k, s + 3);
   strides3(*v, s + 6);
   strides3(qo, s + 9);
-  const int st = g_append(q->const_data_ptr(), k->const_data_ptr(), v->const_data_ptr(), qo.data_ptr(),
-                          c.k->data_ptr(), c.v->data_ptr(), w, c.table->const_data_ptr<int>(),
-                          c.lens->const_data_ptr<int>(), c.fresh, s, static_cast<int>(B),
-                          static_cast<int>(q->size(1)), static_cast<int>(Hk), static_cast<int>(T), static_cast<int>(d),
-                          rot, static_cast<int>(c.k->size(0)), static_cast<int>(c.k->size(2)),
-                          static_cast<int>(c.table->size(1)), offset, static_cast<float>(mag), interleaved,
-                          stream_of(*k));
-  if (st != FA_OK) return none();
-  return a[12] != Py_None ? Py_NewRef(a[12]) : THPVariable_Wrap(qo);
+  const void *qp = q->const_data_ptr(), *kp = k->const_data_ptr(), *vp = v->const_data_ptr();
+  void *qop = qo.data_ptr(), *kc = c.k->data_ptr(), *vc = c.v->data_ptr();
+  const int *table = c.table->const_data_ptr<int>(), *lens = c.lens->const_data_ptr<int>();
+  const int b = static_cast<int>(B), h = static_cast<int>(q->size(1)), hk = static_cast<int>(Hk),
+            rows = static_cast<int>(T), dd = static_cast<int>(d), pages = static_cast<int>(c.k->size(0)),
+            page = static_cast<int>(c.k->size(2)), max_pages = static_cast<int>(c.table->size(1));
+  const float m = static_cast<float>(mag);
+  const cudaStream_t stream = stream_of(*k);
+  const int st = nw ? g_append_norm(qp, kp, vp, qop, kc, vc, w, norm.w[0], norm.w[1], table, lens, c.fresh, shift, s, b,
+                                    h, hk, rows, dd, rot, pages, page, max_pages, offset, m, interleaved,
+                                    nw[0] != Py_None ? 1 : 0, static_cast<float>(norm.eps), norm.f32, stream)
+                    : g_append(qp, kp, vp, qop, kc, vc, w, table, lens, c.fresh, s, b, h, hk, rows, dd, rot, pages, page,
+                               max_pages, offset, m, interleaved, stream);
+  return st == FA_OK ? given_or(a[12], qo) : none();
+}
+PyObject* py_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return n == 13 ? append_call(a, nullptr) : none();
+  END_HANDLE_TH_ERRORS
+}
+PyObject* py_append_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  return n == 17 ? append_call(a, a + 13) : none();
   END_HANDLE_TH_ERRORS
 }
 
@@ -280,19 +447,17 @@ PyObject* py_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       B, H, Hk, T, d, n_pages, page, max_pages, static_cast<float>(scale), static_cast<int>(left),
                       static_cast<int>(right), ws.data_ptr(), bytes, stream_of(*q));
   if (st != FA_OK) return none();
-  PyObject* const first = a[11] != Py_None ? Py_NewRef(a[11]) : THPVariable_Wrap(out);
-  PyObject* const second = a[12] != Py_None ? Py_NewRef(a[12]) : THPVariable_Wrap(lse);
-  PyObject* const r = first && second ? PyTuple_Pack(2, first, second) : nullptr;
-  Py_XDECREF(first);
-  Py_XDECREF(second);
-  return r;
+  return tuple<2>({given_or(a[11], out), given_or(a[12], lse)});
   END_HANDLE_TH_ERRORS
 }
 
 #define FA_FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr
 PyMethodDef g_methods[] = {{"bind", FA_FAST(py_bind)},
                            {"rope", FA_FAST(py_rope)},
+                           {"norm_rope", FA_FAST(py_norm_rope)},
+                           {"norm_rope_bwd", FA_FAST(py_norm_bwd)},
                            {"kv_append", FA_FAST(py_append)},
+                           {"kv_append_norm", FA_FAST(py_append_norm)},
                            {"paged", FA_FAST(py_paged)},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "fa_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,6 +1,7 @@
-"""Rotary positions and the paged K/V cache on torch tensors: ``rope_freqs``,
-``rope``, ``rope_bwd``, ``kv_append``, ``fwd_paged``, ``fwd_prefix`` (re-exported by
-the package).
+"""Rotary positions, the norm of each head with them, and the paged K/V cache on
+torch tensors: ``rope_freqs``, ``rope``, ``rope_bwd``, ``norm_rope``,
+``norm_rope_bwd``, ``kv_append``, ``fwd_paged``, ``fwd_prefix`` (re-exported by the
+package).
 
 Argument checks and marshalling only; the kernels do the work.  A decoding step
 makes these calls for a few microseconds of GPU work each, so the usual case
@@ -39,12 +40,14 @@ def _load_native():
     loader.exec_module(module)
     lib = load()
     module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
-                  for f in ("fa_rope", "fa_kv_append", "fa_fwd_paged", "fa_fwd_prefix", "fa_paged_workspace_bytes")))
+                  for f in ("fa_rope", "fa_kv_append", "fa_fwd_paged", "fa_fwd_prefix", "fa_paged_workspace_bytes",
+                            "fa_norm_rope", "fa_norm_rope_bwd", "fa_norm_bwd_workspace_bytes", "fa_kv_append_norm")))
     return module
 
 
 _native = _load_native()
 _native_rope, _native_append, _native_paged = _native.rope, _native.kv_append, _native.paged
+_native_norm, _native_norm_bwd, _native_append_norm = _native.norm_rope, _native.norm_rope_bwd, _native.kv_append_norm
 
 
 def rope_freqs(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -142,50 +145,70 @@ def _rot(inv_freq):
     return 2 * inv_freq.shape[0]
 
 
-def _rope(backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream):
+def _positions(positions, B, N):
+    """(pointer, stride from one sequence to the next) of int32 positions [B, N] or [N], or None's."""
+    if positions is None:
+        return None, 0
+    if not (isinstance(positions, _Tensor) and positions.dtype is _I32 and positions.is_cuda):
+        raise TypeError("positions must be a CUDA torch.int32 tensor")
+    stride = 0
+    if positions.shape == (B, N):
+        stride = positions.stride(0) if B > 1 else 0
+    elif positions.shape != (N,):
+        raise ValueError(f"positions must be [{B}, {N}] or [{N}], is {tuple(positions.shape)}")
+    if N > 1 and positions.stride(-1) != 1:
+        raise ValueError("positions must be contiguous along the last dimension")
+    return positions.data_ptr(), stride
+
+
+def _like_q(name, k, q_shape):
+    """Heads of ``k``, checked to be a tensor beside q."""
+    _need(name, k, _BF16, 4)
+    B, _, N, d = q_shape
+    shape = k.shape
+    if shape[1] == 0 or shape != (B, shape[1], N, d):
+        raise ValueError(f"shape mismatch: q{tuple(q_shape)} {name}{tuple(shape)}")
+    return shape[1]
+
+
+def _rope(backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream, norm=None):
+    """The rotation; ``norm``: (q_weight, k_weight, eps) of the forward that norms first."""
     if stream is None:
-        done = _native_rope(backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out)
+        done = _native_rope(backward, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out) \
+            if norm is None else _native_norm(q, k, inv_freq, *norm, positions, offset, interleaved, mag, q_out, k_out)
         if done is not None:
             return done
     offset = _c_int("offset", offset, 64)
     _need("q", q, _BF16, 4)
     q_shape = q.shape
     B, H, N, d = q_shape
-    rot = _rot(inv_freq)
+    rot, w_ptr = (0, None) if norm is not None and inv_freq is None else (_rot(inv_freq), inv_freq.data_ptr())
     Hk = 0
     if k is not None:
-        _need("k", k, _BF16, 4)
-        k_shape = k.shape
-        Hk = k_shape[1]
-        if Hk == 0 or k_shape != (B, Hk, N, d):
-            raise ValueError(f"shape mismatch: q{tuple(q_shape)} k{tuple(k_shape)}")
+        Hk = _like_q("k", k, q_shape)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    p_ptr, p_stride = None, 0
-    if positions is not None:
-        if not (isinstance(positions, _Tensor) and positions.dtype is _I32 and positions.is_cuda):
-            raise TypeError("positions must be a CUDA torch.int32 tensor")
-        if positions.shape == (B, N):
-            p_stride = positions.stride(0) if B > 1 else 0
-        elif positions.shape != (N,):
-            raise ValueError(f"positions must be [{B}, {N}] or [{N}], is {tuple(positions.shape)}")
-        if N > 1 and positions.stride(-1) != 1:
-            raise ValueError("positions must be contiguous along the last dimension")
-        p_ptr = positions.data_ptr()
+    p_ptr, p_stride = _positions(positions, B, N)
+    weights = None if norm is None else _norm_weights(*norm, d)
     q_out = _rope_like("q_out", q, q_shape, q_out, stream)
     none = (d, d, d)
     if Hk:
-        k_out = _rope_like("k_out", k, k_shape, k_out, stream)
+        k_out = _rope_like("k_out", k, k.shape, k_out, stream)
         k_ptr, ko_ptr = k.data_ptr(), k_out.data_ptr()
-        ks, ko = _strides3("k", k, k_shape), _strides3("k_out", k_out, k_shape)
+        ks, ko = _strides3("k", k, k.shape), _strides3("k_out", k_out, k.shape)
     else:
         k_ptr = ko_ptr = None
         ks = ko = none
     strides = _pack12(*_strides3("q", q, q_shape), *ks, *_strides3("q_out", q_out, q_shape), *ko)
-    st = load().fa_rope(q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, inv_freq.data_ptr(), p_ptr, p_stride, offset,
-                        strides, B, H, Hk, N, d, rot, mag, bool(interleaved), backward, _handle(stream, q))
+    if norm is None:
+        st = load().fa_rope(q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, w_ptr, p_ptr, p_stride, offset, strides, B, H,
+                            Hk, N, d, rot, mag, bool(interleaved), backward, _handle(stream, q))
+    else:
+        wq, wk, eps, f32 = weights
+        st = load().fa_norm_rope(q.data_ptr(), k_ptr, q_out.data_ptr(), ko_ptr, w_ptr, wq, wk, p_ptr, p_stride, offset,
+                                 strides, B, H, Hk, N, d, rot, mag, bool(interleaved), eps, f32, _handle(stream, q))
     if st != 0:
-        raise FaError(st, "fa_rope")
+        raise FaError(st, "fa_rope" if norm is None else "fa_norm_rope")
     return q_out, k_out
 
 
@@ -209,6 +232,108 @@ def rope_bwd(dq, dk, inv_freq, positions=None, offset: int = 0, interleaved: boo
     """Gradients of ``rope``'s inputs from those of its outputs (from ``bwd``): the transposed rotation, same
     arguments; ``q_out`` and ``k_out`` may be views of a packed gradient."""
     return _rope(True, dq, dk, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream)
+
+
+# ---------------------------------------------------------------------------
+# the norm of each head
+# ---------------------------------------------------------------------------
+def _norm_weights(q_weight, k_weight, eps, d):
+    """(pointers of the weights or None, eps, whether they are fp32)."""
+    f32, ptrs = None, []
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is None:
+            ptrs.append(None)
+            continue
+        if not (isinstance(w, _Tensor) and w.dtype in (_BF16, _F32) and w.is_cuda):
+            raise TypeError(f"{name} must be a CUDA bf16 or fp32 tensor")
+        if w.shape != (d,) or not w.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous [{d}] tensor, is {tuple(w.shape)}")
+        if f32 is not None and f32 != (w.dtype is _F32):
+            raise TypeError("q_weight and k_weight must have the same type")
+        f32 = w.dtype is _F32
+        ptrs.append(w.data_ptr())
+    if not (math.isfinite(eps) and eps >= 0):
+        raise ValueError("eps must be finite and >= 0")
+    return *ptrs, eps, bool(f32)
+
+
+def norm_rope(q, k, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6, positions=None, offset: int = 0,
+              interleaved: bool = False, mag: float = 1.0, q_out=None, k_out=None, stream=None):
+    """(q, k) with each head divided by its root mean square, weighed and turned by its position, in one pass.
+
+    Each head x becomes x * weight / sqrt(mean(x^2) + eps) over its d elements and then turns as in ``rope``
+    (``inv_freq`` None: no rotation).  ``q_weight``, ``k_weight``: [d], bf16 or fp32 alike, or None (ones).  One
+    rounding to bf16 at the end.  All other arguments as in ``rope``; ``norm_rope_bwd`` has the gradients.
+    """
+    return _rope(False, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream,
+                 (q_weight, k_weight, eps))
+
+
+def norm_rope_bwd(dq, dk, q, k, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e-6, positions=None,
+                  offset: int = 0, interleaved: bool = False, mag: float = 1.0, q_out=None, k_out=None, workspace=None,
+                  stream=None):
+    """(dq, dk, dq_weight, dk_weight): gradients of ``norm_rope``'s q, k and weights from those of its outputs.
+
+    dq, dk: as the outputs of ``norm_rope``, from ``bwd``; q, k: its inputs, and its other arguments.  dk and k may be
+    None.  The weights' gradients are fp32 [d], None for a weight that is None.  ``q_out``, ``k_out``: where dq and dk
+    go, views of a packed gradient for instance, or dq and dk themselves.  ``workspace``
+    (``fa_norm_bwd_workspace_bytes(d)`` bytes) may be given; calls that may overlap need one each.
+    """
+    if stream is None:
+        done = _native_norm_bwd(dq, dk, q, k, inv_freq, q_weight, k_weight, eps, positions, offset, interleaved, mag,
+                                q_out, k_out, workspace)
+        if done is not None:
+            return done
+    offset = _c_int("offset", offset, 64)
+    _need("dq", dq, _BF16, 4)
+    _need("q", q, _BF16, 4)
+    q_shape = q.shape
+    if dq.shape != q_shape:
+        raise ValueError(f"shape mismatch: dq{tuple(dq.shape)} q{tuple(q_shape)}")
+    B, H, N, d = q_shape
+    rot, w_ptr = (0, None) if inv_freq is None else (_rot(inv_freq), inv_freq.data_ptr())
+    Hk = 0
+    if k is not None:
+        Hk = _like_q("k", k, q_shape)
+        if dk is None:
+            raise ValueError("k without dk")
+        if _like_q("dk", dk, q_shape) != Hk:
+            raise ValueError(f"shape mismatch: dk{tuple(dk.shape)} k{tuple(k.shape)}")
+    elif dk is not None or k_out is not None or k_weight is not None:
+        raise ValueError("dk, k_out or k_weight without k")
+    p_ptr, p_stride = _positions(positions, B, N)
+    wq, wk, eps, f32 = _norm_weights(q_weight, k_weight, eps, d)
+    q_out = _rope_like("q_out", q, q_shape, q_out, stream)
+    strides = [(d, d, d)] * 6
+    named = [("dq", dq), ("dk", dk), ("q", q), ("k", k), ("q_out", q_out), ("k_out", None)]
+    if Hk:
+        k_out = _rope_like("k_out", k, k.shape, k_out, stream)
+        named[5] = ("k_out", k_out)
+    for i, (name, t) in enumerate(named):
+        if t is not None:
+            strides[i] = _strides3(name, t, t.shape)
+    dwq, dwk = (_empty((d,), _F32, q, stream) if w is not None else None for w in (wq, wk))
+    ws_ptr, ws_bytes = None, 0
+    if wq is not None or wk is not None:
+        if workspace is None:
+            workspace = _empty((_norm_bwd_bytes(q.get_device(), d),), torch.uint8, q, stream)
+        elif not isinstance(workspace, _Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    ptr = [None if t is None else t.data_ptr() for t in (dq, dk, q, k, q_out, k_out, dwq, dwk)]
+    st = load().fa_norm_rope_bwd(*ptr, w_ptr, wq, wk, p_ptr, p_stride, offset, _pack18(*(x for s in strides for x in s)),
+                                 B, H, Hk, N, d, rot, mag, bool(interleaved), eps, f32, ws_ptr, ws_bytes,
+                                 _handle(stream, q))
+    if st != 0:
+        raise FaError(st, "fa_norm_rope_bwd")
+    return q_out, k_out, dwq, dwk
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_bwd_bytes(device, d):
+    """fa_norm_bwd_workspace_bytes, a function of d and the device alone."""
+    with torch.cuda.device(device):
+        return load().fa_norm_bwd_workspace_bytes(d)
 
 
 # ---------------------------------------------------------------------------
@@ -238,7 +363,8 @@ def _cache(k_cache, v_cache, block_table, seq_lens, new_lens, B, d):
 
 
 def kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq=None, new_lens=None, offset: int = 0,
-              interleaved: bool = False, mag: float = 1.0, q_out=None, stream=None):
+              interleaved: bool = False, mag: float = 1.0, q_out=None, stream=None, eps: float | None = None,
+              q_weight=None, k_weight=None, shift=None):
     """Put the new tokens' k (turned by position) and v into the paged cache and return their q, turned.
 
     q: [B, H, T, d] or None; k, v: [B, Hk, T, d] CUDA bf16, d contiguous, other strides free.
@@ -248,10 +374,17 @@ def kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq=None, n
     (None: all).  Row t is the token at own position seq_lens - new_lens + t; its rotation uses ``offset`` + that
     (``inv_freq`` None: no rotation).  Padding rows are not written (q_out included).  Two tokens must not share
     a slot.  Asynchronous; a page index outside the cache is skipped and reported by ``fa_fwd_status``.
+
+    ``eps`` not None: the heads of q and k are normed first as in ``norm_rope``, with ``q_weight`` and ``k_weight``.
+    ``shift``: int32 [B], added to the positions that a sequence's tokens turn by and not to their slots: the
+    tokens that were taken out of its cache.
     """
+    plain = eps is None and shift is None and q_weight is None and k_weight is None
     if stream is None:
         done = _native_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq, new_lens, offset,
-                              interleaved, mag, q_out)
+                              interleaved, mag, q_out) if plain else \
+            _native_append_norm(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq, new_lens, offset,
+                                interleaved, mag, q_out, eps, q_weight, k_weight, shift)
         if done is not None:
             return done
     offset = _c_int("offset", offset, 64)
@@ -282,11 +415,25 @@ def kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq=None, n
     if inv_freq is not None:
         rot, w_ptr = _rot(inv_freq), inv_freq.data_ptr()
     strides = _pack18(*qs, *_strides3("k", k, k_shape), *_strides3("v", v, k_shape), *qo, *caches)
-    st = load().fa_kv_append(q_ptr, k.data_ptr(), v.data_ptr(), qo_ptr, k_cache.data_ptr(), v_cache.data_ptr(), w_ptr,
-                             block_table.data_ptr(), seq_lens.data_ptr(), new, strides, B, H, Hk, T, d, rot, shape[0],
-                             shape[2], max_pages, offset, mag, bool(interleaved), _handle(stream, k))
+    head = (q_ptr, k.data_ptr(), v.data_ptr(), qo_ptr, k_cache.data_ptr(), v_cache.data_ptr(), w_ptr)
+    lists = (block_table.data_ptr(), seq_lens.data_ptr(), new)
+    rest = (B, H, Hk, T, d, rot, shape[0], shape[2], max_pages, offset, mag, bool(interleaved))
+    if plain:
+        st = load().fa_kv_append(*head, *lists, strides, *rest, _handle(stream, k))
+    else:
+        if eps is None and not (q_weight is None and k_weight is None):
+            raise ValueError("q_weight and k_weight belong to a norm: give eps")
+        wq, wk, e, f32 = _norm_weights(q_weight, k_weight, 0.0 if eps is None else eps, d)
+        s_ptr = None
+        if shift is not None:
+            _need("shift", shift, _I32, 1)
+            if shift.shape[0] != B or not shift.is_contiguous():
+                raise ValueError(f"shift must be a contiguous [{B}] tensor")
+            s_ptr = shift.data_ptr()
+        st = load().fa_kv_append_norm(*head, wq, wk, *lists, s_ptr, strides, *rest, eps is not None, e, f32,
+                                      _handle(stream, k))
     if st != 0:
-        raise FaError(st, "fa_kv_append")
+        raise FaError(st, "fa_kv_append" if plain else "fa_kv_append_norm")
     return q_out
 
 

@@ -273,6 +273,69 @@ int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, void*
                  int max_pages, long long offset, float mag, int interleaved, cudaStream_t stream);
 
 /*
+ * fa_norm_rope -- fa_rope of queries and keys whose heads are normed first, in
+ * one pass: each head x of a token becomes
+ *     x * weight / sqrt(mean(x^2) + eps)
+ * (the mean over its d elements), then turns as in fa_rope.
+ *
+ * q_weight, k_weight  [d], bf16 or fp32 (weights_f32 = 1) both, shared by the
+ *             heads; NULL: ones.  16-byte aligned.
+ * eps         finite, >= 0 (with 0 a head of zeros gives NaN).
+ * rot         0 (norm alone; inv_freq may be NULL), or as in fa_rope.
+ * Norm, weight and rotation in fp32 with one rounding to bf16 at the end; squares
+ * are summed in fp32, so elements of 2^60 and more overflow the sum.
+ * All else as fa_rope.
+ */
+int fa_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq, const void* q_weight,
+                 const void* k_weight, const int* positions, long long position_stride, long long offset,
+                 const long long* strides, int B, int H, int Hk, int N, int d, int rot, float mag, int interleaved,
+                 float eps, int weights_f32, cudaStream_t stream);
+
+/*
+ * fa_norm_rope_bwd -- gradients of fa_norm_rope's inputs from those of its
+ * outputs.  With g the gradient turned back, n = x / sqrt(mean(x^2) + eps):
+ *     dweight = sum over tokens and heads of g n,
+ *     dx = (g weight - n mean(g weight n)) / sqrt(mean(x^2) + eps).
+ *
+ * dq, q, dq_out  bf16 [B, H, N, d];  dk, k, dk_out  bf16 [B, Hk, N, d], Hk = 0:
+ *             no k.  q and k are the forward's inputs.  dq_out may be dq or q (same
+ *             pointer, same strides), dk_out likewise; no other overlap.
+ * dq_weight, dk_weight  fp32 [d], written (not added to); NULL: not wanted.
+ * strides     host array of 18: batch, head and row strides of dq, dk, q, k, dq_out,
+ *             dk_out, or NULL: all contiguous.
+ * workspace   fa_norm_bwd_workspace_bytes(d) bytes, 16-byte aligned (NULL where
+ *             neither weight's gradient is wanted); used by nothing else until the
+ *             call's kernels have finished.
+ * The sums over tokens and heads are fp32 in a fixed order: results repeat bit for
+ * bit on one GPU.  N == 0 writes zeros to dq_weight and dk_weight.  All else as
+ * fa_norm_rope, plus FA_ERR_WORKSPACE.
+ */
+int fa_norm_rope_bwd(const void* dq, const void* dk, const void* q, const void* k, void* dq_out, void* dk_out,
+                     float* dq_weight, float* dk_weight, const double* inv_freq, const void* q_weight,
+                     const void* k_weight, const int* positions, long long position_stride, long long offset,
+                     const long long* strides, int B, int H, int Hk, int N, int d, int rot, float mag,
+                     int interleaved, float eps, int weights_f32, void* workspace, size_t workspace_bytes,
+                     cudaStream_t stream);
+
+/* Workspace bytes of fa_norm_rope_bwd on the current device (0 for an invalid d). */
+size_t fa_norm_bwd_workspace_bytes(int d);
+
+/*
+ * fa_kv_append_norm -- fa_kv_append of queries and keys that are normed as in
+ * fa_norm_rope on the way (norm = 1; 0: as they are), at positions of their own.
+ *
+ * shift  int32 [B] or NULL: added to the positions that sequence b's tokens turn
+ *        by (what fa_kv_evict took out of its cache); the slots do not change.
+ * All else as fa_kv_append.
+ */
+int fa_kv_append_norm(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* v_cache,
+                      const double* inv_freq, const void* q_weight, const void* k_weight, const int* block_table,
+                      const int* seq_lens, const int* new_lens, const int* shift, const long long* strides, int B,
+                      int H, int Hk, int T, int d, int rot, int n_pages, int page_size, int max_pages,
+                      long long offset, float mag, int interleaved, int norm, float eps, int weights_f32,
+                      cudaStream_t stream);
+
+/*
  * fa_fwd_paged -- O and LSE (as fa_fwd) of the new tokens' queries over their
  * sequences' cached keys, grouped heads included: query head h reads K/V head
  * h / (H / Hk).
