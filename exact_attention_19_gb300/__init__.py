@@ -1,7 +1,7 @@
 """GB300-native fused exact attention (sm_103a): forward, split-KV, sliding
 window and backward; rotary positions, with the norm of each head or without; a
-paged K/V cache with its append, attention over it, and attention of a batch
-that shares a prefix.
+paged K/V cache with its append, attention over it, attention of a batch that
+shares a prefix, the weight that cached keys gather, and eviction by it.
 
 Thin ctypes binding over ``libfa_gb300.so`` (C ABI in ``include/fa.h``):
 argument marshalling only, every step of the computation runs in the CUDA
@@ -14,6 +14,8 @@ kernels.  PyTorch supplies device memory and streams.
     q = kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq)
     o, lse = fwd_paged(q, k_cache, v_cache, block_table, seq_lens)
     o, lse = fwd_prefix(q, k_cache, v_cache, prefix_pages, prefix_len, block_table, seq_lens)
+    kv_weights(q, lse, k_cache, weights, block_table, seq_lens)
+    lens, kept = kv_evict(k_cache, v_cache, weights, block_table, seq_lens, budget)
     fa_fwd(q_ptr, k_ptr, v_ptr, o_ptr, lse_ptr, B, H, Nq, Nk, d, scale, causal, stream)
 
 There is no fallback: if the library cannot be loaded, every call raises.
@@ -28,11 +30,12 @@ import struct
 __all__ = [
     "FaError", "STATUS", "NOALLOC_SCRATCH_BYTES", "library_path", "load",
     "fwd", "bwd", "rope_freqs", "rope", "rope_bwd", "norm_rope", "norm_rope_bwd", "kv_append", "fwd_paged",
-    "fwd_prefix",
+    "fwd_prefix", "kv_weights", "kv_evict",
     "fa_fwd", "fa_fwd_window", "fa_fwd_splitkv", "fa_fwd_splitkv_noalloc", "fa_splitkv_workspace_bytes",
     "fa_splitkv_heuristic", "fa_bwd", "fa_bwd_window", "fa_bwd_workspace_bytes", "fa_probe_exp2", "fa_selftest_wait",
     "fa_rope", "fa_norm_rope", "fa_norm_rope_bwd", "fa_norm_bwd_workspace_bytes", "fa_kv_append", "fa_kv_append_norm",
-    "fa_fwd_paged", "fa_fwd_prefix", "fa_paged_workspace_bytes",
+    "fa_fwd_paged", "fa_fwd_prefix", "fa_paged_workspace_bytes", "fa_kv_weights", "fa_kv_evict",
+    "fa_evict_workspace_bytes",
     "fa_fwd_status",
     "fa_strerror", "fa_version",
 ]
@@ -127,6 +130,12 @@ def load():
         lib.fa_fwd_prefix.restype = i32
         lib.fa_paged_workspace_bytes.argtypes = [i32] * 6
         lib.fa_paged_workspace_bytes.restype = ctypes.c_size_t
+        lib.fa_kv_weights.argtypes = [vp] * 8 + [i32] * 8 + [ctypes.c_float, i32, i32, ctypes.c_float, vp]
+        lib.fa_kv_weights.restype = i32
+        lib.fa_kv_evict.argtypes = [vp] * 5 + [i32] + [vp] * 5 + [i32] * 10 + [vp, ctypes.c_size_t, vp]
+        lib.fa_kv_evict.restype = i32
+        lib.fa_evict_workspace_bytes.argtypes = [i32, i32]
+        lib.fa_evict_workspace_bytes.restype = ctypes.c_size_t
         _lib = lib
     return _lib
 
@@ -266,6 +275,26 @@ def fa_fwd_prefix(q, k_cache, v_cache, o, lse, prefix_pages, prefix_len, block_t
 
 def fa_paged_workspace_bytes(B, H, Hk, T, d, prefix_len) -> int:
     return int(load().fa_paged_workspace_bytes(int(B), int(H), int(Hk), int(T), int(d), int(prefix_len)))
+
+
+def fa_kv_weights(q, lse, k_cache, weights, block_table, seq_lens, new_lens, strides, B, H, Hk, T, d, n_pages, page_size,
+                  max_pages, scale, window_left, window_right, decay, stream) -> int:
+    """Raw C-ABI weights of cached keys (``strides``: 5 integers); returns the status code."""
+    return load().fa_kv_weights(q, lse, k_cache, weights, block_table, seq_lens, new_lens, _longs(strides), B, H, Hk, T,
+                                d, n_pages, page_size, max_pages, scale, window_left, window_right, decay, stream)
+
+
+def fa_kv_evict(k_cache, v_cache, weights, block_table, table_out, out_pages, seq_lens, lens_out, shift, kept, strides,
+                B, Hk, d, n_pages, page_size, max_pages, budget, recent, sinks, slack, workspace, workspace_bytes,
+                stream) -> int:
+    """Raw C-ABI eviction (``strides``: 8 integers); returns the status code."""
+    return load().fa_kv_evict(k_cache, v_cache, weights, block_table, table_out, out_pages, seq_lens, lens_out, shift,
+                              kept, _longs(strides), B, Hk, d, n_pages, page_size, max_pages, budget, recent, sinks,
+                              slack, workspace, workspace_bytes, stream)
+
+
+def fa_evict_workspace_bytes(B, Hk) -> int:
+    return int(load().fa_evict_workspace_bytes(int(B), int(Hk)))
 
 
 def fa_fwd_status(stream=None, clear: bool = False):
@@ -417,7 +446,8 @@ def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
     return dq, dk, dv
 
 
-_SERVING = ("rope_freqs", "rope", "rope_bwd", "norm_rope", "norm_rope_bwd", "kv_append", "fwd_paged", "fwd_prefix")
+_SERVING = ("rope_freqs", "rope", "rope_bwd", "norm_rope", "norm_rope_bwd", "kv_append", "fwd_paged", "fwd_prefix",
+            "kv_weights", "kv_evict")
 
 
 def __getattr__(name):

@@ -1,9 +1,10 @@
 """Build libfa_gb300.so in-tree with nvcc (sm_103a only).
 
-Five translation units: fa_api.cu (the C-ABI front end with every dense
+Six translation units: fa_api.cu (the C-ABI front end with every dense
 forward, split-KV merge and backward kernel instantiation), fa_rope.cu (rotary
-positions and the paged cache's append), fa_paged.cu (attention over the paged
-cache), fa_probe.cu (the exp2-throughput probe) and fa_selftest.cu (the
+positions, with the norm of each head or without, and the paged cache's append),
+fa_paged.cu (attention over the paged cache), fa_cache.cu (the weight that cached
+keys gather, and eviction), fa_probe.cu (the exp2-throughput probe) and fa_selftest.cu (the
 bounded-wait self-test), compiled in parallel by one nvcc call; beside them
 fa_torch, the host-side fast path of the torch entry points (fa_torch.cpp, the
 host compiler against torch's headers; its file is named after the torch and
@@ -22,10 +23,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libfa_gb300.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_rope.cu", "fa_paged.cu", "fa_probe.cu", "fa_selftest.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_rope.cu", "fa_paged.cu", "fa_cache.cu", "fa_probe.cu",
+                                              "fa_selftest.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_ptx.cuh", "fa_host.h", "fa_fwd_kernel.cuh", "fa_fwd_persist.cuh",
                                                        "fa_bwd_kernel.cuh", "fa_rope_kernel.cuh", "fa_norm_kernel.cuh",
-                                                       "fa_paged_kernel.cuh", "fa_paged_tile.cuh")] + [
+                                                       "fa_paged_kernel.cuh", "fa_paged_tile.cuh",
+                                                       "fa_weights_kernel.cuh", "fa_evict_kernel.cuh")] + [
     os.path.join(INCLUDE, "fa.h")]
 
 TORCH_SOURCE = os.path.join(CSRC, "fa_torch.cpp")
@@ -132,7 +135,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, strict: bool = False
     if torch_failure:
         if strict:
             raise RuntimeError(f"fa_torch was not built: {torch_failure}")
-        sys.stderr.write(f"fa_torch (the torch entry points rope, kv_append, fwd_paged, fwd_prefix) was not built: "
+        sys.stderr.write(f"fa_torch (the torch entry points rope, norm_rope, kv_append, fwd_paged, "
+                         f"fwd_prefix, kv_weights, kv_evict) was not built: "
                          f"{torch_failure}\n")
     return LIB_PATH
 

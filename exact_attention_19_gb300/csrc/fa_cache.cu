@@ -1,0 +1,169 @@
+// fa_cache.cu -- entry points that keep a paged cache small: fa_kv_weights and
+// fa_kv_evict with its workspace size.  See include/fa.h for their contracts.
+#include <cmath>
+#include <cstdint>
+
+#include "fa.h"
+#include "fa_evict_kernel.cuh"
+#include "fa_host.h"
+#include "fa_weights_kernel.cuh"
+
+namespace {
+
+constexpr int kMaxKeys = 1 << 30;  // tokens of a sequence: tile arithmetic stays within an int
+
+bool misaligned(const void* p, unsigned bytes) { return reinterpret_cast<uintptr_t>(p) & (bytes - 1); }
+
+// Strides of bf16 views in multiples of 16 bytes, and of the weights (any).
+bool stride_ok(long long s, int multiple) { return s >= multiple && s % multiple == 0 && s < (1ll << 39); }
+
+int page_shift_of(int page_size) {
+  int s = 0;
+  while ((1 << s) < page_size) ++s;
+  return s;
+}
+bool page_sizes_ok(int n_pages, int page_size, int max_pages) {
+  return n_pages > 0 && max_pages > 0 && page_size >= 16 && page_size <= 256 && (page_size & (page_size - 1)) == 0 &&
+         static_cast<long long>(max_pages) * page_size <= kMaxKeys;
+}
+
+size_t evict_bytes(int B, int Hk) { return static_cast<size_t>(B) * Hk * sizeof(fa::EvictHead); }
+
+}  // namespace
+
+extern "C" {
+
+int fa_kv_weights(const void* q, const float* lse, const void* k_cache, float* weights, const int* block_table,
+                  const int* seq_lens, const int* new_lens, const long long* strides, int B, int H, int Hk, int T, int d,
+                  int n_pages, int page_size, int max_pages, float scale, int window_left, int window_right,
+                  float decay, cudaStream_t stream) {
+  const bool noop = T == 0;
+  if (!k_cache || !weights || !block_table || !seq_lens || !strides || (!noop && (!q || !lse))) return FA_ERR_NULL;
+  if (misaligned(q, 16) || misaligned(k_cache, 16) || misaligned(lse, 4) || misaligned(weights, 4) ||
+      misaligned(block_table, 4) || misaligned(seq_lens, 4) || misaligned(new_lens, 4))
+    return FA_ERR_ALIGN;
+  if (d != 64 && d != 128) return FA_ERR_HEADDIM;
+  if (B <= 0 || H <= 0 || Hk <= 0 || T < 0 || H % Hk != 0 || !page_sizes_ok(n_pages, page_size, max_pages))
+    return FA_ERR_SHAPE;
+  if (window_left < -1 || window_right < -1) return FA_ERR_SHAPE;
+  if (static_cast<long long>(B) * H >= (1ll << 31) || static_cast<long long>(B) * H * T >= (1ll << 31) - 256)
+    return FA_ERR_SHAPE;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return FA_ERR_SCALE;
+  if (!std::isfinite(decay) || !(decay >= 0.f)) return FA_ERR_SCALE;
+  for (int i = 0; i < 5; ++i)  // page, head and token strides of K; page and head strides of the weights
+    if (!stride_ok(strides[i], i < 3 ? 8 : 1)) return FA_ERR_STRIDE;
+  if (noop) return FA_OK;
+  int dev = -1, sms = 0;
+  const int st = fa_host::current_device(&dev, &sms);
+  if (st != FA_OK) return st;
+  const void* ptrs[] = {q, lse, k_cache, weights, block_table, seq_lens};
+  for (const void* x : ptrs)
+    if (!fa_host::is_device_pointer(x, dev)) return FA_ERR_POINTER;
+  if (new_lens && !fa_host::is_device_pointer(new_lens, dev)) return FA_ERR_POINTER;
+  fa::WeightsParams p = {};
+  p.s.q = static_cast<const uint16_t*>(q);
+  p.s.lse = const_cast<float*>(lse);
+  p.s.table = block_table;
+  p.s.lens = seq_lens;
+  p.s.new_lens = new_lens;
+  p.s.B = B;
+  p.s.Hk = Hk;
+  p.s.T = T;
+  p.s.rows = H / Hk * T;
+  p.s.n_pages = n_pages;
+  p.s.max_pages = max_pages;
+  p.s.page_shift = page_shift_of(page_size);
+  p.s.capacity = max_pages * page_size;
+  p.s.left = window_left;
+  p.s.right = window_right;
+  p.s.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+  p.s.status = fa_host::status_word(dev);
+  if (!p.s.status) return FA_ERR_LAUNCH;
+  p.k = static_cast<const uint16_t*>(k_cache);
+  p.k_page = strides[0];
+  p.k_head = strides[1];
+  p.k_token = strides[2];
+  p.w = weights;
+  p.w_page = strides[3];
+  p.w_head = strides[4];
+  p.decay = decay;
+  const long long grid = 3ll * sms;  // what fits at once
+  return d == 64 ? fa_host::launch_kernel(fa::fa_kv_weights_kernel<64>, grid, fa::kWeightThreads, 0, stream, p)
+                 : fa_host::launch_kernel(fa::fa_kv_weights_kernel<128>, grid, fa::kWeightThreads, 0, stream, p);
+}
+
+size_t fa_evict_workspace_bytes(int B, int Hk) {
+  return B > 0 && Hk > 0 && static_cast<long long>(B) * Hk < (1ll << 30) ? evict_bytes(B, Hk) : 0;
+}
+
+int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_table, const int* table_out,
+                int out_pages, const int* seq_lens, int* lens_out, int* shift, int* kept, const long long* strides,
+                int B, int Hk, int d, int n_pages, int page_size, int max_pages, int budget, int recent, int sinks,
+                int slack, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (!k_cache || !v_cache || !weights || !block_table || !seq_lens || !lens_out || !kept || !strides || !workspace)
+    return FA_ERR_NULL;
+  if (misaligned(k_cache, 16) || misaligned(v_cache, 16) || misaligned(workspace, 16)) return FA_ERR_ALIGN;
+  const void* words[] = {weights, block_table, table_out, seq_lens, lens_out, shift, kept};
+  for (const void* x : words)
+    if (misaligned(x, 4)) return FA_ERR_ALIGN;
+  if (d != 64 && d != 128) return FA_ERR_HEADDIM;
+  if (B <= 0 || Hk <= 0 || static_cast<long long>(B) * Hk >= (1ll << 30) ||
+      !page_sizes_ok(n_pages, page_size, max_pages))
+    return FA_ERR_SHAPE;
+  if (budget <= 0 || budget > kMaxKeys || recent < 0 || sinks < 0 || slack < 0 || slack > kMaxKeys - budget ||
+      static_cast<long long>(recent) + sinks > budget)
+    return FA_ERR_SHAPE;
+  const int most = budget + slack;
+  if (table_out && (out_pages <= 0 || static_cast<long long>(out_pages) * page_size > kMaxKeys ||
+                    static_cast<long long>(out_pages) * page_size < most))
+    return FA_ERR_SHAPE;
+  for (int i = 0; i < 8; ++i)  // page, head and token strides of K, then V; page and head strides of the weights
+    if (!stride_ok(strides[i], i < 6 ? 8 : 1)) return FA_ERR_STRIDE;
+  int dev = -1, sms = 0;
+  int st = fa_host::current_device(&dev, &sms);
+  if (st != FA_OK) return st;
+  if (workspace_bytes < evict_bytes(B, Hk)) return FA_ERR_WORKSPACE;
+  const void* ptrs[] = {k_cache, v_cache, weights, block_table, seq_lens, lens_out, kept, workspace};
+  for (const void* x : ptrs)
+    if (!fa_host::is_device_pointer(x, dev)) return FA_ERR_POINTER;
+  if ((table_out && !fa_host::is_device_pointer(table_out, dev)) || (shift && !fa_host::is_device_pointer(shift, dev)))
+    return FA_ERR_POINTER;
+  fa::EvictParams p = {};
+  void* const caches[2] = {k_cache, v_cache};
+  for (int i = 0; i < 2; ++i) {
+    p.cache[i] = static_cast<uint16_t*>(caches[i]);
+    p.page[i] = strides[3 * i];
+    p.head[i] = strides[3 * i + 1];
+    p.token[i] = strides[3 * i + 2];
+  }
+  p.w = weights;
+  p.w_page = strides[6];
+  p.w_head = strides[7];
+  p.table = block_table;
+  p.table_out = table_out ? table_out : block_table;
+  p.lens = seq_lens;
+  p.lens_out = lens_out;
+  p.shift = shift;
+  p.kept = kept;
+  p.heads = static_cast<fa::EvictHead*>(workspace);
+  p.B = B;
+  p.Hk = Hk;
+  p.n_pages = n_pages;
+  p.max_pages = max_pages;
+  p.out_pages = table_out ? out_pages : max_pages;
+  p.page_shift = page_shift_of(page_size);
+  p.capacity = max_pages * page_size;
+  p.budget = budget;
+  p.recent = recent;
+  p.sinks = sinks;
+  p.most = most;
+  p.status = fa_host::status_word(dev);
+  if (!p.status) return FA_ERR_LAUNCH;
+  const long long heads = static_cast<long long>(B) * Hk;
+  st = fa_host::launch_kernel(fa::fa_evict_select_kernel, heads, fa::kSelectThreads, 0, stream, p);
+  if (st != FA_OK) return st;
+  return d == 64 ? fa_host::launch_kernel(fa::fa_evict_move_kernel<64>, 2 * heads, fa::kMoveThreads, 0, stream, p)
+                 : fa_host::launch_kernel(fa::fa_evict_move_kernel<128>, 2 * heads, fa::kMoveThreads, 0, stream, p);
+}
+
+}  // extern "C"

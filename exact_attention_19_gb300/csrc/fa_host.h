@@ -36,6 +36,24 @@ inline int launched(cudaError_t e) {
   return FA_ERR_LAUNCH;
 }
 
+// Programmatic dependent launch: the kernel may be scheduled while the one ahead
+// of it on the stream still runs, and waits on the device (griddepcontrol.wait)
+// for what it needs of it.
+template <typename K, typename... A>
+int launch_kernel(K kernel, long long grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return launched(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
 constexpr int kMaxDevices = 64;
 
 }  // namespace fa_host

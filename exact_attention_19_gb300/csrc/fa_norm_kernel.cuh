@@ -148,12 +148,12 @@ __global__ void __launch_bounds__(kNormBwdThreads, kNormBwdCtasPerSm) fa_norm_bw
   }
 }
 
-// dweight = the sum of the CTAs' parts.  grid: x = 32 columns each, y = q, k; a warp takes every 32nd CTA's.
+// dweight = the sum of the CTAs' parts.  grid: 32 columns of q's, then of k's, to a CTA; a warp takes every 32nd part.
 template <int D>
 __global__ void __launch_bounds__(1024) fa_norm_bwd_sum_kernel(const NormBwdParams p) {
   __shared__ float sums[32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+  const int t = blockIdx.x / (D / 32), lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x % (D / 32) * 32 + lane;
   if (!p.dweight[t]) return;
   const float* const part = p.part + static_cast<long long>(t ? p.ctas[0] : 0) * D + e;
   float v = 0.f;

@@ -130,23 +130,7 @@ Layout layout(int B, int H, int Hk, int T, int d, int prefix_len, int sms) {
 //   19.8 / 17.1 / 16.8;  512 of 3: 25.9 / 23.7 / 23.6;  160 of 31: 21.6 / 11.4 / 10.6;  16 of 77: 23.2 / 9.9 / 9.3
 constexpr long long kMergeRows = 2400, kMergeRowsPerPart = 700, kMergeTwo = 1024;
 
-// Programmatic dependent launch: the kernel may be scheduled while the one ahead
-// of it on the stream still runs, and waits on the device (paged_begin) for what
-// it needs of it.
-template <typename K, typename... A>
-int launch_kernel(K kernel, long long grid, int threads, size_t smem, cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return fa_host::launched(cudaLaunchKernelEx(&cfg, kernel, args...));
-}
+using fa_host::launch_kernel;
 
 template <int D>
 int launch_merge(const fa::PagedParams& p, long long rows, cudaStream_t stream) {

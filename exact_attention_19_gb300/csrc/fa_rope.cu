@@ -244,14 +244,7 @@ int launch_norm_bwd(fa::NormBwdParams& p, int interleaved, int sms, cudaStream_t
   const int st = fa_host::launched(interleaved ? cudaLaunchKernelEx(&cfg, fa::fa_norm_bwd_kernel<D, true>, p)
                                                : cudaLaunchKernelEx(&cfg, fa::fa_norm_bwd_kernel<D, false>, p));
   if (st != FA_OK || (!p.dweight[0] && !p.dweight[1])) return st;
-  cfg.gridDim = dim3(D / 32, 2);
-  cfg.blockDim = dim3(1024);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return fa_host::launched(cudaLaunchKernelEx(&cfg, fa::fa_norm_bwd_sum_kernel<D>, p));
+  return fa_host::launch_kernel(fa::fa_norm_bwd_sum_kernel<D>, 2 * (D / 32), 1024, 0, stream, p);
 }
 
 }  // namespace

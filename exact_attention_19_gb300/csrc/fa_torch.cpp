@@ -32,6 +32,9 @@ decltype(&fa_norm_rope) g_norm = nullptr;
 decltype(&fa_norm_rope_bwd) g_norm_bwd = nullptr;
 decltype(&fa_norm_bwd_workspace_bytes) g_norm_bytes = nullptr;
 decltype(&fa_kv_append_norm) g_append_norm = nullptr;
+decltype(&fa_kv_weights) g_weights = nullptr;
+decltype(&fa_kv_evict) g_evict = nullptr;
+decltype(&fa_evict_workspace_bytes) g_evict_bytes = nullptr;
 
 // A CUDA tensor of the given type and number of dimensions, or nullptr.
 const at::Tensor* tensor(PyObject* o, at::ScalarType type, int64_t dim) {
@@ -88,7 +91,7 @@ cudaStream_t stream_of(const at::Tensor& t) { return c10::cuda::getCurrentCUDASt
 PyObject* none() { Py_RETURN_NONE; }
 
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  constexpr int kFunctions = 9;
+  constexpr int kFunctions = 12;
   void* p[kFunctions];
   if (n != kFunctions) return none();
   for (int i = 0; i < kFunctions; ++i) {
@@ -104,6 +107,9 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   g_norm_bwd = reinterpret_cast<decltype(g_norm_bwd)>(p[6]);
   g_norm_bytes = reinterpret_cast<decltype(g_norm_bytes)>(p[7]);
   g_append_norm = reinterpret_cast<decltype(g_append_norm)>(p[8]);
+  g_weights = reinterpret_cast<decltype(g_weights)>(p[9]);
+  g_evict = reinterpret_cast<decltype(g_evict)>(p[10]);
+  g_evict_bytes = reinterpret_cast<decltype(g_evict_bytes)>(p[11]);
   return none();
 }
 
@@ -451,6 +457,120 @@ PyObject* py_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// The weights beside a cache: fp32 [n_pages, Hk, page], with their page and head strides.
+const at::Tensor* key_weights(PyObject* o, const at::Tensor& cache, long long* s) {
+  const at::Tensor* t = tensor(o, at::kFloat, 3);
+  if (!t || t->size(0) != cache.size(0) || t->size(1) != cache.size(1) || t->size(2) != cache.size(2) ||
+      (t->stride(2) != 1 && t->numel() != 0))
+    return nullptr;
+  for (int i = 0; i < 2; ++i) s[i] = t->size(i) > 1 ? t->stride(i) : t->size(2);
+  return t;
+}
+const at::Tensor* ints_of(PyObject* o, int64_t B) {
+  const at::Tensor* t = tensor(o, at::kInt, 1);
+  return t && t->size(0) == B && t->is_contiguous() ? t : nullptr;
+}
+
+// kv_weights(q, lse, k_cache, weights, block_table, seq_lens, scale, new_lens, left, right, decay)
+PyObject* py_weights(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const at::Tensor* q = n == 11 ? bf16_4d(a[0]) : nullptr;
+  const at::Tensor* lse = q ? tensor(a[1], at::kFloat, 3) : nullptr;
+  long long left = 0, right = 0;
+  double decay = 0;
+  if (!lse || !q->is_contiguous() || !ints(*q) || !lse->is_contiguous() || !integer(a[8], &left) ||
+      !integer(a[9], &right) || !fits_int(left) || !fits_int(right) || !number(a[10], &decay))
+    return none();
+  const int B = static_cast<int>(q->size(0)), H = static_cast<int>(q->size(1)), T = static_cast<int>(q->size(2)),
+            d = static_cast<int>(q->size(3));
+  if (lse->size(0) != B || lse->size(1) != H || lse->size(2) != T) return none();
+  Cache c;
+  long long s[6], ws[2];
+  if (!c.take(a[2], a[2], a[4], a[5], a[7], B, d, s)) return none();
+  const at::Tensor* w = key_weights(a[3], *c.k, ws);
+  const int Hk = static_cast<int>(c.k->size(1));
+  if (!w || Hk == 0 || H % Hk != 0) return none();
+  double scale = 1.0 / std::sqrt(static_cast<double>(d));
+  if (a[6] != Py_None && !number(a[6], &scale)) return none();
+  s[3] = ws[0];
+  s[4] = ws[1];
+  const int st = g_weights(q->const_data_ptr(), lse->const_data_ptr<float>(), c.k->const_data_ptr(),
+                           w->data_ptr<float>(), c.table->const_data_ptr<int>(), c.lens->const_data_ptr<int>(), c.fresh,
+                           s, B, H, Hk, T, d, static_cast<int>(c.k->size(0)), static_cast<int>(c.k->size(2)),
+                           static_cast<int>(c.table->size(1)), static_cast<float>(scale), static_cast<int>(left),
+                           static_cast<int>(right), static_cast<float>(decay), stream_of(*q));
+  return st == FA_OK ? Py_NewRef(a[3]) : none();
+  END_HANDLE_TH_ERRORS
+}
+
+// kv_evict(k_cache, v_cache, weights, block_table, seq_lens, budget, recent, sinks, slack, table_out, lens_out, shift,
+//          kept, workspace)
+PyObject* py_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  const at::Tensor* k = n == 14 ? bf16_4d(a[0]) : nullptr;
+  const at::Tensor* lens = k ? tensor(a[4], at::kInt, 1) : nullptr;
+  if (!lens || !ints(*lens)) return none();
+  long long v[4];
+  for (int i = 0; i < 4; ++i)
+    if (!integer(a[5 + i], v + i) || v[i] < 0 || !fits_int(v[i])) return none();
+  const int64_t most = v[0] + v[3], B = lens->size(0);
+  if (v[0] < 1 || v[1] + v[2] > v[0] || !fits_int(most)) return none();
+  Cache c;
+  long long s[8];
+  if (!c.take(a[0], a[1], a[3], a[4], Py_None, B, k->size(3), s)) return none();
+  const at::Tensor* w = key_weights(a[2], *k, s + 6);
+  if (!w) return none();
+  const int64_t Hk = k->size(1);
+  const int* to = nullptr;
+  int out_pages = 0;
+  if (a[9] != Py_None) {
+    const at::Tensor* t = tensor(a[9], at::kInt, 2);
+    if (!t || !ints(*t) || t->size(0) != B || !t->is_contiguous() || t->size(1) * k->size(2) < most) return none();
+    to = t->const_data_ptr<int>();
+    out_pages = static_cast<int>(t->size(1));
+  }
+  at::Tensor lens_out, kept, ws;
+  if (a[10] == Py_None) {
+    lens_out = at::empty({B}, lens->options());
+  } else {
+    const at::Tensor* t = ints_of(a[10], B);
+    if (!t) return none();
+    lens_out = *t;
+  }
+  int* shift = nullptr;
+  if (a[11] != Py_None) {
+    const at::Tensor* t = ints_of(a[11], B);
+    if (!t) return none();
+    shift = t->data_ptr<int>();
+  }
+  if (a[12] == Py_None) {
+    kept = at::empty({B, Hk, most}, lens->options());
+  } else {
+    const at::Tensor* t = tensor(a[12], at::kInt, 3);
+    if (!t || t->size(0) != B || t->size(1) != Hk || t->size(2) != most || !t->is_contiguous()) return none();
+    kept = *t;
+  }
+  size_t bytes = 0;
+  if (a[13] == Py_None) {
+    bytes = g_evict_bytes(static_cast<int>(B), static_cast<int>(Hk));
+    ws = at::empty({static_cast<int64_t>(bytes)}, lens->options().dtype(at::kByte));
+  } else {
+    if (!THPVariable_Check(a[13])) return none();
+    ws = THPVariable_Unpack(a[13]);
+    if (!ws.is_cuda() || !ws.is_contiguous()) return none();
+    bytes = ws.nbytes();
+  }
+  const int st = g_evict(k->data_ptr(), c.v->data_ptr(), w->data_ptr<float>(), c.table->const_data_ptr<int>(), to,
+                         out_pages, lens->const_data_ptr<int>(), lens_out.data_ptr<int>(), shift, kept.data_ptr<int>(), s,
+                         static_cast<int>(B), static_cast<int>(Hk), static_cast<int>(k->size(3)),
+                         static_cast<int>(k->size(0)), static_cast<int>(k->size(2)), static_cast<int>(c.table->size(1)),
+                         static_cast<int>(v[0]), static_cast<int>(v[1]), static_cast<int>(v[2]), static_cast<int>(v[3]),
+                         ws.data_ptr(), bytes, stream_of(*k));
+  if (st != FA_OK) return none();
+  return tuple<2>({given_or(a[10], lens_out), given_or(a[12], kept)});
+  END_HANDLE_TH_ERRORS
+}
+
 #define FA_FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr
 PyMethodDef g_methods[] = {{"bind", FA_FAST(py_bind)},
                            {"rope", FA_FAST(py_rope)},
@@ -459,6 +579,8 @@ PyMethodDef g_methods[] = {{"bind", FA_FAST(py_bind)},
                            {"kv_append", FA_FAST(py_append)},
                            {"kv_append_norm", FA_FAST(py_append_norm)},
                            {"paged", FA_FAST(py_paged)},
+                           {"kv_weights", FA_FAST(py_weights)},
+                           {"kv_evict", FA_FAST(py_evict)},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "fa_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 

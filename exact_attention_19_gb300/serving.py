@@ -1,7 +1,7 @@
 """Rotary positions, the norm of each head with them, and the paged K/V cache on
 torch tensors: ``rope_freqs``, ``rope``, ``rope_bwd``, ``norm_rope``,
-``norm_rope_bwd``, ``kv_append``, ``fwd_paged``, ``fwd_prefix`` (re-exported by the
-package).
+``norm_rope_bwd``, ``kv_append``, ``fwd_paged``, ``fwd_prefix``, ``kv_weights``,
+``kv_evict`` (re-exported by the package).
 
 Argument checks and marshalling only; the kernels do the work.  A decoding step
 makes these calls for a few microseconds of GPU work each, so the usual case
@@ -26,7 +26,7 @@ from .build import torch_lib_path
 
 _BF16, _F32, _F64, _I32 = torch.bfloat16, torch.float32, torch.float64, torch.int32
 _Tensor = torch.Tensor
-_pack6, _pack12, _pack18 = (struct.Struct(f"{n}q").pack for n in (6, 12, 18))
+_pack5, _pack6, _pack8, _pack12, _pack18 = (struct.Struct(f"{n}q").pack for n in (5, 6, 8, 12, 18))
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -41,13 +41,15 @@ def _load_native():
     lib = load()
     module.bind(*(ctypes.cast(getattr(lib, f), ctypes.c_void_p).value
                   for f in ("fa_rope", "fa_kv_append", "fa_fwd_paged", "fa_fwd_prefix", "fa_paged_workspace_bytes",
-                            "fa_norm_rope", "fa_norm_rope_bwd", "fa_norm_bwd_workspace_bytes", "fa_kv_append_norm")))
+                            "fa_norm_rope", "fa_norm_rope_bwd", "fa_norm_bwd_workspace_bytes", "fa_kv_append_norm",
+                            "fa_kv_weights", "fa_kv_evict", "fa_evict_workspace_bytes")))
     return module
 
 
 _native = _load_native()
 _native_rope, _native_append, _native_paged = _native.rope, _native.kv_append, _native.paged
 _native_norm, _native_norm_bwd, _native_append_norm = _native.norm_rope, _native.norm_rope_bwd, _native.kv_append_norm
+_native_weights, _native_evict = _native.kv_weights, _native.kv_evict
 
 
 def rope_freqs(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -426,10 +428,7 @@ def kv_append(q, k, v, k_cache, v_cache, block_table, seq_lens, inv_freq=None, n
         wq, wk, e, f32 = _norm_weights(q_weight, k_weight, 0.0 if eps is None else eps, d)
         s_ptr = None
         if shift is not None:
-            _need("shift", shift, _I32, 1)
-            if shift.shape[0] != B or not shift.is_contiguous():
-                raise ValueError(f"shift must be a contiguous [{B}] tensor")
-            s_ptr = shift.data_ptr()
+            s_ptr = _per_sequence("shift", shift, B)
         st = load().fa_kv_append_norm(*head, wq, wk, *lists, s_ptr, strides, *rest, eps is not None, e, f32,
                                       _handle(stream, k))
     if st != 0:
@@ -530,3 +529,128 @@ def fwd_prefix(q, k_cache, v_cache, prefix_pages, prefix_len: int, block_table, 
     if st != 0:
         raise FaError(st, "fa_fwd_prefix")
     return out, lse
+
+
+# ---------------------------------------------------------------------------
+# keeping the cache small
+# ---------------------------------------------------------------------------
+def _key_weights(weights, shape):
+    """Page and head strides of the fp32 [n_pages, Hk, page_size] weights beside a cache."""
+    _need("weights", weights, _F32, 3)
+    if weights.shape != shape[:3]:
+        raise ValueError(f"weights must be {list(shape[:3])}, is {tuple(weights.shape)}")
+    s0, s1, s2 = weights.stride()
+    n0, n1, n2 = shape[:3]
+    if s2 != 1 and n0 * n1 * n2:
+        raise ValueError("weights: the last dimension must be contiguous")
+    return (s0 if n0 > 1 else n2, s1 if n1 > 1 else n2)
+
+
+def _per_sequence(name, t, B):
+    _need(name, t, _I32, 1)
+    if t.shape[0] != B or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{B}] tensor")
+    return t.data_ptr()
+
+
+def kv_weights(q, lse, k_cache, weights, block_table, seq_lens, scale: float | None = None, new_lens=None,
+               window: tuple = (-1, 0), decay: float = 1.0, stream=None):
+    """Add to ``weights`` what the new tokens' rows give each cached key, and return it.
+
+    weights: fp32 [n_pages, Hk, page_size] beside the cache, slots contiguous.  For every key j of a sequence with
+    new tokens, weights[j] = decay * weights[j] + the sum of exp(scale q . k_j - lse) over the rows that see j: all
+    query heads of its K/V head and all new tokens.  The new tokens' own keys begin at 0, so a fresh array
+    needs no zeros.  ``decay`` 1 leaves keys that no row sees alone, 0 forgets everything before this call (its rows
+    may be a prompt's last ones alone).  q, ``lse``, new_lens, window and the cache as given to and returned by
+    ``fwd_paged`` or ``fwd_prefix``; call it once a step.  Runs on ``stream`` (default: the current torch
+    stream), asynchronously; a captured call stays right as the lengths grow.
+    """
+    if stream is None:
+        done = _native_weights(q, lse, k_cache, weights, block_table, seq_lens, scale, new_lens, window[0], window[1],
+                               decay)
+        if done is not None:
+            return done
+    left, right = _reach("window[0]", window[0]), _reach("window[1]", window[1])
+    _need("q", q, _BF16, 4)
+    if not q.is_contiguous():
+        raise ValueError("q must be a contiguous [B, H, T, d] tensor")
+    B, H, T, d = q.shape
+    _need("lse", lse, _F32, 3)
+    if lse.shape != (B, H, T) or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous [{B}, {H}, {T}] tensor")
+    shape, caches, max_pages, new = _cache(k_cache, k_cache, block_table, seq_lens, new_lens, B, d)
+    Hk = shape[1]
+    if Hk == 0 or H % Hk:
+        raise ValueError(f"{H} query heads do not share {Hk} K/V heads evenly")
+    st = load().fa_kv_weights(q.data_ptr(), lse.data_ptr(), k_cache.data_ptr(), weights.data_ptr(),
+                              block_table.data_ptr(), seq_lens.data_ptr(), new,
+                              _pack5(*caches[:3], *_key_weights(weights, shape)), B, H, Hk, T, d, shape[0], shape[2],
+                              max_pages, 1.0 / math.sqrt(d) if scale is None else scale, left, right, decay,
+                              _handle(stream, q))
+    if st != 0:
+        raise FaError(st, "fa_kv_weights")
+    return weights
+
+
+def kv_evict(k_cache, v_cache, weights, block_table, seq_lens, budget: int, recent: int = 0, sinks: int = 0,
+             slack: int = 0, table_out=None, lens_out=None, shift=None, kept=None, workspace=None, stream=None):
+    """Shorten the sequences to the keys that gathered most weight: (lengths, kept slots).
+
+    A sequence of more than ``budget + slack`` tokens keeps ``budget`` of them, each K/V head its own: the first
+    ``sinks``, the last ``recent``, and of those between the ones with the largest ``weights`` (``kv_weights``; of
+    equal ones the lower slots).  They keep their order and move, keys, values and weights, to slots 0 ..
+    budget - 1: of their own pages, or, with ``table_out`` (int32 [B, pages], room for budget + slack tokens), of
+    those, to which sequences that keep all their tokens are copied too; block_table's pages may then be shared.
+    In place every page belongs to one sequence, and those past the new length are free afterwards.  Keys keep the
+    positions they were turned by; ``shift`` (int32 [B], optional) is increased by the tokens that left, which is
+    what ``kv_append(shift=...)`` takes for the next ones.  A window in ``fwd_paged`` counts the kept tokens.
+
+    lengths: int32 [B] (``lens_out``, which may be ``seq_lens``); kept: int32 [B, Hk, budget + slack], the slots that
+    the kept tokens had, -1 past their number.  ``workspace`` (``fa_evict_workspace_bytes(B, Hk)`` bytes) may be
+    given; calls that may overlap need one each.  The lengths are read on the GPU, so a captured call may run every
+    step.  Runs on ``stream`` (default: the current torch stream), asynchronously.
+    """
+    if stream is None:
+        done = _native_evict(k_cache, v_cache, weights, block_table, seq_lens, budget, recent, sinks, slack, table_out,
+                             lens_out, shift, kept, workspace)
+        if done is not None:
+            return done
+    budget, recent, sinks, slack = (_c_int(n, v, 32) for n, v in (("budget", budget), ("recent", recent),
+                                                                  ("sinks", sinks), ("slack", slack)))
+    if budget < 1 or min(recent, sinks, slack) < 0 or recent + sinks > budget:
+        raise ValueError("budget must be at least 1, recent, sinks and slack at least 0, and recent + sinks at most budget")
+    most = _c_int("budget + slack", budget + slack, 32)
+    _need("seq_lens", seq_lens, _I32, 1)
+    B = seq_lens.shape[0]
+    _need("k_cache", k_cache, _BF16, 4)
+    shape, caches, max_pages, _ = _cache(k_cache, v_cache, block_table, seq_lens, None, B, k_cache.shape[3])
+    n_pages, Hk, page, d = shape
+    w_strides = _key_weights(weights, shape)
+    to_ptr, out_pages = None, 0
+    if table_out is not None:
+        _need("table_out", table_out, _I32, 2)
+        out_pages = table_out.shape[1]
+        if table_out.shape[0] != B or not table_out.is_contiguous() or out_pages * page < most:
+            raise ValueError(f"table_out must be a contiguous [{B}, pages] tensor with room for {most} tokens")
+        to_ptr = table_out.data_ptr()
+    if lens_out is None:
+        lens_out = _empty((B,), _I32, seq_lens, stream)
+    if kept is None:
+        kept = _empty((B, Hk, most), _I32, seq_lens, stream)
+    else:
+        _need("kept", kept, _I32, 3)
+        if kept.shape != (B, Hk, most) or not kept.is_contiguous():
+            raise ValueError(f"kept must be a contiguous [{B}, {Hk}, {most}] tensor")
+    if workspace is None:
+        workspace = _empty((load().fa_evict_workspace_bytes(B, Hk),), torch.uint8, seq_lens, stream)
+    elif not isinstance(workspace, _Tensor) or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    st = load().fa_kv_evict(k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr(), block_table.data_ptr(), to_ptr,
+                            out_pages, seq_lens.data_ptr(), _per_sequence("lens_out", lens_out, B),
+                            None if shift is None else _per_sequence("shift", shift, B), kept.data_ptr(),
+                            _pack8(*caches, *w_strides), B, Hk, d, n_pages, page, max_pages, budget, recent, sinks, slack,
+                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                            _handle(stream, k_cache))
+    if st != 0:
+        raise FaError(st, "fa_kv_evict")
+    return lens_out, kept

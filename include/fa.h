@@ -227,7 +227,8 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const double
             int rot, float mag, int interleaved, int backward, cudaStream_t stream);
 
 /*
- * The paged K/V cache of fa_kv_append, fa_fwd_paged and fa_fwd_prefix.
+ * The paged K/V cache of fa_kv_append, fa_fwd_paged, fa_fwd_prefix, fa_kv_weights
+ * and fa_kv_evict.
  *
  * k_cache, v_cache  bf16 [n_pages, Hk, page_size, d] views with free page, head
  *                   and token strides (elements, multiples of 8, > 0; d contiguous),
@@ -389,6 +390,72 @@ int fa_fwd_prefix(const void* q, const void* k_cache, const void* v_cache, void*
 /* Workspace bytes of fa_fwd_paged (prefix_len 0) and fa_fwd_prefix on the
  * current device (0 for invalid sizes); it does not depend on the lengths. */
 size_t fa_paged_workspace_bytes(int B, int H, int Hk, int T, int d, int prefix_len);
+
+/*
+ * fa_kv_weights -- what the new tokens' rows give each cached key, added to what
+ * it gathered before.  For every key j of a sequence with new tokens,
+ *     weights[j] = decay * weights[j] + sum exp(scale q . k_j - lse)
+ * over the rows (query heads of the key's K/V head, new tokens) that see j; the
+ * new tokens' own keys begin at 0, whatever their slots held.
+ *
+ * q, lse    bf16 [B, H, T, d] and fp32 [B, H, T], contiguous: the queries of
+ *           fa_fwd_paged or fa_fwd_prefix and the LSE that it wrote (with a prefix
+ *           the weights are those of the sequences' own keys beside it).  A row
+ *           with lse = -inf gives nothing.
+ * weights   fp32 [n_pages, Hk, page_size] view beside the cache, slots contiguous.
+ * strides   host array of 5: page, head and token strides of k_cache (as elsewhere),
+ *           page and head strides of weights (elements, > 0).
+ * decay     finite, >= 0.  1: keys that no row sees are left alone.  0: what the
+ *           slots held is not read, so every key of the sequence begins anew.
+ * Cache, table, lengths and window as in fa_fwd_paged.  Slots past a length, and
+ * those of sequences without new tokens, stay as they are.  One call a step: a
+ * second one for the same new tokens begins their weights at 0 again.
+ * Scores, exponentials and sums in fp32, each key's in a fixed order: results
+ * repeat bit for bit.  Errors as fa_fwd_paged (FA_ERR_SCALE for decay too); T == 0
+ * is a successful no-op.  No workspace.
+ */
+int fa_kv_weights(const void* q, const float* lse, const void* k_cache, float* weights, const int* block_table,
+                  const int* seq_lens, const int* new_lens, const long long* strides, int B, int H, int Hk, int T, int d,
+                  int n_pages, int page_size, int max_pages, float scale, int window_left, int window_right,
+                  float decay, cudaStream_t stream);
+
+/*
+ * fa_kv_evict -- shorten the sequences of a paged cache to the keys that gathered
+ * most.  A sequence of more than budget + slack tokens keeps `budget` of them, each
+ * K/V head its own: its first `sinks`, its last `recent`, and of those between
+ * the ones with the largest weights (of equal ones the lower slots; NaN counts
+ * as the largest, -0 as 0).  They keep their order and move, keys, values and
+ * weights, to slots 0 .. budget - 1.  Keys keep the positions they were turned by.
+ *
+ * k_cache, v_cache, weights  as in fa_kv_weights; read and written.
+ * table_out  NULL: the kept tokens stay in the sequence's own pages, of which those
+ *            past ceil(budget / page_size) are free afterwards; no page may then
+ *            be named twice by the sequences' tokens.  Else int32 [B, out_pages],
+ *            out_pages * page_size >= budget + slack: they are copied there, and so
+ *            are all tokens of a sequence that keeps them all; the pages of
+ *            block_table are only read and may be shared, those of table_out
+ *            are named once and not by block_table.
+ * seq_lens   int32 [B];  lens_out int32 [B] (may be seq_lens): the lengths afterwards.
+ * shift      int32 [B] or NULL: increased by the number of tokens that left
+ *            (fa_kv_append_norm turns the next tokens by it).
+ * kept       int32 [B, Hk, budget + slack]: the slots that the kept tokens had, in
+ *            order, -1 past their number.
+ * strides    host array of 8: page, head and token strides of k_cache and v_cache,
+ *            page and head strides of weights.
+ * budget >= 1, recent + sinks <= budget, slack >= 0.
+ * workspace  fa_evict_workspace_bytes(B, Hk) bytes, 16-byte aligned, used by nothing
+ *            else until the call's kernels have finished.
+ * A page index outside the cache that is needed raises bit 1 of the status word; its
+ * tokens count as weighing 0 and are not moved.  Lengths are read on the device, so a
+ * captured call may be replayed every step.  Errors as fa_fwd_paged.
+ */
+int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_table, const int* table_out,
+                int out_pages, const int* seq_lens, int* lens_out, int* shift, int* kept, const long long* strides,
+                int B, int Hk, int d, int n_pages, int page_size, int max_pages, int budget, int recent, int sinks,
+                int slack, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes of fa_kv_evict (0 for invalid sizes). */
+size_t fa_evict_workspace_bytes(int B, int Hk);
 
 /* Size of the fixed device array fa_fwd_splitkv_noalloc works in. */
 #define FA_NOALLOC_SCRATCH_BYTES (16u << 20)
