@@ -1,5 +1,6 @@
 // fa_cache.cu -- entry points that keep a paged cache small: fa_kv_weights and
 // fa_kv_evict with its workspace size.  See include/fa.h for their contracts.
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -25,6 +26,55 @@ int page_shift_of(int page_size) {
 bool page_sizes_ok(int n_pages, int page_size, int max_pages) {
   return n_pages > 0 && max_pages > 0 && page_size >= 16 && page_size <= 256 && (page_size & (page_size - 1)) == 0 &&
          static_cast<long long>(max_pages) * page_size <= kMaxKeys;
+}
+
+// 3-D map over the queries: (d, row of [B * H * T], 1), 128-byte swizzle, `box_rows` rows x 64 elements per box.
+bool make_rows_map(CUtensorMap* map, const void* ptr, int d, long long rows, int box_rows) {
+  fa_host::EncodeTiledFn enc = fa_host::encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows), 1u};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(d) * 2u, static_cast<cuuint64_t>(rows) * d * 2u};
+  cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_rows), 1u};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+std::atomic<bool> g_ready[fa_host::kMaxDevices];
+
+template <typename K>
+bool allow(K kernel, size_t smem) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) ==
+         cudaSuccess;
+}
+
+// The kernels' shared-memory opt-in, once per device (a repeated call is harmless).
+int ready(int dev) {
+  if (g_ready[dev].load(std::memory_order_acquire)) return FA_OK;
+  if (!allow(fa::fa_kv_weights_tile_kernel<64>, fa::WTileCfg<64>::kSmemBytes) ||
+      !allow(fa::fa_kv_weights_tile_kernel<128>, fa::WTileCfg<128>::kSmemBytes))
+    return FA_ERR_LAUNCH;
+  g_ready[dev].store(true, std::memory_order_release);
+  return FA_OK;
+}
+
+// Rows of a (sequence, K/V head) up to which the warp-level kernel takes them.
+constexpr int kWarpRows = 16;
+
+template <int D>
+int launch_weights(const fa::WeightsParams& p, long long all_rows, int page_size, int sms, cudaStream_t stream) {
+  if (p.s.rows <= kWarpRows)
+    return fa_host::launch_kernel(fa::fa_kv_weights_kernel<D>, 3ll * sms, fa::kWeightThreads, 0, stream, p);
+  using C = fa::WTileCfg<D>;
+  CUtensorMap mk, mq;
+  const long long strides[3] = {p.k_page, p.k_head, p.k_token};
+  if (!fa_host::make_cache_map(&mk, p.k, D, page_size, p.s.Hk, p.s.n_pages, strides,
+                               page_size < fa::kWeightTile ? page_size : fa::kWeightTile) ||
+      !make_rows_map(&mq, p.s.q, D, all_rows, C::kPiece))
+    return FA_ERR_LAUNCH;
+  return fa_host::launch_kernel(fa::fa_kv_weights_tile_kernel<D>, 2ll * sms, C::kThreads, C::kSmemBytes, stream, mk, mq,
+                                p);
 }
 
 size_t evict_bytes(int B, int Hk) { return static_cast<size_t>(B) * Hk * sizeof(fa::EvictHead); }
@@ -60,6 +110,7 @@ int fa_kv_weights(const void* q, const float* lse, const void* k_cache, float* w
   for (const void* x : ptrs)
     if (!fa_host::is_device_pointer(x, dev)) return FA_ERR_POINTER;
   if (new_lens && !fa_host::is_device_pointer(new_lens, dev)) return FA_ERR_POINTER;
+  if (const int r = ready(dev); r != FA_OK) return r;
   fa::WeightsParams p = {};
   p.s.q = static_cast<const uint16_t*>(q);
   p.s.lse = const_cast<float*>(lse);
@@ -87,9 +138,9 @@ int fa_kv_weights(const void* q, const float* lse, const void* k_cache, float* w
   p.w_page = strides[3];
   p.w_head = strides[4];
   p.decay = decay;
-  const long long grid = 3ll * sms;  // what fits at once
-  return d == 64 ? fa_host::launch_kernel(fa::fa_kv_weights_kernel<64>, grid, fa::kWeightThreads, 0, stream, p)
-                 : fa_host::launch_kernel(fa::fa_kv_weights_kernel<128>, grid, fa::kWeightThreads, 0, stream, p);
+  const long long all_rows = static_cast<long long>(B) * H * T;
+  return d == 64 ? launch_weights<64>(p, all_rows, page_size, sms, stream)
+                 : launch_weights<128>(p, all_rows, page_size, sms, stream);
 }
 
 size_t fa_evict_workspace_bytes(int B, int Hk) {

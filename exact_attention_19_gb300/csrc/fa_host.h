@@ -28,6 +28,23 @@ bool is_device_pointer(const void* p, int dev);
 // up); the first lookup on a device must not run inside a stream capture
 unsigned int* status_word(int dev);
 
+// 4-D map over a cache: (d, token of the page, K/V head, page), 128-byte
+// swizzle, `rows` tokens x 64 elements per box.
+inline bool make_cache_map(CUtensorMap* map, const void* ptr, int d, int page, int Hk, int n_pages, const long long* s,
+                    int rows) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(Hk),
+                        static_cast<cuuint64_t>(n_pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(s[2]) * 2u, static_cast<cuuint64_t>(s[1]) * 2u,
+                           static_cast<cuuint64_t>(s[0]) * 2u};
+  cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(rows), 1u, 1u};
+  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Status of a launch by what the launch itself returned: an error that an earlier call of the process left behind
 // is not this one's, and a call that reports a failure has turned nothing in place.
 inline int launched(cudaError_t e) {

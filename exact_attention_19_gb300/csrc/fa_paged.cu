@@ -46,22 +46,7 @@ int ready(int dev) {
   return FA_OK;
 }
 
-// 4-D map over a cache: (d, token of the page, K/V head, page), 128-byte
-// swizzle, `rows` tokens x 64 elements per box.
-bool make_cache_map(CUtensorMap* map, const void* ptr, int d, int page, int Hk, int n_pages, const long long* s,
-                    int rows) {
-  fa_host::EncodeTiledFn enc = fa_host::encode_fn();
-  if (!enc) return false;
-  cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page), static_cast<cuuint64_t>(Hk),
-                        static_cast<cuuint64_t>(n_pages)};
-  cuuint64_t strides[3] = {static_cast<cuuint64_t>(s[2]) * 2u, static_cast<cuuint64_t>(s[1]) * 2u,
-                           static_cast<cuuint64_t>(s[0]) * 2u};
-  cuuint32_t box[4] = {64u, static_cast<cuuint32_t>(rows), 1u, 1u};
-  cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
+using fa_host::make_cache_map;
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
