@@ -59,13 +59,22 @@ int ready(int dev) {
   return FA_OK;
 }
 
-// Rows of a (sequence, K/V head) up to which the warp-level kernel takes them.
-constexpr int kWarpRows = 16;
+// Rows of a (sequence, K/V head) up to which the warp-level kernel takes them.  us on it / on the tensor cores, 16
+// sequences x 8192 keys, 8 K/V heads of 128: 16 rows 59 / 141, 32 83 / 141, 48 110 / 142, 64 138 / 141, 96 193 / 142;  8 x
+// 1000 keys, 2 heads: 16 rows 5.4 / 7.6, 32 6.9 / 7.6, 48 8.3 / 7.6, 64 9.8 / 7.6;  d = 64 within 5% of these.
+constexpr int kWarpRows = 48;
 
 template <int D>
 int launch_weights(const fa::WeightsParams& p, long long all_rows, int page_size, int sms, cudaStream_t stream) {
-  if (p.s.rows <= kWarpRows)
-    return fa_host::launch_kernel(fa::fa_kv_weights_kernel<D>, 3ll * sms, fa::kWeightThreads, 0, stream, p);
+  if (p.s.rows <= kWarpRows) {
+    // 8 KB of K to a warp, or where those units are fewer than the places (by the table's width) 4 KB
+    constexpr int kM = 256 / D;
+    const long long grid = 3ll * sms;
+    const int tile = fa::WRowsCfg<kM>::kTile;
+    if (1ll * p.s.B * p.s.Hk * ((p.s.capacity + tile - 1) / tile) >= grid)
+      return fa_host::launch_kernel(fa::fa_kv_weights_kernel<D, kM>, grid, fa::kWeightThreads, 0, stream, p);
+    return fa_host::launch_kernel(fa::fa_kv_weights_kernel<D, kM / 2>, grid, fa::kWeightThreads, 0, stream, p);
+  }
   using C = fa::WTileCfg<D>;
   CUtensorMap mk, mq;
   const long long strides[3] = {p.k_page, p.k_head, p.k_token};
@@ -73,8 +82,32 @@ int launch_weights(const fa::WeightsParams& p, long long all_rows, int page_size
                                page_size < fa::kWeightTile ? page_size : fa::kWeightTile) ||
       !make_rows_map(&mq, p.s.q, D, all_rows, C::kPiece))
     return FA_ERR_LAUNCH;
-  return fa_host::launch_kernel(fa::fa_kv_weights_tile_kernel<D>, 2ll * sms, C::kThreads, C::kSmemBytes, stream, mk, mq,
-                                p);
+  // CTAs to a unit: two where a unit has many row blocks (us with 1 / 2 / 4, 32/8 heads of 128: 4096 tokens over 8192
+  // keys 229 / 215 / 268, 2 x 2048 over 8192 231 / 204 / 352, 8 x 512 over 4096 129 / 121 / 290; 12 heads, 8 x 1024 over
+  // 1024, 8 blocks: 34.6 / 35.2 / 63.5), and two or four where even they leave SMs without a unit (1024 over 1024:
+  // 38.5 / 23.4 / 17.1;  8/2 heads, 4096 over 4096: 119 / 64 / 38;  12 heads, 1024 over 1024: 14.2 / 11.6 / 16.8).  Clusters of
+  // four do not fill all SMs, which the wide ones of the first lines pay for.
+  const int blocks = (p.s.rows + 127) / 128;
+  const long long units = 1ll * p.s.B * p.s.Hk * ((p.s.capacity + C::kUnit - 1) / C::kUnit);  // at most
+  int cluster = blocks >= 16 ? 2 : 1;
+  if (blocks >= 4 && 4 * units <= sms) cluster = 4;
+  else if (blocks >= 2 && 2 * units <= sms) cluster = 2;
+  long long grid = sms / cluster;
+  if (grid > units) grid = units;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid * cluster));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return fa_host::launched(cudaLaunchKernelEx(&cfg, fa::fa_kv_weights_tile_kernel<D>, mk, mq, p));
 }
 
 size_t evict_bytes(int B, int Hk) { return static_cast<size_t>(B) * Hk * sizeof(fa::EvictHead); }
@@ -138,6 +171,13 @@ int fa_kv_weights(const void* q, const float* lse, const void* k_cache, float* w
   p.w_page = strides[3];
   p.w_head = strides[4];
   p.decay = decay;
+  p.group = H / Hk;
+  if (T > 1) {  // 2^(31 + s) / T rounded up makes r / T too large by less than 2^-s <= 1 / T for r < 2^31
+    int s = 0;
+    while ((1ll << s) < T) ++s;
+    p.t_mul = static_cast<unsigned>(((1ull << (31 + s)) + T - 1) / T);
+    p.t_shift = s - 1;
+  }
   const long long all_rows = static_cast<long long>(B) * H * T;
   return d == 64 ? launch_weights<64>(p, all_rows, page_size, sms, stream)
                  : launch_weights<128>(p, all_rows, page_size, sms, stream);
