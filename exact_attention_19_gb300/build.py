@@ -28,6 +28,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_rope.cu", "fa_paged.
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_ptx.cuh", "fa_host.h", "fa_fwd_kernel.cuh", "fa_fwd_persist.cuh",
                                                        "fa_bwd_kernel.cuh", "fa_rope_kernel.cuh", "fa_norm_kernel.cuh",
                                                        "fa_paged_kernel.cuh", "fa_paged_tile.cuh",
+                                                       "fa_cache_ptx.cuh",
                                                        "fa_weights_kernel.cuh", "fa_evict_kernel.cuh")] + [
     os.path.join(INCLUDE, "fa.h")]
 

@@ -49,11 +49,16 @@ bool allow(K kernel, size_t smem) {
          cudaSuccess;
 }
 
+// Weights that a CTA of the selection holds: as many as fit beside its histogram; up to kSelectSmall 256 threads do.
+constexpr int kSelectWindow = 48 << 10, kSelectSmall = 4 << 10;
+
 // The kernels' shared-memory opt-in, once per device (a repeated call is harmless).
 int ready(int dev) {
   if (g_ready[dev].load(std::memory_order_acquire)) return FA_OK;
   if (!allow(fa::fa_kv_weights_tile_kernel<64>, fa::WTileCfg<64>::kSmemBytes) ||
-      !allow(fa::fa_kv_weights_tile_kernel<128>, fa::WTileCfg<128>::kSmemBytes))
+      !allow(fa::fa_kv_weights_tile_kernel<128>, fa::WTileCfg<128>::kSmemBytes) ||
+      !allow(fa::fa_evict_select_kernel<256>, kSelectSmall * sizeof(float)) ||
+      !allow(fa::fa_evict_select_kernel<1024>, kSelectWindow * sizeof(float)))
     return FA_ERR_LAUNCH;
   g_ready[dev].store(true, std::memory_order_release);
   return FA_OK;
@@ -108,6 +113,26 @@ int launch_weights(const fa::WeightsParams& p, long long all_rows, int page_size
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return fa_host::launched(cudaLaunchKernelEx(&cfg, fa::fa_kv_weights_tile_kernel<D>, mk, mq, p));
+}
+
+template <int D>
+int launch_move(const fa::EvictParams& p, long long heads, int sms, cudaStream_t stream) {
+  constexpr int kRound = fa::kMoveThreads / (D / 8) * 8;  // rows of a CTA and round
+  int cluster = 1;
+  while (cluster < 8 && 2 * heads * cluster < 8ll * sms && static_cast<long long>(kRound) * cluster < p.most) cluster *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * heads * cluster));
+  cfg.blockDim = dim3(fa::kMoveThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return fa_host::launched(cudaLaunchKernelEx(&cfg, fa::fa_evict_move_kernel<D>, p));
 }
 
 size_t evict_bytes(int B, int Hk) { return static_cast<size_t>(B) * Hk * sizeof(fa::EvictHead); }
@@ -250,11 +275,16 @@ int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_t
   p.most = most;
   p.status = fa_host::status_word(dev);
   if (!p.status) return FA_ERR_LAUNCH;
-  const long long heads = static_cast<long long>(B) * Hk;
-  st = fa_host::launch_kernel(fa::fa_evict_select_kernel, heads, fa::kSelectThreads, 0, stream, p);
+  st = ready(dev);
   if (st != FA_OK) return st;
-  return d == 64 ? fa_host::launch_kernel(fa::fa_evict_move_kernel<64>, 2 * heads, fa::kMoveThreads, 0, stream, p)
-                 : fa_host::launch_kernel(fa::fa_evict_move_kernel<128>, 2 * heads, fa::kMoveThreads, 0, stream, p);
+  const long long heads = static_cast<long long>(B) * Hk;
+  p.window = p.capacity < kSelectWindow ? p.capacity : kSelectWindow;
+  st = p.window <= kSelectSmall ? fa_host::launch_kernel(fa::fa_evict_select_kernel<256>, heads, 256,
+                                                         p.window * sizeof(float), stream, p)
+                                : fa_host::launch_kernel(fa::fa_evict_select_kernel<1024>, heads, 1024,
+                                                         p.window * sizeof(float), stream, p);
+  if (st != FA_OK) return st;
+  return d == 64 ? launch_move<64>(p, heads, sms, stream) : launch_move<128>(p, heads, sms, stream);
 }
 
 }  // extern "C"

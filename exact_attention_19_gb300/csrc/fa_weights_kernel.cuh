@@ -9,6 +9,7 @@
 // rows, so there are no parts to join, no atomics, and results repeat bit for bit.
 #pragma once
 
+#include "fa_cache_ptx.cuh"
 #include "fa_paged_kernel.cuh"
 
 namespace fa {
@@ -135,18 +136,6 @@ struct WRowsCfg {
   static constexpr int kKeys = 16 * kM;                      // keys of a warp
   static constexpr int kTile = kWeightThreads / 32 * kKeys;  // keys of a unit
 };
-
-// A load that stays where it stands: left to itself the compiler puts K's loads behind the wait for the old weights.
-__device__ __forceinline__ uint4 load16(const uint16_t* at) {
-  uint4 v;
-  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
-  return v;
-}
-__device__ __forceinline__ float load4(const float* at) {
-  float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(at));
-  return v;
-}
 
 template <int D, int M>
 __global__ void __launch_bounds__(kWeightThreads, 3) fa_kv_weights_kernel(const WeightsParams p) {
@@ -333,20 +322,6 @@ struct WTileCfg {
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-// All threads of all CTAs of the cluster, warps converged.
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // The address of `addr` (this CTA's shared memory) in another CTA of the cluster.
 __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
   uint32_t r;
