@@ -49,7 +49,7 @@ bool allow(K kernel, size_t smem) {
          cudaSuccess;
 }
 
-// Weights that a CTA of the selection holds: as many as fit beside its histogram; up to kSelectSmall 256 threads do.
+// Weights that a CTA of the selection holds: as many as fit beside its histogram; up to kSelectSmall 512 threads do.
 constexpr int kSelectWindow = 48 << 10, kSelectSmall = 4 << 10;
 
 // The kernels' shared-memory opt-in, once per device (a repeated call is harmless).
@@ -57,11 +57,31 @@ int ready(int dev) {
   if (g_ready[dev].load(std::memory_order_acquire)) return FA_OK;
   if (!allow(fa::fa_kv_weights_tile_kernel<64>, fa::WTileCfg<64>::kSmemBytes) ||
       !allow(fa::fa_kv_weights_tile_kernel<128>, fa::WTileCfg<128>::kSmemBytes) ||
-      !allow(fa::fa_evict_select_kernel<256>, kSelectSmall * sizeof(float)) ||
+      !allow(fa::fa_evict_select_kernel<512>, kSelectSmall * sizeof(float)) ||
       !allow(fa::fa_evict_select_kernel<1024>, kSelectWindow * sizeof(float)))
     return FA_ERR_LAUNCH;
   g_ready[dev].store(true, std::memory_order_release);
   return FA_OK;
+}
+
+// fa_host::launch_kernel for a grid of clusters.
+template <typename K, typename... A>
+int launch_clusters(K kernel, long long clusters, int cluster, int threads, size_t smem, cudaStream_t stream,
+                    const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * cluster));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return fa_host::launched(cudaLaunchKernelEx(&cfg, kernel, args...));
 }
 
 // Rows of a (sequence, K/V head) up to which the warp-level kernel takes them.  us on it / on the tensor cores, 16
@@ -99,20 +119,7 @@ int launch_weights(const fa::WeightsParams& p, long long all_rows, int page_size
   else if (blocks >= 2 && 2 * units <= sms) cluster = 2;
   long long grid = sms / cluster;
   if (grid > units) grid = units;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid * cluster));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return fa_host::launched(cudaLaunchKernelEx(&cfg, fa::fa_kv_weights_tile_kernel<D>, mk, mq, p));
+  return launch_clusters(fa::fa_kv_weights_tile_kernel<D>, grid, cluster, C::kThreads, C::kSmemBytes, stream, mk, mq, p);
 }
 
 template <int D>
@@ -120,19 +127,7 @@ int launch_move(const fa::EvictParams& p, long long heads, int sms, cudaStream_t
   constexpr int kRound = fa::kMoveThreads / (D / 8) * 8;  // rows of a CTA and round
   int cluster = 1;
   while (cluster < 8 && 2 * heads * cluster < 8ll * sms && static_cast<long long>(kRound) * cluster < p.most) cluster *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * heads * cluster));
-  cfg.blockDim = dim3(fa::kMoveThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return fa_host::launched(cudaLaunchKernelEx(&cfg, fa::fa_evict_move_kernel<D>, p));
+  return launch_clusters(fa::fa_evict_move_kernel<D>, 2 * heads, cluster, fa::kMoveThreads, 0, stream, p);
 }
 
 size_t evict_bytes(int B, int Hk) { return static_cast<size_t>(B) * Hk * sizeof(fa::EvictHead); }
@@ -279,10 +274,9 @@ int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_t
   if (st != FA_OK) return st;
   const long long heads = static_cast<long long>(B) * Hk;
   p.window = p.capacity < kSelectWindow ? p.capacity : kSelectWindow;
-  st = p.window <= kSelectSmall ? fa_host::launch_kernel(fa::fa_evict_select_kernel<256>, heads, 256,
-                                                         p.window * sizeof(float), stream, p)
-                                : fa_host::launch_kernel(fa::fa_evict_select_kernel<1024>, heads, 1024,
-                                                         p.window * sizeof(float), stream, p);
+  const size_t smem = p.window * sizeof(float);
+  st = p.window <= kSelectSmall ? fa_host::launch_kernel(fa::fa_evict_select_kernel<512>, heads, 512, smem, stream, p)
+                                : fa_host::launch_kernel(fa::fa_evict_select_kernel<1024>, heads, 1024, smem, stream, p);
   if (st != FA_OK) return st;
   return d == 64 ? launch_move<64>(p, heads, sms, stream) : launch_move<128>(p, heads, sms, stream);
 }

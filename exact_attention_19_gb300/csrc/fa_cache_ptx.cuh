@@ -21,6 +21,13 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The address of `addr` (this CTA's shared memory) in another CTA of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
 // Loads that stay where they stand: left to itself the compiler puts them behind waits that they are to overlap.
 __device__ __forceinline__ uint4 load16(const uint16_t* at) {
   uint4 v;

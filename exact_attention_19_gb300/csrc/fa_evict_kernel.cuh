@@ -52,8 +52,10 @@ __device__ __forceinline__ unsigned weight_order(float w) {
 // histogram of the free weights that share the bits so far, and the digit at which the
 // kept ones run out.  11 bits first (sign, exponent, two of the fraction), because
 // weights share exponents: with 8 most counts of a warp met in the same few words.
+// It ends early where all weights of that digit stay, after two digits as a rule.
 // Then every warp counts what stays in its part of the list, and after one sum over
 // the warps writes it, in order.
+// Bound: latency (lengths, pages, weights, then a few barriers to a digit).
 constexpr int kSelectBins = 2048;
 
 template <int THREADS>
@@ -62,7 +64,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_evict_select_kernel(const Evict
   extern __shared__ float vals[];  // [window]
   __shared__ int hist[kSelectBins];
   __shared__ int counts[2][kWarps];
-  __shared__ int found[2];  // digit, how many of the digit's weights stay
+  __shared__ int found[3];  // digit, how many of its weights stay, how many there are
   __shared__ int first_gone;
   grid_wait();
   grid_release();
@@ -86,20 +88,25 @@ __global__ void __launch_bounds__(THREADS, 1) fa_evict_select_kernel(const Evict
   float* const w = p.w + hk * p.w_head;
   auto load = [&](int w0) {  // the weights of tokens w0 .. of a window
     const int n = min(p.window, len - w0);
-    for (int j0 = tid; j0 < n; j0 += 4 * THREADS) {
-      int page[4];
+    constexpr int kU = 8;  // in flight
+    for (int j0 = tid; j0 < n; j0 += kU * THREADS) {
+      int page[kU];
+      float v[kU];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        page[u] = j0 + u * THREADS < n ? coherent(table + ((w0 + j0 + u * THREADS) >> p.page_shift)) : -1;
+      for (int u = 0; u < kU; ++u)
+        page[u] = j0 + u * THREADS < n ? coherent(table + ((w0 + j0 + u * THREADS) >> p.page_shift)) : 0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+      for (int u = 0; u < kU; ++u) {
         const int j = j0 + u * THREADS;
-        if (j >= n) break;
-        float v = 0.f;  // a page outside the cache: its tokens weigh nothing
-        if (static_cast<unsigned>(page[u]) < static_cast<unsigned>(p.n_pages)) v = w[page[u] * p.w_page + ((w0 + j) & mask)];
-        else atomicOr(p.status, kPagedPage);
-        vals[j] = v;
+        v[u] = 0.f;  // a page outside the cache: its tokens weigh nothing
+        if (j < n) {
+          if (static_cast<unsigned>(page[u]) < static_cast<unsigned>(p.n_pages)) v[u] = load4(w + page[u] * p.w_page + ((w0 + j) & mask));
+          else atomicOr(p.status, kPagedPage);
+        }
       }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (j0 + u * THREADS < n) vals[j0 + u * THREADS] = v[u];
     }
   };
   const int windows = (len + p.window - 1) / p.window;
@@ -107,7 +114,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_evict_select_kernel(const Evict
 
   unsigned least = 0;  // the smallest order that is kept among the free ones
   int ties = 0;        // how many of that order
-  bool loaded = false;
+  bool loaded = false, from_least = false;
   if (over) {
     int want = p.budget - p.sinks - p.recent;
     if (want == 0) {
@@ -158,6 +165,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_evict_select_kernel(const Evict
             if (above < want && want <= above + n[i]) {
               found[0] = kSelectBins - 1 - kBinsEach * tid - i;
               found[1] = want - above;
+              found[2] = n[i];
             }
             above += n[i];
           }
@@ -165,9 +173,11 @@ __global__ void __launch_bounds__(THREADS, 1) fa_evict_select_kernel(const Evict
         __syncthreads();
         prefix |= static_cast<unsigned>(found[0]) << shift;
         want = found[1];
+        if (want == found[2]) break;
       }
-      least = prefix;
-      ties = want;
+      least = prefix;  // zeros below the digits that were looked at
+      ties = want;     // those with these digits; all of them where that ended the search, so their order from `least` on
+      from_least = want == found[2];
     }
   }
   // the list.  All of a window's weights have been read before any moves, and those that do land at or below their own
@@ -191,11 +201,12 @@ __global__ void __launch_bounds__(THREADS, 1) fa_evict_select_kernel(const Evict
         sure = true;
       } else {
         const unsigned o = weight_order(vals[j]);
-        sure = o > least;
-        tie = ties > 0 && o == least;
+        sure = from_least ? o >= least : o > least;
+        tie = !from_least && ties > 0 && o == least;
       }
     };
     int a = 0, t = 0;
+#pragma unroll 4
     for (int j = j0; j < j1; j += 32) {
       bool sure, tie;
       stays(j + lane, sure, tie);
@@ -217,6 +228,7 @@ __global__ void __launch_bounds__(THREADS, 1) fa_evict_select_kernel(const Evict
       equal += counts[1][i];
     }
     int gone = 0x7fffffff;
+#pragma unroll 4
     for (int j = j0; j < j1; j += 32) {
       bool sure, tie;
       stays(j + lane, sure, tie);
