@@ -122,12 +122,20 @@ int launch_weights(const fa::WeightsParams& p, long long all_rows, int page_size
   return launch_clusters(fa::fa_kv_weights_tile_kernel<D>, grid, cluster, C::kThreads, C::kSmemBytes, stream, mk, mq, p);
 }
 
+// CTAs to a head's K or V, while each has rows to move: in place a cluster of at most 8, up to three CTAs per SM in all
+// (16 x up to 8192 keys halved, 128 heads, the move alone with 1 / 2 / 4 / 8: 100 / 76 / 76 / 83 us); into other pages,
+// where none waits for another, up to four (4 x up to 31999 to 8000, 16 heads: 162 / 92 / 55 / 35 us).
 template <int D>
-int launch_move(const fa::EvictParams& p, long long heads, int sms, cudaStream_t stream) {
+int launch_move(fa::EvictParams& p, long long heads, int sms, cudaStream_t stream) {
   constexpr int kRound = fa::kMoveThreads / (D / 8) * 8;  // rows of a CTA and round
-  int cluster = 1;
-  while (cluster < 8 && 2 * heads * cluster < 8ll * sms && static_cast<long long>(kRound) * cluster < p.most) cluster *= 2;
-  return launch_clusters(fa::fa_evict_move_kernel<D>, 2 * heads, cluster, fa::kMoveThreads, 0, stream, p);
+  const bool fork = p.table_out != p.table;
+  p.parts = 1;
+  while (p.parts < (fork ? 64 : 8) && 2 * heads * p.parts < (fork ? 4ll : 3ll) * sms &&
+         static_cast<long long>(kRound) * p.parts < p.most)
+    p.parts *= 2;
+  if (fork)
+    return fa_host::launch_kernel(fa::fa_evict_move_kernel<D>, 3 * heads * p.parts, fa::kMoveThreads, 0, stream, p);
+  return launch_clusters(fa::fa_evict_move_kernel<D>, 3 * heads, p.parts, fa::kMoveThreads, 0, stream, p);
 }
 
 size_t evict_bytes(int B, int Hk) { return static_cast<size_t>(B) * Hk * sizeof(fa::EvictHead); }
@@ -204,7 +212,7 @@ int fa_kv_weights(const void* q, const float* lse, const void* k_cache, float* w
 }
 
 size_t fa_evict_workspace_bytes(int B, int Hk) {
-  return B > 0 && Hk > 0 && static_cast<long long>(B) * Hk < (1ll << 30) ? evict_bytes(B, Hk) : 0;
+  return B > 0 && Hk > 0 && static_cast<long long>(B) * Hk < (1ll << 28) ? evict_bytes(B, Hk) : 0;
 }
 
 int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_table, const int* table_out,
@@ -218,7 +226,7 @@ int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_t
   for (const void* x : words)
     if (misaligned(x, 4)) return FA_ERR_ALIGN;
   if (d != 64 && d != 128) return FA_ERR_HEADDIM;
-  if (B <= 0 || Hk <= 0 || static_cast<long long>(B) * Hk >= (1ll << 30) ||
+  if (B <= 0 || Hk <= 0 || static_cast<long long>(B) * Hk >= (1ll << 28) ||
       !page_sizes_ok(n_pages, page_size, max_pages))
     return FA_ERR_SHAPE;
   if (budget <= 0 || budget > kMaxKeys || recent < 0 || sinks < 0 || slack < 0 || slack > kMaxKeys - budget ||
@@ -250,6 +258,7 @@ int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_t
   p.w = weights;
   p.w_page = strides[6];
   p.w_head = strides[7];
+  p.w_vec = !misaligned(weights, 16) && strides[6] % 4 == 0 && strides[7] % 4 == 0;
   p.table = block_table;
   p.table_out = table_out ? table_out : block_table;
   p.lens = seq_lens;
