@@ -215,21 +215,17 @@ int append_impl(const void* q, const void* k, const void* v, void* q_out, void* 
 }
 
 // The CTAs of the norm's backward, and the sums they leave.
-constexpr long long kNormBwdHeads = 8;  // heads of an item, where items are many
 int bwd_ctas(int sms) { return fa::kNormBwdCtasPerSm * sms; }
 
 template <int D>
 int launch_norm_bwd(fa::NormBwdParams& p, int interleaved, int sms, cudaStream_t stream) {
   constexpr int kTokens = fa::kNormBwdThreads / (D / 16);
   const long long tiles = (p.tokens + kTokens - 1) / kTokens;
-  const long long grid = bwd_ctas(sms), heads = static_cast<long long>(p.heads[0]) + p.heads[1];
-  long long per = tiles * heads / grid;  // few tokens are spread over the SMs whatever the angles cost
-  per = per < 1 ? 1 : (per > kNormBwdHeads ? kNormBwdHeads : per);
-  p.heads_per_item = static_cast<int>(per);
-  const long long items[2] = {tiles * ((p.heads[0] + per - 1) / per), tiles * ((p.heads[1] + per - 1) / per)};
-  const long long all = items[0] + items[1];
+  const long long grid = bwd_ctas(sms);
+  // the line of (token tile, head) of each tensor is cut for its share of the CTAs
+  const long long line[2] = {tiles * p.heads[0], tiles * p.heads[1]}, all = line[0] + line[1];
   long long ctas = all < grid ? all : grid;
-  long long k = items[1] ? (ctas * items[1] + all - 1) / all : 0;  // k's share, q's not empty either
+  long long k = line[1] ? (ctas * line[1] + all - 1) / all : 0;  // k's CTAs, q's not none either
   if (k >= ctas) k = ctas - 1;
   if (all == 0) {  // no tokens: the weights' gradients are zeros
     k = p.heads[1] > 0;
@@ -244,7 +240,7 @@ int launch_norm_bwd(fa::NormBwdParams& p, int interleaved, int sms, cudaStream_t
   const int st = fa_host::launched(interleaved ? cudaLaunchKernelEx(&cfg, fa::fa_norm_bwd_kernel<D, true>, p)
                                                : cudaLaunchKernelEx(&cfg, fa::fa_norm_bwd_kernel<D, false>, p));
   if (st != FA_OK || (!p.dweight[0] && !p.dweight[1])) return st;
-  return fa_host::launch_kernel(fa::fa_norm_bwd_sum_kernel<D>, 2 * (D / 32), 1024, 0, stream, p);
+  return fa_host::launch_kernel(fa::fa_norm_bwd_sum_kernel<D>, 2 * (D / 8), fa::kNormSumThreads, 0, stream, p);
 }
 
 }  // namespace
