@@ -234,7 +234,8 @@ int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_t
     return FA_ERR_SHAPE;
   const int most = budget + slack;
   if (table_out && (out_pages <= 0 || static_cast<long long>(out_pages) * page_size > kMaxKeys ||
-                    static_cast<long long>(out_pages) * page_size < most))
+                    static_cast<long long>(out_pages) * page_size < most ||
+                    (table_out == block_table && out_pages != max_pages)))
     return FA_ERR_SHAPE;
   for (int i = 0; i < 8; ++i)  // page, head and token strides of K, then V; page and head strides of the weights
     if (!stride_ok(strides[i], i < 6 ? 8 : 1)) return FA_ERR_STRIDE;

@@ -57,8 +57,10 @@ __device__ __forceinline__ unsigned weight_order(float w) {
 // counts of a warp met in the same few words.  It ends early where all weights of that
 // digit stay, after two digits as a rule.  Then every warp counts what stays in its
 // part of the list, and after one sum over the warps writes it, in order.
-// Bound: one SM's latency and instructions per head; a thread takes four weights at a
-// time everywhere (a head of 32000: 8 us of loads, 3 us a digit, ...).
+// Bound: one SM's instructions and latency per head, four weights to a thread everywhere.
+// Under a profiler, caches cold: 16 heads of up to 31999 weights 35 us, 128 of up to 8192
+// 15.6, 96 of up to 1024 8.4 (with one weight to a thread 55, 23 and 12).  A bracket from a
+// sample of the weights before the first digit made the first 74 us of 54.
 constexpr int kSelectBins = 2048;
 
 template <int THREADS>
@@ -278,6 +280,9 @@ __global__ void __launch_bounds__(THREADS, 1) fa_evict_select_kernel(const Evict
 // destination lies at or below its own source, it lies below the sources of later
 // rounds, so that one barrier of the cluster stands between a round's loads and its
 // stores and nothing after them.  Into other pages no barrier is needed.
+// Bound: memory; a round in place waits for its loads (a cluster has its rows of the
+// next round looked up meanwhile), which shows where few rows are moved: 128 heads of up to
+// 8192 halved, K and V of 128, 74 us cold, 16 heads of up to 31999 to 8000 into other pages 32.
 constexpr int kMoveThreads = 512;
 
 template <int D>

@@ -129,6 +129,10 @@ __device__ __forceinline__ bool weights_share(const WeightsParams& p, long long*
 // elements in any order as long as both sides agree, so no shuffle, shared memory
 // or barrier stands between load and product.  A warp has 8 KB of K in flight (4 KB where
 // units are few), and the page indices of its next tile are read behind them.
+// Bound: memory, K once and 8 bytes a key.  32 sequences of up to 8192 keys, 8 K/V heads of
+// 128 under 32 query heads: 51.1 us, 5.6 TB/s (58.6 without the pages read ahead, 71 where
+// the compiler may sink K's loads behind those of the old weights); 8 x up to 1024 keys, 12
+// heads of 64: 4.9 us, most of it the launch and three reads in a row (length, page, K).
 constexpr int kWeightThreads = 128;
 template <int M>
 struct WRowsCfg {
@@ -278,9 +282,13 @@ __global__ void __launch_bounds__(kWeightThreads, 3) fa_kv_weights_kernel(const 
 //   warp 18    the rows' tokens and LSE (times -log2 e) beside each S buffer
 //   warp 19    the writer, while the next unit's products run: joins the groups' sums,
 //              sends them to the cluster's first CTA, and there adds all to the old weights
-// 256 keys, because a row block is read from L2 for each of them: at 128 keys the tensor
-// rate would need 15 TB/s of Q (2 x 2048 tokens over 8192, 32/8 heads of 128: 220 us,
-// 6.4 TB/s, however the CTAs were arranged).
+// 256 keys and one CTA to an SM: a row block, once loaded, waited for and described,
+// passes two tiles (2 x 2048 tokens over 8192, 32/8 heads of 128: 169 us, with 128 keys and
+// two CTAs 221; 147 us since a writer has a warp of its own, the units come described
+// and the MMAs are issued with constant indexes).
+// Bound: the products (80 us at the measured tensor rate) and one exponential per key and
+// row, which take turns on two buffers: 0.85 us for a row block and 256 keys, 0.66 of it
+// the products at that rate; a unit's start and end, 4.5 us alone, hide behind eight blocks.
 // With many row blocks the CTAs of a cluster share a unit, so that it is small beside a
 // CTA's share and few keys still reach many SMs.
 // Rows that do not exist, hold no token or have lse = -inf, and keys that some row of the
@@ -337,8 +345,7 @@ __device__ __forceinline__ void copy_to_cta(uint32_t dst, uint32_t src, uint32_t
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// One arrival for the whole warp: those of 128 threads, one after another at the barrier, took longer than the products
-// of a row block.
+// One arrival for the whole warp.
 __device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
@@ -453,8 +460,8 @@ struct WTileUnits {
 
 // The row blocks of a unit that this CTA takes, every (CTAs of the cluster)-th.  With 128 tokens or more a block
 // holds tokens of one query head, of those that see some key of the unit; with fewer it holds rows of several heads,
-// whatever they see.  Found by additions alone: the roles walk over blocks in a few hundred cycles each, and divisions
-// and tests of blocks that no row needs held them up (496 us for 2 x 2048 tokens over 8192).
+// whatever they see.  Found by additions alone: each role walks over the blocks for itself, with a few hundred cycles for
+// one.
 struct WTileBlocks {
   int head, part, left;  // query head of the group (0: blocks over all rows), block in its tokens, blocks to come
   int per;               // blocks of a head

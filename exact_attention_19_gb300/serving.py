@@ -562,7 +562,8 @@ def kv_weights(q, lse, k_cache, weights, block_table, seq_lens, scale: float | N
     query heads of its K/V head and all new tokens.  The new tokens' own keys begin at 0, so a fresh array
     needs no zeros.  ``decay`` 1 leaves keys that no row sees alone, 0 forgets everything before this call (its rows
     may be a prompt's last ones alone).  q, ``lse``, new_lens, window and the cache as given to and returned by
-    ``fwd_paged`` or ``fwd_prefix``; call it once a step.  Runs on ``stream`` (default: the current torch
+    ``fwd_paged`` or ``fwd_prefix``, but that each page belongs to one sequence (of two that share one, one's weights
+    would stay); call it once a step.  Runs on ``stream`` (default: the current torch
     stream), asynchronously; a captured call stays right as the lengths grow.
     """
     if stream is None:
@@ -600,7 +601,8 @@ def kv_evict(k_cache, v_cache, weights, block_table, seq_lens, budget: int, rece
     ``sinks``, the last ``recent``, and of those between the ones with the largest ``weights`` (``kv_weights``; of
     equal ones the lower slots).  They keep their order and move, keys, values and weights, to slots 0 ..
     budget - 1: of their own pages, or, with ``table_out`` (int32 [B, pages], room for budget + slack tokens), of
-    those, to which sequences that keep all their tokens are copied too; block_table's pages may then be shared.
+    those, to which sequences that keep all their tokens are copied too; block_table's pages may then be shared,
+    and table_out names none of them (to stay in place, leave it out).
     In place every page belongs to one sequence, and those past the new length are free afterwards.  Keys keep the
     positions they were turned by; ``shift`` (int32 [B], optional) is increased by the tokens that left, which is
     what ``kv_append(shift=...)`` takes for the next ones.  A window in ``fwd_paged`` counts the kept tokens.

@@ -407,8 +407,10 @@ size_t fa_paged_workspace_bytes(int B, int H, int Hk, int T, int d, int prefix_l
  *           page and head strides of weights (elements, > 0).
  * decay     finite, >= 0.  1: keys that no row sees are left alone.  0: what the
  *           slots held is not read, so every key of the sequence begins anew.
- * Cache, table, lengths and window as in fa_fwd_paged.  Slots past a length, and
- * those of sequences without new tokens, stay as they are.  One call a step: a
+ * Cache, table, lengths and window as in fa_fwd_paged, but that no page may be named
+ * by the keys of two sequences: its weights would be those of one of them (a shared
+ * beginning goes into fa_fwd_prefix's pages).  Slots past a length, and those of
+ * sequences without new tokens, stay as they are.  One call a step: a
  * second one for the same new tokens begins their weights at 0 again.
  * Scores, exponentials and sums in fp32, each key's in a fixed order: results
  * repeat bit for bit.  Errors as fa_fwd_paged (FA_ERR_SCALE for decay too); T == 0
@@ -434,7 +436,8 @@ int fa_kv_weights(const void* q, const float* lse, const void* k_cache, float* w
  *            out_pages * page_size >= budget + slack: they are copied there, and so
  *            are all tokens of a sequence that keeps them all; the pages of
  *            block_table are only read and may be shared, those of table_out
- *            are named once and not by block_table.
+ *            are named once and not by block_table (the same array as block_table:
+ *            in place, with out_pages = max_pages).
  * seq_lens   int32 [B];  lens_out int32 [B] (may be seq_lens): the lengths afterwards.
  * shift      int32 [B] or NULL: increased by the number of tokens that left
  *            (fa_kv_append_norm turns the next tokens by it).

@@ -65,14 +65,16 @@ def call_evict(**kw):
     (dict(B=0), 3), (dict(Hk=0), 3), (dict(n_pages=0), 3), (dict(page_size=24), 3), (dict(max_pages=0), 3),
     (dict(budget=0), 3), (dict(budget=-3), 3), (dict(recent=-1), 3), (dict(sinks=-1), 3), (dict(slack=-1), 3),
     (dict(recent=8), 3), (dict(budget=1 << 30, slack=1), 3), (dict(recent=2 ** 31 - 1, sinks=2 ** 31 - 1), 3),
-    (dict(table_out=FAKE, out_pages=0), 3), (dict(table_out=FAKE, out_pages=1, budget=16, slack=1), 3),
+    (dict(table_out=FAKE + 4, out_pages=0), 3), (dict(table_out=FAKE + 4, out_pages=1, budget=16, slack=1), 3),
+    (dict(table_out=FAKE, out_pages=1), 3), (dict(table_out=FAKE, out_pages=3), 3),  # block_table with rows of another width
     (dict(strides=[64] * 7 + [0]), 13), (dict(strides=[64] * 5 + [12] + [64] * 2), 13)])
 def test_evict_refusals(kw, code):
     assert call_evict(**kw) == code
 
 
 def test_evict_optional_arguments_pass_the_checks():
-    for kw in (dict(), dict(shift=FAKE), dict(table_out=FAKE, out_pages=1, budget=16), dict(recent=7),
+    for kw in (dict(), dict(shift=FAKE), dict(table_out=FAKE + 4, out_pages=1, budget=16), dict(recent=7),
+               dict(table_out=FAKE, out_pages=2),
                dict(strides=[64] * 6 + [1, 1])):
         assert call_evict(**kw) not in (0, 1, 2, 3, 4, 9, 13)
 

@@ -145,6 +145,58 @@ def test_weights(fa, B, H, Hk, T, d, page, lens, new, decay):
     check_weights(fa, c, q, lse, lens, new, decay=decay)
 
 
+@pytest.mark.parametrize("B,H,Hk,T,d,page,lens,new", [
+    (1, 48, 1, 1, 64, 16, [200], None),    # the most rows of the warp-level kernel, and one more
+    (1, 49, 1, 1, 64, 16, [200], None),
+    (2, 24, 2, 4, 128, 32, [300, 70], [4, 3]),
+    (2, 14, 2, 7, 128, 32, [300, 70], [7, 3]),
+    (1, 130, 1, 1, 128, 64, [520], None),  # more heads than a row block holds
+    (4, 8, 8, 1, 128, 64, [2000, 1025, 1, 1999], None),                 # enough units for 32 keys to a warp
+    (8, 8, 8, 2, 64, 128, [2048, 2047, 300, 0, 1, 2, 900, 1300], None),  # and for 64
+    (5, 8, 4, 100, 64, 32, [1100, 100, 1023, 7, 500], [100, 64, 1, 7, 100]),      # many units: a CTA each
+    (3, 16, 1, 130, 128, 16, [700, 131, 300], [130, 100, 129]),         # few: clusters of four
+    (3, 4, 2, 140, 64, 64, [2100, 140, 1000], None),                    # of two
+    (20, 8, 4, 1024, 64, 64, [1024 + 16 * b for b in range(20)], [1024 - 50 * b for b in range(20)]),  # many row blocks
+])
+def test_weights_variants(fa, B, H, Hk, T, d, page, lens, new):
+    c = Cache(B + T, lens, Hk, d, page)
+    q = rand(T, B, H, T, d)
+    check_weights(fa, c, q, lse_of(fa, c, q, lens, new), lens, new, decay=0.5)
+
+
+@pytest.mark.parametrize("T", [1, 60])
+def test_weights_captured_as_the_lengths_grow(fa, T):
+    """One capture, replayed at other lengths of the same cache, some of them empty, on another stream."""
+    B, H, Hk, d, page, width = 3, 8, 2, 64, 16, [900, 400, 64]
+    c = Cache(60, width, Hk, d, page)
+    q = rand(61, B, H, T, d)
+    table, lens, new = c.device_table(), i32([T, T, T]), i32([T, T, T])
+    start = c.w.clone()
+
+    def step():
+        _, lse = fa.fwd_paged(q, c.k, c.v, table, lens, new_lens=new, window=(300, 0))
+        fa.kv_weights(q, lse, c.k, c.w, table, lens, new_lens=new, window=(300, 0), decay=0.5)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for n, m in (([900, 400, 64], [T, T, T]), ([T, 0, 64], [T, 0, 1]), ([880, -3, 63], [max(1, T - 1), T, 0])):
+        c.w.copy_(start)
+        lens.copy_(i32(n))
+        new.copy_(i32(m))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(torch.cuda.Stream()):
+            graph.replay()
+        torch.cuda.synchronize()
+        got = c.w.clone()
+        c.w.copy_(start)
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(got.contiguous()), bits(c.w.contiguous()))
+
+
 @pytest.mark.parametrize("B,H,Hk,T,d,page,lens", [
     (2, 4, 2, 1, 128, 16, [400, 20]), (2, 8, 2, 5, 64, 64, [300, 7]), (1, 4, 4, 200, 64, 32, [450]),
     (1, 8, 1, 150, 128, 128, [777])])
@@ -381,6 +433,32 @@ def test_evict_long_and_many(fa):
     lens = [20 + 3 * b for b in range(90)]
     c = Cache(34, lens, 8, 64, 16)
     check_evict(fa, c, lens, 100, 10, 2, with_shift=False)
+
+
+@pytest.mark.parametrize("fork", [False, True])
+def test_evict_weights_off_the_grid_of_four(fa, fork):
+    """Weights whose pages begin on no 16-byte boundary."""
+    lens = [300, 77]
+    c = Cache(62, lens, 2, 64, 16, more_pages=24)
+    flat = torch.full((c.n_pages * 2 * 19 + 1,), math.nan, device="cuda")
+    w = flat[1:].view(c.n_pages, 2, 19)[..., :16]
+    w.copy_(c.w)
+    c.w = w
+    check_evict(fa, c, lens, 60, 7, 1, fork=fork)
+    q = rand(63, 2, 4, 1, 64)
+    n = [60, 60]
+    if not fork:
+        check_weights(fa, c, q, lse_of(fa, c, q, n, None), n, None, decay=0.5)
+    assert bool(torch.isnan(flat[0])) and bool(torch.isnan(flat[1:].view(c.n_pages, 2, 19)[..., 16:]).all())
+
+
+@pytest.mark.parametrize("fork", [False, True])
+def test_evict_ties_over_windows(fa, fork):
+    """More weights than a CTA holds at once, nearly all of them equal: the lower slots stay; many CTAs to a head's rows."""
+    lens = [50200, 49153]
+    c = Cache(64, lens, 1, 128, 256, more_pages=400 if fork else 0)
+    c.w.copy_((torch.rand(c.w.shape, generator=torch.Generator().manual_seed(65)) < 0.02).float())
+    check_evict(fa, c, lens, 40000, 100, 5, fork=fork)
 
 
 def test_evict_repeats_and_takes_buffers(fa):

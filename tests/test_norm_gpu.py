@@ -129,6 +129,18 @@ def test_norm_rope_backward(fa, B, H, Hk, N, d, rot, interleaved, kind):
     check_bwd(gk, gwk, dk, k, wk, 1e-5, p, w, 1.25, interleaved, "k")
 
 
+@pytest.mark.parametrize("B,H,Hk,N,d", [(1, 700, 3, 1, 64), (1, 1, 1, 1, 128), (3, 5, 2, 700, 64), (2, 40, 40, 129, 128)])
+def test_backward_shares_of_the_heads(fa, B, H, Hk, N, d):
+    """CTAs whose heads begin and end within a tile of tokens, and tiles that two sequences share."""
+    _, (q, k, _) = packed(N, B, N, H, Hk, d)
+    dq, dk = rand(N + 1, B, H, N, d), rand(N + 2, B, Hk, N, d)
+    w, wq, wk = freqs(fa, 64), weights(1, d, torch.float32), weights(2, d, torch.float32)
+    gq, gk, gwq, gwk = fa.norm_rope_bwd(dq, dk, q, k, w, wq, wk, eps=1e-5, offset=3, mag=1.0)
+    p = np.arange(N) + 3
+    check_bwd(gq, gwq, dq, q, wq, 1e-5, p, w, 1.0, False, "q")
+    check_bwd(gk, gwk, dk, k, wk, 1e-5, p, w, 1.0, False, "k")
+
+
 def test_many_tokens_and_one_weight(fa):
     """More items than CTAs, a weight for q alone, positions of packed documents; the results repeat bit for bit."""
     B, H, Hk, N, d, rot = 2, 9, 3, 1501, 128, 64
