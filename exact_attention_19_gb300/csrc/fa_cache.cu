@@ -58,7 +58,8 @@ int ready(int dev) {
   if (!allow(fa::fa_kv_weights_tile_kernel<64>, fa::WTileCfg<64>::kSmemBytes) ||
       !allow(fa::fa_kv_weights_tile_kernel<128>, fa::WTileCfg<128>::kSmemBytes) ||
       !allow(fa::fa_evict_select_kernel<512>, kSelectSmall * sizeof(float)) ||
-      !allow(fa::fa_evict_select_kernel<1024>, kSelectWindow * sizeof(float)))
+      !allow(fa::fa_evict_select_kernel<1024>, kSelectWindow * sizeof(float)) ||
+      !allow(fa::fa_evict_list_kernel, kSelectWindow * sizeof(float)))
     return FA_ERR_LAUNCH;
   g_ready[dev].store(true, std::memory_order_release);
   return FA_OK;
@@ -138,7 +139,49 @@ int launch_move(fa::EvictParams& p, long long heads, int sms, cudaStream_t strea
   return launch_clusters(fa::fa_evict_move_kernel<D>, 3 * heads, p.parts, fa::kMoveThreads, 0, stream, p);
 }
 
-size_t evict_bytes(int B, int Hk) { return static_cast<size_t>(B) * Hk * sizeof(fa::EvictHead); }
+// The workspace: what the selection leaves per head, then what its parts leave for one another.
+// From how many weights of a head (the capacity, times what of it leaves a CTA) the selection goes in parts.  The whole
+// call, into other pages, us with one CTA to a head / in parts: 16384 tokens, 1 head 25 / 26, 16 heads 34 / 39; 32768: 1 head
+// 38 / 27, 8 46 / 42, 16 64 / 60, 32 91 / 93; 65536: 8 heads 109 / 63, 32 197 / 181, 64 327 / 314; 131072: 1 head 151 / 35.
+constexpr long long kSplitWeights = 26 << 10;
+
+struct EvictWorkspace {
+  size_t found, above, hist, bytes;  // offsets of 16 bytes
+  EvictWorkspace(int B, int Hk) {
+    const size_t heads = static_cast<size_t>(B) * Hk, parts = fa::select_parts(static_cast<long long>(heads));
+    found = heads * sizeof(fa::EvictHead);
+    bytes = above = hist = found;
+    if (parts < 2) return;
+    above = found + 2 * heads * sizeof(fa::EvictFound);
+    hist = above + (heads * parts * sizeof(int) + 15) / 16 * 16;
+    bytes = hist + 2 * heads * parts * fa::kSelectBins * sizeof(int);
+  }
+};
+
+int launch_select(fa::EvictParams& p, const EvictWorkspace& at, long long heads, cudaStream_t stream) {
+  const int parts = fa::select_parts(heads);
+  if (parts >= 2 && p.capacity * (parts - 1ll) >= kSplitWeights * parts) {
+    uint8_t* const ws = reinterpret_cast<uint8_t*>(p.heads);
+    p.found = reinterpret_cast<fa::EvictFound*>(ws + at.found);
+    p.above = reinterpret_cast<int*>(ws + at.above);
+    p.hist = reinterpret_cast<int*>(ws + at.hist);
+    p.split = parts;
+    const int part = (p.capacity / parts + 511) & ~255;  // of the longest sequence, not less
+    p.window = part < kSelectWindow ? part : kSelectWindow;
+    const long long grid = heads * parts;
+    constexpr int kT = fa::kSplitThreads;
+    int st = fa_host::launch_kernel(fa::fa_evict_count_kernel<0>, grid, kT, 0, stream, p);
+    if (st == FA_OK) st = fa_host::launch_kernel(fa::fa_evict_count_kernel<1>, grid, kT, 0, stream, p);
+    if (st == FA_OK) st = fa_host::launch_kernel(fa::fa_evict_count_kernel<2>, grid, kT, 0, stream, p);
+    if (st == FA_OK)
+      st = fa_host::launch_kernel(fa::fa_evict_list_kernel, grid, kT, p.window * sizeof(float), stream, p);
+    return st;
+  }
+  p.window = p.capacity < kSelectWindow ? p.capacity : kSelectWindow;
+  const size_t smem = p.window * sizeof(float);
+  return p.window <= kSelectSmall ? fa_host::launch_kernel(fa::fa_evict_select_kernel<512>, heads, 512, smem, stream, p)
+                                  : fa_host::launch_kernel(fa::fa_evict_select_kernel<1024>, heads, 1024, smem, stream, p);
+}
 
 }  // namespace
 
@@ -212,7 +255,7 @@ int fa_kv_weights(const void* q, const float* lse, const void* k_cache, float* w
 }
 
 size_t fa_evict_workspace_bytes(int B, int Hk) {
-  return B > 0 && Hk > 0 && static_cast<long long>(B) * Hk < (1ll << 28) ? evict_bytes(B, Hk) : 0;
+  return B > 0 && Hk > 0 && static_cast<long long>(B) * Hk < (1ll << 28) ? EvictWorkspace(B, Hk).bytes : 0;
 }
 
 int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_table, const int* table_out,
@@ -242,7 +285,8 @@ int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_t
   int dev = -1, sms = 0;
   int st = fa_host::current_device(&dev, &sms);
   if (st != FA_OK) return st;
-  if (workspace_bytes < evict_bytes(B, Hk)) return FA_ERR_WORKSPACE;
+  const EvictWorkspace at(B, Hk);
+  if (workspace_bytes < at.bytes) return FA_ERR_WORKSPACE;
   const void* ptrs[] = {k_cache, v_cache, weights, block_table, seq_lens, lens_out, kept, workspace};
   for (const void* x : ptrs)
     if (!fa_host::is_device_pointer(x, dev)) return FA_ERR_POINTER;
@@ -283,10 +327,7 @@ int fa_kv_evict(void* k_cache, void* v_cache, float* weights, const int* block_t
   st = ready(dev);
   if (st != FA_OK) return st;
   const long long heads = static_cast<long long>(B) * Hk;
-  p.window = p.capacity < kSelectWindow ? p.capacity : kSelectWindow;
-  const size_t smem = p.window * sizeof(float);
-  st = p.window <= kSelectSmall ? fa_host::launch_kernel(fa::fa_evict_select_kernel<512>, heads, 512, smem, stream, p)
-                                : fa_host::launch_kernel(fa::fa_evict_select_kernel<1024>, heads, 1024, smem, stream, p);
+  st = launch_select(p, at, heads, stream);
   if (st != FA_OK) return st;
   return d == 64 ? launch_move<64>(p, heads, sms, stream) : launch_move<128>(p, heads, sms, stream);
 }

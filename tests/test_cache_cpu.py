@@ -80,7 +80,9 @@ def test_evict_optional_arguments_pass_the_checks():
 
 
 def test_evict_workspace_size():
-    assert fa.fa_evict_workspace_bytes(3, 5) == 15 * 16
+    for B, Hk in ((1, 1), (3, 5), (7, 11), (64, 64)):
+        n = fa.fa_evict_workspace_bytes(B, Hk)
+        assert n >= 16 * B * Hk and n <= 16 * B * Hk + (4 << 20)
     for bad in ((0, 1), (1, 0), (1 << 20, 1 << 12)):
         assert fa.fa_evict_workspace_bytes(*bad) == 0
 

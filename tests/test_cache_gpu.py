@@ -461,6 +461,62 @@ def test_evict_ties_over_windows(fa, fork):
     check_evict(fa, c, lens, 40000, 100, 5, fork=fork)
 
 
+@pytest.mark.parametrize("kind,budget,recent,sinks", [
+    ("random", 9000, 500, 7), ("random", 1, 0, 0), ("random", 600, 500, 100), ("random", 32000, 0, 300), ("ties", 9000, 31, 40),
+    ("digit 0", 16000, 0, 0), ("digit 1", 16000, 0, 0), ("digit 2", 16000, 0, 0), ("digit 2", 15999, 0, 0), ("equal", 20000, 3, 2),
+    ("nan", 12000, 100, 0)])
+@pytest.mark.parametrize("fork", [False, True])
+def test_evict_in_parts(fa, kind, budget, recent, sinks, fork):
+    """Few heads of many weights, whose selection several CTAs share: the search ends at every digit, and beside a sequence
+    that keeps all its tokens; the other head's weights are random ones."""
+    lens, page = [32000, min(budget, 300), 40003], 64
+    c = Cache(budget + recent, lens, 2, 64, page, more_pages=3 * (-(-budget // page)) + 20 if fork else 0)
+    g = torch.Generator().manual_seed(66)
+    j = torch.arange(lens[0])
+    w = {"random": torch.randn(lens[0], generator=g).exp(), "ties": torch.randint(0, 9, (lens[0],), generator=g).float(),
+         "digit 0": 2.0 ** (j % 4), "digit 1": 1 + (j % 4) * 2.0 ** -12, "digit 2": 1 + (j % 4) * 2.0 ** -22,
+         "equal": torch.ones(lens[0]),
+         "nan": torch.where(torch.rand(lens[0], generator=g) < 0.5, torch.tensor(math.nan), torch.tensor(-1.0))}[kind]
+    pages = torch.from_numpy(c.table[0]).long()[j // page]
+    c.w[pages.cuda(), 1, (j % page).cuda()] = w.cuda()
+    check_evict(fa, c, lens, budget, recent, sinks, fork=fork)
+
+
+def test_evict_in_parts_bad_pages_unaligned_and_captured(fa):
+    lens, page = [33000, 700], 128
+    c = Cache(67, lens, 1, 64, page)
+    flat = torch.full((c.n_pages * 131 + 1,), math.nan, device="cuda")
+    w = flat[1:].view(c.n_pages, 1, 131)[..., :page]
+    w.copy_(c.w)
+    c.w = w
+    first = [a.clone() for a in (c.k, c.v, c.w)]
+    check_evict(fa, c, lens, 600, 50, 3)
+    want = [bits(a.contiguous()).clone() for a in (c.k, c.v, c.w)]
+    table, n, out = c.device_table(), i32(lens), i32([0, 0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.kv_evict(c.k, c.v, c.w, table, n, 600, recent=50, sinks=3, lens_out=out)
+    for _ in range(3):
+        for a, f in zip((c.k, c.v, c.w), first):
+            a.copy_(f)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(bits(a.contiguous()), x) for a, x in zip((c.k, c.v, c.w), want))
+        assert out.tolist() == [600, 600]
+    fa.fa_fwd_status(None, clear=True)
+    for bad in (-1, c.n_pages, 2 ** 31 - 1, -2 ** 31):
+        for a, f in zip((c.k, c.v, c.w), first):
+            a.copy_(f)
+        t = c.table.copy()
+        t[0, 3] = bad
+        _, kept = fa.kv_evict(c.k, c.v, c.w, torch.from_numpy(t).cuda(), n, 600, recent=50, sinks=3)
+        assert fa.fa_fwd_status(None, clear=True) == (12, 2)
+        k = kept[0, 0].cpu().numpy()
+        assert np.all((k >= 0) & (k < lens[0])) and np.all(np.diff(k) > 0)
+        for p in c.table[1]:
+            assert all(torch.equal(bits(a[p]), x[p]) for a, x in zip((c.k, c.v, c.w), want) if p >= 0)
+
+
 def test_evict_repeats_and_takes_buffers(fa):
     lens = [400, 90]
     first = None
