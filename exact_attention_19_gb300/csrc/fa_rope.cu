@@ -28,7 +28,11 @@ fa::RopeView contiguous(int heads, int n, int d) {
 // several heads; but enough CTAs are wanted that the last wave of them is short
 // (3 x 4099 tokens, 32 heads: 33.5 us with 4 heads, 34.0 with 8, 41.2 with 16;
 // 2 x 2000 of 40: 13.9, 13.2, 12.8, with 2 it takes 16.4).  Few
-// tokens are spread over the SMs whatever the angles cost.
+// tokens are spread over the SMs whatever the angles cost.  The append with the norm, whose
+// CTAs have more to begin with (the weights too) and more heads in flight, takes as many
+// heads as leave the least number of CTAs: with that / with kCtasPerSm, 32 + 2 x 8 heads of
+// 128, 4 x 2048 tokens 36.8 / 40.0 us, of 1 .. 2048 19.5 / 23.0, 2 x 8192 67.8 / 68.4, 32768
+// 130 / 127; 12 + 2 x 12 of 64, 4 x 2048 11.9 / 15.1.
 constexpr long long kCtasPerSm = 24;
 constexpr long long kLeastHeads = 4;
 constexpr long long kLeastCtasPerSm = 4;
@@ -38,7 +42,7 @@ int launch(fa::RopeParams& p, int interleaved, int sms, cudaStream_t stream) {
   constexpr int kTokens = fa::kRopeThreads / (D / 16);
   const long long tiles = (p.tokens + kTokens - 1) / kTokens;
   const long long heads = static_cast<long long>(p.heads[0]) + p.heads[1] + (PAGED ? p.heads[2] : 0);
-  long long groups = (kCtasPerSm * sms + tiles - 1) / tiles;
+  long long groups = NORM && PAGED ? 0 : (kCtasPerSm * sms + tiles - 1) / tiles;
   if (groups > heads / kLeastHeads) groups = heads / kLeastHeads;
   const long long least = (kLeastCtasPerSm * sms + tiles - 1) / tiles;
   if (groups < least) groups = least;

@@ -25,7 +25,8 @@
 // copy rate; 3 x 4099 tokens, 16 + 16 heads (201 MB), 33.3 us, 89% (one and a
 // half waves of CTAs); a call of 256 tokens 2.9 us, its launch.  Appending 4 x up
 // to 2048 tokens, 32 + 2 x 8 heads (115 MB): 22.0 us, 77% (the page's index comes
-// before the first store).
+// before the first store).  With the norm: 4 x 8192 tokens 108.6 us, 6.2 TB/s, the
+// append 25.3 us, 68% (a head's sum stands between its loads and its stores).
 #pragma once
 
 #include <cstdint>
@@ -292,8 +293,9 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
     if constexpr (NORM)
       if (t < 2) load_weight16(p.weight[t], p.weight_f32, c0, c1, weight);
     // heads in flight, two loads of 16 bytes each (4 x 2048 appended: 22.0 us with 2, 24.1 with 4; 4 x 8192
-    // rotated: 103.6 with 2, 102.5 with 4)
-    constexpr int kU = PAGED ? 2 : 4;
+    // rotated: 103.6 with 2, 102.5 with 4; 4 x 1 .. 2048 appended with the norm: 28.7 with 2, 26.6 with 3, 25.6 with
+    // 4, 25.3 with 6, 31.5 with 8)
+    constexpr int kU = !PAGED ? 4 : (NORM ? 6 : 2);
     for (int h = lo; h < hi; h += kU) {
       uint4 a[kU], e[kU];
 #pragma unroll
