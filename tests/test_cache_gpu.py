@@ -461,6 +461,17 @@ def test_evict_ties_over_windows(fa, fork):
     check_evict(fa, c, lens, 40000, 100, 5, fork=fork)
 
 
+@pytest.mark.parametrize("ties", [False, True])
+@pytest.mark.parametrize("fork", [False, True])
+def test_evict_long_beside_many_short(fa, fork, ties):
+    """Too many heads for several CTAs each, and one with more weights than a CTA holds at once."""
+    lens = [50001] + [20 + b for b in range(80)]
+    c = Cache(68, lens, 1, 64, 256, more_pages=120 if fork else 0)
+    if ties:
+        c.w.copy_((torch.rand(c.w.shape, generator=torch.Generator().manual_seed(69)) < 0.02).float())
+    check_evict(fa, c, lens, 9000, 100, 5, fork=fork)
+
+
 @pytest.mark.parametrize("kind,budget,recent,sinks", [
     ("random", 9000, 500, 7), ("random", 1, 0, 0), ("random", 600, 500, 100), ("random", 32000, 0, 300), ("ties", 9000, 31, 40),
     ("digit 0", 16000, 0, 0), ("digit 1", 16000, 0, 0), ("digit 2", 16000, 0, 0), ("digit 2", 15999, 0, 0), ("equal", 20000, 3, 2),
