@@ -91,7 +91,7 @@ int launch_clusters(K kernel, long long clusters, int cluster, int threads, size
 constexpr int kWarpRows = 48;
 
 template <int D>
-int launch_weights(const fa::WeightsParams& p, long long all_rows, int page_size, int sms, cudaStream_t stream) {
+int launch_weights(fa::WeightsParams& p, long long all_rows, int page_size, int sms, cudaStream_t stream) {
   if (p.s.rows <= kWarpRows) {
     // 8 KB of K to a warp, or where those units are fewer than the places (by the table's width) 4 KB
     constexpr int kM = 256 / D;
@@ -120,6 +120,9 @@ int launch_weights(const fa::WeightsParams& p, long long all_rows, int page_size
   else if (blocks >= 2 && 2 * units <= sms) cluster = 2;
   long long grid = sms / cluster;
   if (grid > units) grid = units;
+  // units that a CTA works long on are given out one by one: by the number of clusters, and by the rows, which the lengths
+  // on the device may yet leave too few of
+  p.uneven = blocks >= 20 * cluster && grid <= 32 * fa::WTileUnits::kMost;
   return launch_clusters(fa::fa_kv_weights_tile_kernel<D>, grid, cluster, C::kThreads, C::kSmemBytes, stream, mk, mq, p);
 }
 

@@ -22,6 +22,7 @@ struct WeightsParams {
   long long w_page, w_head;
   float decay;           // 1: keys that no row sees are left alone; 0: old values are not read
   int group;                // query heads of a K/V head
+  int uneven;               // units differ by many row blocks: given out by what each cluster has to do
   unsigned t_mul, t_shift;  // r / T = r * t_mul >> 32 + t_shift for the rows r < 2^31 (T > 1)
 };
 // Query head (in its group) of row r.
@@ -282,10 +283,12 @@ __global__ void __launch_bounds__(kWeightThreads, 3) fa_kv_weights_kernel(const 
 //   warp 18    the rows' tokens and LSE (times -log2 e) beside each S buffer
 //   warp 19    the writer, while the next unit's products run: joins the groups' sums,
 //              sends them to the cluster's first CTA, and there adds all to the old weights
+//              before and after that it finds the cluster's units and describes them, a few ahead
 // 256 keys and one CTA to an SM: a row block, once loaded, waited for and described,
 // passes two tiles (2 x 2048 tokens over 8192, 32/8 heads of 128: 169 us, with 128 keys and
 // two CTAs 221; 147 us since a writer has a warp of its own, the units come described
-// and the MMAs are issued with constant indexes).
+// and the MMAs are issued with constant indexes, 141 since long units are given out by
+// what each cluster has to do).
 // Bound: the products (80 us at the measured tensor rate) and one exponential per key and
 // row, which take turns on two buffers: 0.85 us for a row block and 256 keys, 0.66 of it
 // the products at that rate; a unit's start and end, 4.5 us alone, hide behind eight blocks.
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(kWeightThreads, 3) fa_kv_weights_kernel(const 
 // Rows that do not exist, hold no token or have lse = -inf, and keys that some row of the
 // block does not see, are masked element by element (their Q may hold anything): a key
 // is seen by an interval of tokens.  A block without any takes the path without masks.
-// A unit, as the producer describes it to the other warps.
+// A unit, as the writer describes it to all warps.
 struct __align__(16) WTileUnit {
   int b, hk, k0, k1;   // keys [k0, k1) of a sequence and K/V head
   int len, fresh, lo;  // the sequence's tokens, new ones, first key whose weight changes
@@ -319,7 +322,7 @@ struct WTileCfg {
   static constexpr uint32_t kSumBytes = kUnit * 4;
   static constexpr uint32_t kJoinOff = kSideOff + 2 * kSideBytes;  // [2 units] sums of two groups, of each other CTA
   static constexpr uint32_t kJoinBytes = (2 + kMaxCluster - 1) * kSumBytes;
-  static constexpr int kUnits = 4;  // descriptions of units
+  static constexpr int kUnits = 8;  // descriptions of units
   static constexpr uint32_t kUnitOff = kJoinOff + 2 * kJoinBytes;
   static constexpr uint32_t kBarOff = kUnitOff + kUnits * sizeof(WTileUnit);
   static constexpr uint32_t kTmemSlot = kBarOff + (16 + 2 * kRing + 2 * kUnits + 1) * 8;
@@ -394,22 +397,116 @@ __device__ __forceinline__ void key_tokens(const WeightsParams& p, int len, int 
   tb = static_cast<int>(max(b, 0ll));
 }
 
-// The units of a cluster: its number and every (number of clusters)-th after it, 32 at a time, one to a lane of a whole
-// converged warp.
+// The units of a cluster, in a whole converged warp that describes 32 at a time, one to a lane.  Short units: its
+// number and every (number of clusters)-th after it.  Long ones differ by whole sequences' row blocks, and a cluster has
+// few of them, so each goes to the cluster that has least to do so far; every cluster finds the same assignment for
+// itself, beside the products of its units (about 0.09 us for each unit of the call).  32/8 heads of 128, us so / in turn:
+// 2 x up to 2048 tokens over 8192 115 / 132, another two 141 / 149, prompts of 4 x up to 4096 (64 heads) 279 / 348, one of
+// 8192 271 / 324; where units are shorter, 4 x up to 1024 over 8192 141 / 132, 8 x up to 512 over 4096 132 / 89.
 struct WTileUnits {
-  WTileUnit mine;   // of this lane
-  long long u;      // its number
-  int b_from;       // sequences before it are behind all units to come
-  long long first;  // first unit of that one
-  __device__ __forceinline__ void begin(const WeightsParams& p) {
+  static constexpr int kMost = 3;  // clusters of a lane: 96 of a launch
+  WTileUnit mine;      // of this lane
+  long long u;         // its number
+  int b_from;          // sequences before it are behind all units to come
+  long long first;     // first unit of that one
+  int at;              // lane of the next unit
+  int cluster, clusters;
+  bool uneven;
+  unsigned cost;         // of this lane's unit
+  unsigned load[kMost];  // of clusters lane, lane + 32, ...: blocks, and the number in the low 8 bits
+  __device__ __forceinline__ void copy(WTileUnit& v, int lane) const {
+    const int* const from = reinterpret_cast<const int*>(&mine);
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(WTileUnit) / 4); ++i)
+      reinterpret_cast<int*>(&v)[i] = __shfl_sync(0xffffffffu, from[i], lane);
+  }
+  // What this lane's unit keeps a CTA busy for, in row blocks above the cluster's number (its ends count for two); 0: none.
+  __device__ __forceinline__ void weigh(const WeightsParams& p) {
+    const int blocks = mine.tb <= mine.ta ? 0
+                       : p.s.T >= 128     ? (mine.tb - mine.ta + 127) / 128 * p.group
+                                          : (p.s.rows + 127) / 128;
+    const int ranks = static_cast<int>(cluster_size());
+    const int each = ranks == 1 ? blocks : (ranks == 2 ? (blocks + 1) >> 1 : (blocks + 3) >> 2);
+    cost = mine.last ? 0u : static_cast<unsigned>(min(each, 1 << 14) + 2) << 8;
+  }
+  // Whether units keep a CTA busy for 20 row blocks and more on average (17 us; the search for one 7 us).
+  __device__ __forceinline__ bool long_units(const WeightsParams& p) const {
+    long long more = 0;
+    for (int b = threadIdx.x & 31; b < p.s.B; b += 32) {
+      const SeqKeys s = weight_keys(p, b);
+      const long long each = static_cast<long long>((s.fresh + 127) / 128) * p.group - 20 * cluster_size();
+      more += (tiles_of(s.lo, s.hi, kWeightTile) + 1) / 2 * each;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) more += __shfl_xor_sync(0xffffffffu, more, o);
+    return more >= 0;
+  }
+  // The first unit into v.
+  __device__ __forceinline__ void begin(const WeightsParams& p, WTileUnit& v) {
+    const int lane = threadIdx.x & 31;
+    uneven = p.uneven && long_units(p);
+    cluster = static_cast<int>(blockIdx.x / cluster_size());
+    clusters = static_cast<int>(gridDim.x / cluster_size());
     b_from = 0;
     first = 0;
-    u = blockIdx.x / cluster_size() + static_cast<long long>(threadIdx.x & 31) * (gridDim.x / cluster_size());
-    fill(p);
+    if (!uneven) {
+      u = cluster + static_cast<long long>(lane) * clusters;
+      fill(p);
+      copy(v, 0);
+      at = 1;
+      return;
+    }
+    // nobody has anything to do: unit i goes to cluster i
+#pragma unroll
+    for (int r = 0; r < kMost; ++r) {
+      const int c = 32 * r + lane;
+      load[r] = 0xffffffffu;
+      if (32 * r >= clusters) continue;
+      u = min(c, clusters - 1);
+      fill(p);
+      weigh(p);
+      if (c < clusters) load[r] = cost | static_cast<unsigned>(c);
+      if (cluster / 32 == r) copy(v, cluster % 32);
+    }
+    u = clusters + lane - 32;
+    at = 32;
   }
-  __device__ __forceinline__ void more(const WeightsParams& p) {
-    u += 32ll * (gridDim.x / cluster_size());
-    fill(p);
+  // The next one into v.
+  __device__ __forceinline__ void next(const WeightsParams& p, WTileUnit& v) {
+    for (;;) {
+      if (at == 32) {
+        u += uneven ? 32 : 32ll * clusters;
+        fill(p);
+        at = 0;
+        if (uneven) {  // only differences count
+          weigh(p);
+          unsigned least = 0xffffffffu;
+#pragma unroll
+          for (int r = 0; r < kMost; ++r) least = min(least, load[r]);
+          least = __reduce_min_sync(0xffffffffu, least) & ~0xffu;
+#pragma unroll
+          for (int r = 0; r < kMost; ++r)
+            if (load[r] != 0xffffffffu) load[r] -= least;
+        }
+      }
+      const int j = at++;
+      const unsigned more = uneven ? __shfl_sync(0xffffffffu, cost, j) : 0u;
+      if (more == 0) {
+        copy(v, j);
+        return;
+      }
+      unsigned least = 0xffffffffu;
+#pragma unroll
+      for (int r = 0; r < kMost; ++r) least = min(least, load[r]);
+      least = __reduce_min_sync(0xffffffffu, least);
+#pragma unroll
+      for (int r = 0; r < kMost; ++r)
+        if (load[r] == least) load[r] += more;
+      if (static_cast<int>(least & 0xffu) == cluster) {
+        copy(v, j);
+        return;
+      }
+    }
   }
   __device__ __forceinline__ void fill(const WeightsParams& p) {
     const int lane = threadIdx.x & 31;
@@ -550,7 +647,7 @@ __global__ void __launch_bounds__(WTileCfg<D>::kThreads, 1)
     }
     for (int i = 0; i < C::kUnits; ++i) {
       mbar_init(unit_full(i), 1);
-      mbar_init(unit_free(i), C::kThreads / 32 - 1);
+      mbar_init(unit_free(i), C::kThreads / 32);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -580,16 +677,17 @@ __global__ void __launch_bounds__(WTileCfg<D>::kThreads, 1)
   WTileUnit w = {};
   int units_read = 0;
   bool ok = true;
-  // the next unit, for the warps that the producer describes it to; false: none, or a wait gave up
-  auto next_unit = [&]() -> bool {
+  // the next unit as the writer described it; false: none, or a wait gave up
+  auto read_unit = [&](WTileUnit& v) -> bool {
     const int i = units_read % C::kUnits;
     ok = uniform(mbar_wait(unit_full(i), (units_read / C::kUnits) & 1, abort_flag));
     if (!ok) return false;
     ++units_read;
-    w = units[i];
+    v = units[i];
     mbar_arrive_warp(unit_free(i));
-    return !w.last;
+    return !v.last;
   };
+  auto next_unit = [&]() -> bool { return read_unit(w); };
 
   if (warp == C::kWarpProd) {
     // ======================= TMA producer =================================
@@ -616,38 +714,25 @@ __global__ void __launch_bounds__(WTileCfg<D>::kThreads, 1)
                  ? coherent(p.s.table + static_cast<long long>(v.b) * p.s.max_pages + (key_of(v, tile) >> p.s.page_shift))
                  : -1;
     };
-    WTileUnits list;
-    list.begin(p);
-    int told = 0;
-    auto tell = [&](WTileUnit& v) {  // the next unit, described to the other warps too
-      if (told > 0 && told % 32 == 0) list.more(p);
-      const int* const mine = reinterpret_cast<const int*>(&list.mine);
-#pragma unroll
-      for (int i = 0; i < static_cast<int>(sizeof(WTileUnit) / 4); ++i)
-        reinterpret_cast<int*>(&v)[i] = __shfl_sync(0xffffffffu, mine[i], told % 32);
-      const int i = told % C::kUnits;
-      ok = uniform(mbar_wait(unit_free(i), ((told / C::kUnits) & 1) ^ 1u, abort_flag));
-      if (!ok) return;
-      if (lane == 0) units[i] = v;
-      mbar_arrive_warp(unit_full(i));
-      ++told;
-    };
-    tell(w);
     int page[2] = {-1, -1};
-    if (ok && !w.last) {
+    if (next_unit()) {
       page[0] = page_of(w, 0);
       page[1] = page_of(w, 1);
     }
     while (ok && !w.last) {
-      // the next unit's pages are read, and its K brought to L2, while this one's row blocks are loaded
+      // the next unit's pages are read, and its K brought to L2, while this one's row blocks are loaded; where finding it
+      // takes long, not before some of them
       WTileUnit v;
-      tell(v);
-      if (!ok) break;
-      int next_page[2] = {-1, -1};
-      if (!v.last) {
+      int next_page[2] = {-1, -1}, wait = p.uneven ? min(8, max(WTileBlocks(p, w).count() - 1, 0)) : 0;
+      auto look = [&]() {
+        if (!read_unit(v)) return;
         next_page[0] = page_of(v, 0);
         next_page[1] = page_of(v, 1);
-      }
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile)
+          if (static_cast<unsigned>(next_page[tile]) < static_cast<unsigned>(p.s.n_pages))
+            tma_prefetch_4d(&tmK, x * 64, key_of(v, tile) & ((1 << p.s.page_shift) - 1), v.hk, next_page[tile]);
+      };
       int k_slot[2] = {-1, -1};
       for (WTileBlocks at(p, w); at; at.step()) {
         if (k_slot[0] < 0) {
@@ -667,11 +752,9 @@ __global__ void __launch_bounds__(WTileCfg<D>::kThreads, 1)
                           key_of(w, tile) & ((1 << p.s.page_shift) - 1), w.hk, page[tile]);
           }
           if (!ok) break;
-#pragma unroll
-          for (int tile = 0; tile < 2; ++tile)
-            if (static_cast<unsigned>(next_page[tile]) < static_cast<unsigned>(p.s.n_pages))
-              tma_prefetch_4d(&tmK, x * 64, key_of(v, tile) & ((1 << p.s.page_shift) - 1), v.hk, next_page[tile]);
         }
+        if (wait-- == 0) look();
+        if (!ok) break;
         const int s = take();
         if (!ok) break;
         const int pieces = (at.rows() + C::kPiece - 1) / C::kPiece;
@@ -685,6 +768,7 @@ __global__ void __launch_bounds__(WTileCfg<D>::kThreads, 1)
 #pragma unroll
       for (int tile = 0; tile < 2; ++tile)
         if (k_slot[tile] >= 0) slots.give(k_slot[tile]);
+      if (ok && wait >= 0) look();
       w = v;
       page[0] = next_page[0];
       page[1] = next_page[1];
@@ -817,9 +901,26 @@ __global__ void __launch_bounds__(WTileCfg<D>::kThreads, 1)
     }
     if (!ok) failed(32u);
   } else if (warp > C::kWarpSide) {
-    // ======================= writer =======================================
+    // ======================= writer, planner ===============================
+    WTileUnits list;
+    WTileUnit plan;
+    int told = 0;
+    auto tell = [&]() {  // one more unit, described to all warps; the last one says that there is none
+      if (told == 0) list.begin(p, plan);
+      else if (!plan.last) list.next(p, plan);
+      else return;
+      const int i = told % C::kUnits;
+      ok = uniform(mbar_wait(unit_free(i), ((told / C::kUnits) & 1) ^ 1u, abort_flag));
+      if (!ok) return;
+      if (lane == 0) units[i] = plan;
+      mbar_arrive_warp(unit_full(i));
+      ++told;
+    };
+    // so many before the first sums are waited for: where finding one takes long, only as many as the rest needs
+    tell();
+    for (int i = list.uneven ? 2 : C::kUnits - 2; i > 0 && ok; --i) tell();
     int unit = 0;
-    while (next_unit()) {
+    while (ok && next_unit()) {
       float* to[8];
       float old[8];
 #pragma unroll
@@ -871,6 +972,7 @@ __global__ void __launch_bounds__(WTileCfg<D>::kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         if (to[i]) *to[i] = old[i] + v[i];
+      tell();
     }
     if (!ok) failed(8u);
   } else {

@@ -156,6 +156,9 @@ def test_weights(fa, B, H, Hk, T, d, page, lens, new, decay):
     (5, 8, 4, 100, 64, 32, [1100, 100, 1023, 7, 500], [100, 64, 1, 7, 100]),      # many units: a CTA each
     (3, 16, 1, 130, 128, 16, [700, 131, 300], [130, 100, 129]),         # few: clusters of four
     (3, 4, 2, 140, 64, 64, [2100, 140, 1000], None),                    # of two
+    (3, 8, 2, 1300, 64, 64, [4000, 3500, 3777], [1300, 1290, 1281]),    # units given out by what each cluster has to do
+    (3, 8, 2, 1300, 128, 64, [4000, 3500, 1300], [1300, 5, 1]),         # too few rows for that
+    (1, 8, 1, 1300, 64, 128, [4000], None),                             # the same, clusters of four
     (20, 8, 4, 1024, 64, 64, [1024 + 16 * b for b in range(20)], [1024 - 50 * b for b in range(20)]),  # many row blocks
 ])
 def test_weights_variants(fa, B, H, Hk, T, d, page, lens, new):
