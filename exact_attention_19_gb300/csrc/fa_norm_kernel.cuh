@@ -12,16 +12,17 @@
 // Bound: memory, 6 bytes per element (x and dy read, dx written, bf16); then, with
 // 16 warps to an SM, the way from a head's loads through its two sums to its
 // stores.  Threads hold the elements that fa_rope_kernel's do (16 of a head, so its
-// sums are D / 16 lanes', both in one pass), two heads' loads in flight, and a CTA
-// walks over an equal share of the line of (token tile, head) of q or of k with
-// the 16 weight gradients of its elements in registers: they leave once, D sums
-// per CTA, which a second kernel adds in the order of the CTAs (no atomics:
-// results repeat bit for bit on one GPU).  Measured with the second kernel: 3 x 4099
-// tokens of 16 + 16 heads at d = 128, half turned, 62.0 us (4.87 TB/s; 66 with whole items of
-// 8 heads strided over the CTAs, which leave a last round one in twenty full), 8 x 1024
-// of 12 + 12 at d = 64, 23.5 us.  Slower: five CTAs to an SM (80 and 29 us: 96
-// registers spill), one head in flight (67 and 24.6), x and dy through shared memory
-// by asynchronous copies two to four heads ahead (82 and 20.6).
+// sums are D / 16 lanes', both in one pass), two heads' loads in flight, their angles
+// in shared memory, and a CTA walks over an equal share of the line of (token tile, head)
+// of q or of k with the 16 weight gradients of its elements in registers: they leave
+// once, D sums per CTA, which a second kernel adds in the order of the CTAs (no
+// atomics: results repeat bit for bit on one GPU).  Measured with the second kernel:
+// 3 x 4099 tokens of 16 + 16 heads at d = 128, half turned, 59.9 us (5.0 TB/s), 8 x 1024
+// of 12 + 12 at d = 64, 22.8 us.  Slower: angles in registers (61.7 and 23.2), three CTAs
+// to an SM (with four heads in flight 59.8 and 24.5) or five (72 and 26.9; 80 and 29 with
+// angles in registers, which spill), one head in flight (67 and 24.6), whole items of 8
+// heads strided over the CTAs (66 and 24.4), x and dy through shared memory by
+// asynchronous copies two to four heads ahead (82 and 20.6).
 #pragma once
 
 #include "fa_rope_kernel.cuh"
@@ -49,6 +50,13 @@ struct NormBwdParams {
 constexpr int kNormBwdThreads = 128;
 constexpr int kNormBwdCtasPerSm = 4;
 
+// Loaded again for each head, so that they hold no registers between.
+__device__ __forceinline__ void own_angles(const float4* at, float* v) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(at))));
+}
+
 template <int D, bool INTERLEAVED>
 __global__ void __launch_bounds__(kNormBwdThreads, kNormBwdCtasPerSm) fa_norm_bwd_kernel(const NormBwdParams p) {
   constexpr int kUnits = D / 16;  // threads per token
@@ -56,6 +64,7 @@ __global__ void __launch_bounds__(kNormBwdThreads, kNormBwdCtasPerSm) fa_norm_bw
   constexpr int kU = 2;  // heads in flight, four loads of 16 bytes each
   __shared__ unsigned long long freq[D / 2];
   __shared__ float sums[kNormBwdThreads / 32][D];
+  __shared__ float4 angles[4][kNormBwdThreads];  // each thread's 8 cosines and sines
   __shared__ float4 weights[4][kUnits];  // elements 4 q .. of the 16 that each unit of a token holds
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the sum over CTAs waits for this grid's end
   const int t = static_cast<int>(blockIdx.x) < p.ctas[0] ? 0 : 1;
@@ -92,8 +101,8 @@ __global__ void __launch_bounds__(kNormBwdThreads, kNormBwdCtasPerSm) fa_norm_bw
     const long long tok = tile * kTokens + threadIdx.x / kUnits;
     if (tok >= p.tokens) continue;
     const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok - static_cast<long long>(b) * p.N);
-    float c[8], s[8];
     if (turns) {
+      float c[8], s[8];
       const unsigned long long pos =
           static_cast<unsigned long long>(p.offset) + (p.positions ? p.positions[b * p.pos_stride + n] : n);
 #pragma unroll
@@ -103,6 +112,11 @@ __global__ void __launch_bounds__(kNormBwdThreads, kNormBwdCtasPerSm) fa_norm_bw
         if (broken && !finite(__ldg(p.inv_freq + 8 * u + i))) cs = sn = __int_as_float(0x7fffffff);
         c[i] = cs * p.mag;
         s[i] = sn * -p.mag;
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        angles[q][threadIdx.x] = make_float4(c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]);
+        angles[2 + q][threadIdx.x] = make_float4(s[4 * q], s[4 * q + 1], s[4 * q + 2], s[4 * q + 3]);
       }
     }
     const uint16_t* dy = p.dy[t] + b * p.dy_s[t].b + n * p.dy_s[t].n + h_lo * p.dy_s[t].h;
@@ -126,7 +140,15 @@ __global__ void __launch_bounds__(kNormBwdThreads, kNormBwdCtasPerSm) fa_norm_bw
           float g[16], v[16];
           unpack16(ga[i], ge[i], g);
           unpack16(xa[i], xe[i], v);
-          if (turns) rotate16<INTERLEAVED>(g, c, s);
+          if (turns) {
+            float c[8], s[8];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              own_angles(&angles[q][threadIdx.x], c + 4 * q);
+              own_angles(&angles[2 + q][threadIdx.x], s + 4 * q);
+            }
+            rotate16<INTERLEAVED>(g, c, s);
+          }
           // both sums over the head at once: of x^2, and of g w x, which r makes that of g w n
           float ss0 = 0.f, ss1 = 0.f, dot0 = 0.f, dot1 = 0.f;
 #pragma unroll
