@@ -846,10 +846,12 @@ __global__ void __launch_bounds__(WTileCfg<D>::kThreads, 1)
     uniform(mbar_wait(drain, 0, nullptr));
   } else if (warp == C::kWarpSide) {
     // ======================= LSE and tokens of the rows ====================
+    // A block is handed over before the next one is looked for: units without blocks may lie between, more of them than
+    // the writer describes ahead of this block's unit, whose sums wait for it.
     int block = 0;
     bool more = next_unit();
     WTileBlocks at(p, w);
-    float l2[4];  // LSE of the block's rows, read a block ahead
+    float l2[4];  // LSE of the block's rows, on their way while the S buffer is waited for
     auto seek = [&]() {
       while (more && !at) {
         more = next_unit();
@@ -883,8 +885,6 @@ __global__ void __launch_bounds__(WTileCfg<D>::kThreads, 1)
         l[i] = l2[i] * -1.44269504f;
       }
       cut = !uniform(!cut);
-      at.step();
-      seek();
       const uint32_t ph = ((block >> 1) & 1) ^ 1u;
       ok = ok && uniform(mbar_wait(s_free(buf, 0), ph, abort_flag) && mbar_wait(s_free(buf, 1), ph, abort_flag));
       if (!ok) break;
@@ -898,6 +898,8 @@ __global__ void __launch_bounds__(WTileCfg<D>::kThreads, 1)
       mbar_arrive_warp(s_full(buf, 0));
       mbar_arrive_warp(s_full(buf, 1));
       ++block;
+      at.step();
+      seek();
     }
     if (!ok) failed(32u);
   } else if (warp > C::kWarpSide) {
