@@ -31,12 +31,15 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
 // Loads that stay where they stand: left to itself the compiler puts them behind waits that they are to overlap.
 __device__ __forceinline__ uint4 load16(const uint16_t* at) {
   uint4 v;
-  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(at));
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(at)
+               : "memory");
   return v;
 }
 __device__ __forceinline__ float load4(const float* at) {
   float v;
-  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(at));
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(at) : "memory");
   return v;
 }
 

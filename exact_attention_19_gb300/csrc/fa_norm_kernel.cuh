@@ -54,7 +54,8 @@ constexpr int kNormBwdCtasPerSm = 4;
 __device__ __forceinline__ void own_angles(const float4* at, float* v) {
   asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(at))));
+               : "r"(static_cast<unsigned>(__cvta_generic_to_shared(at)))
+               : "memory");
 }
 
 template <int D, bool INTERLEAVED>
