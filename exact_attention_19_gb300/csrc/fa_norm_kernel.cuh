@@ -58,7 +58,7 @@ __device__ __forceinline__ void own_angles(const float4* at, float* v) {
                : "memory");
 }
 
-template <int D, bool INTERLEAVED>
+template <int D, bool INTERLEAVED, int NORM>
 __global__ void __launch_bounds__(kNormBwdThreads, kNormBwdCtasPerSm) fa_norm_bwd_kernel(const NormBwdParams p) {
   constexpr int kUnits = D / 16;  // threads per token
   constexpr int kTokens = kNormBwdThreads / kUnits;
@@ -151,21 +151,34 @@ __global__ void __launch_bounds__(kNormBwdThreads, kNormBwdCtasPerSm) fa_norm_bw
             rotate16<INTERLEAVED>(g, c, s);
           }
           // both sums over the head at once: of x^2, and of g w x, which r makes that of g w n
-          float ss0 = 0.f, ss1 = 0.f, dot0 = 0.f, dot1 = 0.f;
+          float ss0, ss1, dot0, dot1, scale = 1.f;
+          auto sums = [&]() {
+            ss0 = ss1 = dot0 = dot1 = 0.f;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 w = weights[q][u];
-            const int j = 4 * q;
-            ss0 = fmaf(v[j], v[j], ss0);
-            ss1 = fmaf(v[j + 1], v[j + 1], ss1);
-            ss0 = fmaf(v[j + 2], v[j + 2], ss0);
-            ss1 = fmaf(v[j + 3], v[j + 3], ss1);
-            dot0 = fmaf(g[j] * w.x, v[j], dot0);
-            dot1 = fmaf(g[j + 1] * w.y, v[j + 1], dot1);
-            dot0 = fmaf(g[j + 2] * w.z, v[j + 2], dot0);
-            dot1 = fmaf(g[j + 3] * w.w, v[j + 3], dot1);
-          }
-          const float r = rsqrtf(fmaf(head_sum<kUnits>(ss0 + ss1), 1.f / D, p.eps));
+            for (int q = 0; q < 4; ++q) {
+              const float4 w = weights[q][u];
+              const int j = 4 * q;
+              ss0 = fmaf(v[j], v[j], ss0);
+              ss1 = fmaf(v[j + 1], v[j + 1], ss1);
+              ss0 = fmaf(v[j + 2], v[j + 2], ss0);
+              ss1 = fmaf(v[j + 3], v[j + 3], ss1);
+              dot0 = fmaf(g[j] * w.x, v[j], dot0);
+              dot1 = fmaf(g[j + 1] * w.y, v[j + 1], dot1);
+              dot0 = fmaf(g[j + 2] * w.z, v[j + 2], dot0);
+              dot1 = fmaf(g[j + 3] * w.w, v[j + 3], dot1);
+            }
+          };
+          sums();
+          float m = fmaf(head_sum<kUnits>(ss0 + ss1), 1.f / D, p.eps);
+          if constexpr (NORM == kNormAnySize)
+            if (!plain_mean(m)) {  // n and dw do not see the scale, dx takes it at the end
+              scale = head_scale(m);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] *= scale;
+              sums();
+              m = fmaf(head_sum<kUnits>(ss0 + ss1), 1.f / D, p.eps * scale * scale);
+            }
+          const float r = rsqrtf(m);
           const float mean = head_sum<kUnits>(dot0 + dot1) * r * (1.f / D);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -178,6 +191,10 @@ __global__ void __launch_bounds__(kNormBwdThreads, kNormBwdCtasPerSm) fa_norm_bw
               dw[j] = fmaf(g[j], n, dw[j]);
               g[j] = r * fmaf(-mean, n, g[j] * w4[e]);
             }
+          }
+          if constexpr (NORM == kNormAnySize) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) g[j] *= scale;
           }
           pack16(g, ga[i], ge[i]);
           *reinterpret_cast<uint4*>(dx + c0) = ga[i];

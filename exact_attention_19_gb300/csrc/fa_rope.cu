@@ -37,7 +37,7 @@ constexpr long long kCtasPerSm = 24;
 constexpr long long kLeastHeads = 4;
 constexpr long long kLeastCtasPerSm = 4;
 
-template <int D, bool PAGED, bool NORM>
+template <int D, bool PAGED, int NORM>
 int launch(fa::RopeParams& p, int interleaved, int sms, cudaStream_t stream) {
   constexpr int kTokens = fa::kRopeThreads / (D / 16);
   const long long tiles = (p.tokens + kTokens - 1) / kTokens;
@@ -57,13 +57,16 @@ int launch(fa::RopeParams& p, int interleaved, int sms, cudaStream_t stream) {
   return fa_host::launched(interleaved ? cudaLaunchKernelEx(&cfg, fa::fa_rope_kernel<D, true, PAGED, NORM>, p)
                                        : cudaLaunchKernelEx(&cfg, fa::fa_rope_kernel<D, false, PAGED, NORM>, p));
 }
+template <bool PAGED, int NORM>
+int launch(fa::RopeParams& p, int d, int interleaved, int sms, cudaStream_t stream) {
+  return d == 64 ? launch<64, PAGED, NORM>(p, interleaved, sms, stream)
+                 : launch<128, PAGED, NORM>(p, interleaved, sms, stream);
+}
 template <bool PAGED>
 int launch(fa::RopeParams& p, int d, bool norm, int interleaved, int sms, cudaStream_t stream) {
-  if (norm)
-    return d == 64 ? launch<64, PAGED, true>(p, interleaved, sms, stream)
-                   : launch<128, PAGED, true>(p, interleaved, sms, stream);
-  return d == 64 ? launch<64, PAGED, false>(p, interleaved, sms, stream)
-                 : launch<128, PAGED, false>(p, interleaved, sms, stream);
+  if (!norm) return launch<PAGED, fa::kNoNorm>(p, d, interleaved, sms, stream);
+  return p.eps < fa::kNormLeastEps ? launch<PAGED, fa::kNormAnySize>(p, d, interleaved, sms, stream)
+                                   : launch<PAGED, fa::kNorm>(p, d, interleaved, sms, stream);
 }
 
 bool misaligned(const void* p) { return reinterpret_cast<uintptr_t>(p) & 15u; }
@@ -221,7 +224,7 @@ int append_impl(const void* q, const void* k, const void* v, void* q_out, void* 
 // The CTAs of the norm's backward, and the sums they leave.
 int bwd_ctas(int sms) { return fa::kNormBwdCtasPerSm * sms; }
 
-template <int D>
+template <int D, int NORM>
 int launch_norm_bwd(fa::NormBwdParams& p, int interleaved, int sms, cudaStream_t stream) {
   constexpr int kTokens = fa::kNormBwdThreads / (D / 16);
   const long long tiles = (p.tokens + kTokens - 1) / kTokens;
@@ -241,10 +244,16 @@ int launch_norm_bwd(fa::NormBwdParams& p, int interleaved, int sms, cudaStream_t
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(fa::kNormBwdThreads);
   cfg.stream = stream;
-  const int st = fa_host::launched(interleaved ? cudaLaunchKernelEx(&cfg, fa::fa_norm_bwd_kernel<D, true>, p)
-                                               : cudaLaunchKernelEx(&cfg, fa::fa_norm_bwd_kernel<D, false>, p));
+  const int st = fa_host::launched(interleaved ? cudaLaunchKernelEx(&cfg, fa::fa_norm_bwd_kernel<D, true, NORM>, p)
+                                               : cudaLaunchKernelEx(&cfg, fa::fa_norm_bwd_kernel<D, false, NORM>, p));
   if (st != FA_OK || (!p.dweight[0] && !p.dweight[1])) return st;
   return fa_host::launch_kernel(fa::fa_norm_bwd_sum_kernel<D>, 2 * (D / 8), fa::kNormSumThreads, 0, stream, p);
+}
+
+template <int D>
+int launch_norm_bwd(fa::NormBwdParams& p, int interleaved, int sms, cudaStream_t stream) {
+  return p.eps < fa::kNormLeastEps ? launch_norm_bwd<D, fa::kNormAnySize>(p, interleaved, sms, stream)
+                                   : launch_norm_bwd<D, fa::kNorm>(p, interleaved, sms, stream);
 }
 
 }  // namespace

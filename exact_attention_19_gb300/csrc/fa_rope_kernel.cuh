@@ -205,16 +205,39 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
-// One head of one token: 1 / sqrt(mean x^2 + eps), the squares summed in fp32 (two sums a thread, then lanes).
+// The norm of a call: none; squares summed in fp32; or so for heads of any size.
+enum : int { kNoNorm = 0, kNorm = 1, kNormAnySize = 2 };
+// From 2^-96 on an eps covers every square that underflows; with less a head of small elements needs them.
+// Calls with less (and they alone: the test costs 4 x 8192 tokens 119 us for 108.6) multiply a head whose mean square
+// fp32 does not hold well by a power of two first, which the norm does not see where eps takes its square: below
+// 2^-96 elements are less than 2^-44, above what fp32 holds none passes 2^128.
+constexpr float kNormLeastEps = 0x1p-96f;
+__device__ __forceinline__ bool plain_mean(float m) { return m >= kNormLeastEps && m <= 3.402823466e38f; }
+__device__ __forceinline__ float head_scale(float m) { return m < kNormLeastEps ? 0x1p100f : 0x1p-70f; }
+
+// One head of one token: mean x^2 + eps, the squares summed in fp32 (two sums a thread, then lanes).
 template <int D>
-__device__ __forceinline__ float inverse_rms(const float (&x)[16], float eps) {
+__device__ __forceinline__ float mean_square(const float (&x)[16], float eps) {
   float a = 0.f, b = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     a = fmaf(x[i], x[i], a);
     b = fmaf(x[8 + i], x[8 + i], b);
   }
-  return rsqrtf(fmaf(head_sum<D / 16>(a + b), 1.f / D, eps));
+  return fmaf(head_sum<D / 16>(a + b), 1.f / D, eps);
+}
+// 1 / sqrt of it, and x scaled if it has to be.
+template <int D, int NORM>
+__device__ __forceinline__ float inverse_rms(float (&x)[16], float eps) {
+  float m = mean_square<D>(x, eps);
+  if constexpr (NORM == kNormAnySize)
+    if (!plain_mean(m)) {
+      const float scale = head_scale(m);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] *= scale;
+      m = mean_square<D>(x, eps * scale * scale);
+    }
+  return rsqrtf(m);
 }
 
 constexpr int kRopeThreads = 128;
@@ -226,7 +249,7 @@ constexpr int kRopeThreads = 128;
 // NORM: the 16 elements stay in fp32 from the load through norm, weight and
 // rotation to one rounding at the end (a rounding between norm and rotation, as
 // two calls have it, would be as large as the result's own).
-template <int D, bool INTERLEAVED, bool PAGED, bool NORM>
+template <int D, bool INTERLEAVED, bool PAGED, int NORM>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams p) {
   constexpr int kUnits = D / 16;  // threads per token
   // head range of this CTA over q, then k, then v
@@ -321,7 +344,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const RopeParams 
             if (t < 2) {
               float x[16];
               unpack16(a[i], e[i], x);
-              const float r = inverse_rms<D>(x, p.eps);
+              const float r = inverse_rms<D, NORM>(x, p.eps);
 #pragma unroll
               for (int j = 0; j < 16; ++j) x[j] *= r * weight[j];
               if (turns) rotate16<INTERLEAVED>(x, c, s);

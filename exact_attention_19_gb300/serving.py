@@ -265,7 +265,9 @@ def norm_rope(q, k, inv_freq=None, q_weight=None, k_weight=None, eps: float = 1e
 
     Each head x becomes x * weight / sqrt(mean(x^2) + eps) over its d elements and then turns as in ``rope``
     (``inv_freq`` None: no rotation).  ``q_weight``, ``k_weight``: [d], bf16 or fp32 alike, or None (ones).  One
-    rounding to bf16 at the end.  All other arguments as in ``rope``; ``norm_rope_bwd`` has the gradients.
+    rounding to bf16 at the end.  Elements are to be below 2^60, or eps below 2^-96 (any finite head, up to a tenth
+    slower; with eps 0 a head of zeros gives NaN).  All other arguments as in ``rope``; ``norm_rope_bwd`` has the
+    gradients.
     """
     return _rope(False, q, k, inv_freq, positions, offset, interleaved, mag, q_out, k_out, stream,
                  (q_weight, k_weight, eps))

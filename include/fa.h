@@ -284,7 +284,10 @@ int fa_kv_append(const void* q, const void* k, const void* v, void* q_out, void*
  * eps         finite, >= 0 (with 0 a head of zeros gives NaN).
  * rot         0 (norm alone; inv_freq may be NULL), or as in fa_rope.
  * Norm, weight and rotation in fp32 with one rounding to bf16 at the end; squares
- * are summed in fp32, so elements of 2^60 and more overflow the sum.
+ * are summed in fp32, so elements of 2^60 and more overflow the sum.  With eps below
+ * 2^-96 small heads are left to their own squares: then a head whose squares fp32
+ * does not hold is scaled by a power of two first, and finite ones of any size are
+ * normed (up to a tenth slower).
  * All else as fa_rope.
  */
 int fa_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const double* inv_freq, const void* q_weight,
