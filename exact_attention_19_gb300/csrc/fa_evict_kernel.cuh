@@ -342,9 +342,11 @@ __global__ void __launch_bounds__(THREADS, 1) fa_evict_select_kernel(const Evict
 // Few heads of many weights: p.split CTAs to a head, each with a part of its weights, and a
 // kernel to a digit and one for the list.  Bound: four kernels' chains of dependent reads and
 // barriers, about 4.5 us each.  (Parts in a cluster that read one another's counts from
-// shared memory would be one launch; a kernel of that kind faulted, and its cause was not found.)  A part's histogram goes to the workspace; the
-// next kernel's CTAs each add those of their head up, and note what of their own part
-// stays by the digit found, so that the last one knows where each part's list begins.
+// shared memory would be one launch; a kernel of that kind faulted and was taken out.  The
+// move took its list's slots unchecked then, so a list with places left out would explain it.)
+// A part's histogram goes to the workspace; the next kernel's CTAs each add those of their
+// head up, and note what of their own part stays by the digit found, so that the last one
+// knows where each part's list begins.
 constexpr int kSplitThreads = 512;
 constexpr int kMostParts = 16, kPartCtas = 152;  // parts of a head at most, of all heads about
 inline int select_parts(long long heads) {
@@ -509,7 +511,8 @@ __global__ void __launch_bounds__(kSplitThreads) fa_evict_list_kernel(const Evic
 // stores and nothing after them.  Into other pages no barrier is needed.
 // Bound: memory; a round in place waits for its loads (a cluster has its rows of the
 // next round looked up meanwhile), which shows where few rows are moved: 128 heads of up to
-// 8192 halved, K and V of 128, 74 us cold, 16 heads of up to 31999 to 8000 into other pages 32.
+// 8192 halved, K and V of 128, 74 us cold (the whole call 87 on caches that L2 does not hold, 38 to
+// 41 repeated on one), 16 heads of up to 31999 to 8000 into other pages 32.
 constexpr int kMoveThreads = 512;
 
 template <int D>

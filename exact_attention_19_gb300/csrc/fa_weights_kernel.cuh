@@ -5,8 +5,10 @@
 // group.  For every key j,
 //   W'[j] = decay W[j] + sum_r [row r sees j] exp(scale q_r . k_j - LSE_r),
 // with 0 for W[j] where j is a new token.  With the LSE known the sum of a key
-// needs nothing of the other keys: a key belongs to one warp, which meets all its
-// rows, so there are no parts to join, no atomics, and results repeat bit for bit.
+// needs nothing of the other keys.  On the warp-level kernel a key belongs to one warp,
+// which meets all its rows; on the tensor cores two groups of warps, and the CTAs of a
+// cluster, take row blocks in turn, and a writer joins their sums in a fixed order.
+// No atomics: results repeat bit for bit.
 #pragma once
 
 #include "fa_cache_ptx.cuh"
@@ -287,11 +289,13 @@ __global__ void __launch_bounds__(kWeightThreads, 3) fa_kv_weights_kernel(const 
 // 256 keys and one CTA to an SM: a row block, once loaded, waited for and described,
 // passes two tiles (2 x 2048 tokens over 8192, 32/8 heads of 128: 169 us, with 128 keys and
 // two CTAs 221; 147 us since a writer has a warp of its own, the units come described
-// and the MMAs are issued with constant indexes, 141 since long units are given out by
+// and the MMAs are issued with constant indexes, 142 since long units are given out by
 // what each cluster has to do).
 // Bound: the products (80 us at the measured tensor rate) and one exponential per key and
-// row, which take turns on two buffers: 0.85 us for a row block and 256 keys, 0.66 of it
-// the products at that rate; a unit's start and end, 4.5 us alone, hide behind eight blocks.
+// row, which take turns on two buffers.  By timestamps in that case (146 us with them) a CTA
+// needs 7 us to its first block (3.4 of them the search for its units), 0.77 us for a row
+// block and 256 keys (0.66 of it the products at that rate), 4.6 us for a unit beside its
+// blocks and 3 us after the last; the last CTA to end has 134 blocks in 7 units.
 // With many row blocks the CTAs of a cluster share a unit, so that it is small beside a
 // CTA's share and few keys still reach many SMs.
 // Rows that do not exist, hold no token or have lse = -inf, and keys that some row of the
