@@ -451,6 +451,7 @@ struct WTileUnits {
     uneven = p.uneven && long_units(p);
     cluster = static_cast<int>(blockIdx.x / cluster_size());
     clusters = static_cast<int>(gridDim.x / cluster_size());
+    mine = {};  // the description that there is no unit has no row blocks either, whoever walks over them
     b_from = 0;
     first = 0;
     if (!uneven) {

@@ -304,7 +304,7 @@ int fa_norm_rope(const void* q, const void* k, void* q_out, void* k_out, const d
  * dq, q, dq_out  bf16 [B, H, N, d];  dk, k, dk_out  bf16 [B, Hk, N, d], Hk = 0:
  *             no k.  q and k are the forward's inputs.  dq_out may be dq or q (same
  *             pointer, same strides), dk_out likewise; no other overlap.
- * dq_weight, dk_weight  fp32 [d], written (not added to); NULL: not wanted.
+ * dq_weight, dk_weight  fp32 [d], 16-byte aligned, written (not added to); NULL: not wanted.
  * strides     host array of 18: batch, head and row strides of dq, dk, q, k, dq_out,
  *             dk_out, or NULL: all contiguous.
  * workspace   fa_norm_bwd_workspace_bytes(d) bytes, 16-byte aligned (NULL where

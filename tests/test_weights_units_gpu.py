@@ -57,23 +57,24 @@ def definition(q, lse, k, old, n, m, left, decay):
     return kept + total, err + (q.shape[0] * m + 8) * 2.0 ** -24 * (total + kept.abs())
 
 
-@pytest.mark.parametrize("decay", [0.5, 0.0, 1.0])
-@pytest.mark.parametrize("B,H,Hk,T,d,page,lens,new,left", roles.CASES)
-def test_units_that_no_row_sees(fa, B, H, Hk, T, d, page, lens, new, left, decay):
-    c = Cache(B + T, lens, Hk, d, page)
+def check(fa, c, B, H, Hk, T, lens, new, left, decay, table):
+    """One call against the definition; `table` is the cache's, or wider."""
     fresh = [T] * B if new is None else new
-    q, window = rand(T, B, H, T, d), (left, 0)
+    q, window = rand(T, B, H, T, c.d), (left, 0)
     kw = dict(new_lens=None if new is None else i32(new), window=window)
-    table, n_dev = c.device_table(), i32(lens)
+    n_dev, page = i32(lens), c.page
     _, lse = fa.fwd_paged(q, c.k, c.v, table, n_dev, **kw)
     for b in range(B):
-        c.forget(b, 0 if decay == 0 else lens[b] - fresh[b], lens[b])
+        if lens[b] > 0:
+            c.forget(b, 0 if decay == 0 and fresh[b] else lens[b] - fresh[b], lens[b])
     before = c.w.clone()
     fa.kv_weights(q, lse, c.k, c.w, table, n_dev, decay=decay, **kw)
     torch.cuda.synchronize()
     assert fa.fa_fwd_status(None) == (0, 0)
     written = torch.zeros(c.w.shape, dtype=torch.bool, device="cuda")
     for b, (n, m) in enumerate(zip(lens, fresh)):
+        if n <= 0 or m == 0:
+            continue
         j = np.arange(n)
         pages, slots = torch.from_numpy(c.table[b][j // page]).long().cuda(), torch.from_numpy(j % page).cuda()
         for h in range(Hk):
@@ -84,3 +85,24 @@ def test_units_that_no_row_sees(fa, B, H, Hk, T, d, page, lens, new, left, decay
             assert bool((err <= tol).all()), f"sequence {b}, head {h}: off by {float(err.max()):.3e}"
             written[at] = True
     assert torch.equal(bits(c.w)[~written], bits(before)[~written])
+
+
+@pytest.mark.parametrize("decay", [0.5, 0.0, 1.0])
+@pytest.mark.parametrize("B,H,Hk,T,d,page,lens,new,left", roles.CASES)
+def test_units_that_no_row_sees(fa, B, H, Hk, T, d, page, lens, new, left, decay):
+    c = Cache(B + T, lens, Hk, d, page)
+    check(fa, c, B, H, Hk, T, lens, new, left, decay, c.device_table())
+
+
+@pytest.mark.parametrize("B,H,Hk,T,d,lens,new", [
+    (4, 8, 4, 70, 64, [300, 0, -1, 5], [70, 0, 70, 5]),
+    (3, 12, 2, 1300, 128, [0, 1300, 40], [0, 1300, 3]),  # by cost, or with as many CTAs to a unit as there are SMs for
+    (2, 5, 5, 200, 128, [0, -2], [200, 0]),              # no unit at all
+])
+@pytest.mark.parametrize("width", [30, 900])
+def test_clusters_without_a_unit(fa, B, H, Hk, T, d, lens, new, width):
+    """A table for far longer sequences: most clusters of the launch find nothing to do."""
+    c = Cache(B + T, lens, Hk, d, 64)
+    table = np.full((B, width), -9, np.int32)
+    table[:, :c.table.shape[1]] = c.table
+    check(fa, c, B, H, Hk, T, lens, new, -1, 0.5, torch.from_numpy(table).cuda())
